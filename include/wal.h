@@ -529,6 +529,164 @@ int wal_graph_create(uint32_t n, const wal_grouped_info* ginfos, const void* con
 int wal_graph_launch(const wal_graph* graph, void* stream);
 int wal_graph_destroy(wal_graph* graph);
 
+/* ---------------------------------------------------------------------------
+ * Attention between the q | k | v products and the o product: rotary
+ * positions, a paged key/value cache, attention over the cache and over
+ * whole prompts.  (The pages list attention and its cache only as parts of
+ * their runtimes; the formulas below are the usual ones.)  In the masks and
+ * sums below `head` is a query head h, and its key/value head is
+ * h / (q_heads / kv_heads): query heads share key/value heads in groups.
+ *
+ * Rotary positions.  Pair i of a head (0 <= i < rot_dim / 2) at position p
+ * turns by the angle p f_i and is multiplied by the magnitude m:
+ *     (a, b) -> m (a cos p f_i - b sin p f_i, b cos p f_i + a sin p f_i)
+ * with (a, b) = elements (i, i + rot_dim / 2) (WAL_ROPE_HALF) or (2 i, 2 i + 1)
+ * (WAL_ROPE_INTERLEAVED); elements from rot_dim on are copied unchanged.
+ * Frequencies are held in turns: t_i = round(2^64 f_i / 2 pi), so that the
+ * low 64 bits of p t_i are the fraction of a turn, exact at any position.
+ * The table is plain data: wal_rope_freqs makes the usual ones, a model with
+ * other frequencies brings its own.
+ *
+ * wal_rope_freqs (host): f_i = base^(-2 i / rot_dim), and
+ *   WAL_ROPE_PLAIN   as it is
+ *   WAL_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   WAL_ROPE_NTK     base replaced by base factor^(rot_dim / (rot_dim - 2))
+ *   WAL_ROPE_PARTS   by parts (Peng et al. 2023, "YaRN: Efficient Context
+ *                    Window Extension of Large Language Models"): with
+ *                    r_i = trained_len f_i / 2 pi turns over the trained
+ *                    length and g_i = clamp((r_i - turns_low) / (turns_high -
+ *                    turns_low), 0, 1): f_i (g_i + (1 - g_i) / factor), and
+ *                    the magnitude 0.1 ln(factor) + 1 (else it is 1)
+ * turns [rot_dim / 2]; magnitude may be NULL.
+ * Errors: ARG (NULL, unknown scaling, base <= 1, factor < 1, PARTS without
+ * trained_len or turns_high > turns_low >= 0), SHAPE (rot_dim). */
+enum { WAL_ROPE_HALF = 0, WAL_ROPE_INTERLEAVED = 1 };
+enum { WAL_ROPE_PLAIN = 0, WAL_ROPE_LINEAR = 1, WAL_ROPE_NTK = 2, WAL_ROPE_PARTS = 3 };
+typedef struct {
+  uint32_t rot_dim;             /* rotated elements of a head: a multiple of 16, 16..512 */
+  uint32_t scaling;             /* WAL_ROPE_PLAIN ..                                     */
+  double base, factor;          /* factor is not read by WAL_ROPE_PLAIN                  */
+  double trained_len, turns_low, turns_high; /* WAL_ROPE_PARTS only                      */
+} wal_rope_desc;
+int wal_rope_freqs(const wal_rope_desc* d, uint64_t* turns, float* magnitude);
+
+/* What a call that rotates reads: the frequency table and the positions
+ * (any int32) in device memory. */
+typedef struct {
+  const uint64_t* turns_dev;    /* [rot_dim / 2], 8-byte aligned                         */
+  const int32_t* pos_dev;       /* [n] position of each token                            */
+  uint32_t rot_dim;             /* a multiple of 16, at most head_dim                    */
+  uint32_t layout;              /* WAL_ROPE_HALF or WAL_ROPE_INTERLEAVED                 */
+  float magnitude;
+} wal_rotary;
+
+/* wal_rope: out[t][h] = x[t][h] rotated at position pos[t], for n tokens of
+ * `heads` heads of head_dim elements (a multiple of 16, at most 512).
+ *   x_dev    [n][ldx] fp32 or bf16, heads side by side; out_dev [n][ldo]
+ *            fp32 or bf16; 16-byte aligned rows.  out may be x itself (same
+ *            type and pitch); any other overlap is rejected.
+ * Angles, sines and products are fp32 (the angle's reduction is exact), bf16
+ * output rounds to nearest even.  n = 0 does nothing.
+ * Errors: ARG, SHAPE, ALIGN, DEVICE. */
+int wal_rope(const void* x_dev, int x_dtype, uint32_t n, uint32_t heads, uint32_t head_dim, uint32_t ldx,
+             const wal_rotary* r, void* out_dev, int out_dtype, uint32_t ldo, void* stream);
+
+/* The paged cache of one layer: n_pages pages of page_size tokens, one device
+ * buffer of total_bytes (256-byte aligned) with the planes
+ *   K, V    [n_pages][kv_heads][page_size][head_dim] bf16 or int8 codes
+ *   KS, VS  [n_pages][kv_heads][page_size] fp32 scales (WAL_KV_INT8 only)
+ * at multiples of 256 bytes in that order.  Token slot s is place
+ * s % page_size of page s / page_size.  WAL_KV_INT8 holds a row (one token of
+ * one head) as codes c_j in [-127, 127] and one scale s: values s c_j, with
+ *     s = a * fp32(1/127),  c_j = round-to-nearest-even(x_j * (127 / a)),
+ * a = max |x_j|, all in fp32.  A row with a < 2^-100 is held as zeros, and a row
+ * with an infinity or a NaN as a NaN scale: it reads back as NaN, it does not
+ * pass for numbers.  WAL_KV_BF16 rounds to nearest even and keeps
+ * infinities and NaN.
+ * wal_kv_size fills the plane offsets of a descriptor.
+ * Errors: ARG, SHAPE (sizes; n_pages * page_size above 2^31). */
+enum { WAL_KV_BF16 = 0, WAL_KV_INT8 = 1 };
+typedef struct {
+  uint32_t n_pages;
+  uint32_t page_size;           /* tokens: 16, 32, 64, 128 or 256                        */
+  uint32_t kv_heads;            /* 1..256                                                */
+  uint32_t head_dim;            /* 64, 128 or 256                                        */
+  uint32_t fmt;                 /* WAL_KV_BF16 or WAL_KV_INT8                            */
+} wal_kv_desc;
+typedef struct {
+  wal_kv_desc d;
+  uint64_t total_bytes, off_k, off_v, off_ks, off_vs;
+} wal_kv_info;
+int wal_kv_size(const wal_kv_desc* d, wal_kv_info* info);
+
+/* wal_kv_write: token t's keys and values go to slot slots[t] of the cache, the
+ * keys rotated first when r is given, and, when q is given too, q_out[t] = q[t]
+ * rotated (in one launch: what a decode step needs between the products and
+ * wal_attn_paged).
+ *   slots_dev  [n] int32, distinct; a slot outside the cache drops its token
+ *              (q_out is written all the same)
+ *   k, v       [n][ldk], [n][ldv], kv_heads heads side by side, fp32 or bf16
+ *              (kv_dtype; q has the same type); 16-byte aligned rows
+ *   r          NULL: nothing is rotated (q must be NULL then)
+ *   q, q_out   [n][ldq], q_heads heads, and [n][ldqo] bf16, 16-byte aligned
+ *              rows; NULL, NULL: no query.  q_out may be q itself when that is
+ *              bf16 with the same pitch
+ * The rotated keys are not rounded before they are quantised.
+ * Errors: ARG, SHAPE, ALIGN, DEVICE. */
+int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n, const void* k_dev,
+                 uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype, const wal_rotary* r,
+                 const void* q_dev, uint32_t q_heads, uint32_t ldq, void* q_out_dev, uint32_t ldqo, void* stream);
+
+/* wal_kv_read: the rows of slots[0..n) as numbers, k_out [n][ldk] and v_out
+ * [n][ldv] in fp32 or bf16 (out_dtype; nearest even), 16-byte aligned rows;
+ * either may be NULL.  A slot outside the cache reads as zeros.
+ * Errors: ARG, SHAPE, ALIGN, DEVICE. */
+int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const int32_t* slots_dev, uint32_t n, void* k_out_dev,
+                uint32_t ldk, void* v_out_dev, uint32_t ldv, int out_dtype, void* stream);
+
+/* wal_attn_paged: attention of the newest tokens of n_seqs sequences over the
+ * cache that holds all their tokens, the new ones among them.  Sequence s has
+ * lens[s] tokens in the cache and new_s = starts[s + 1] - starts[s] query rows,
+ * rows starts[s] .. of q; row i of them is its token lens[s] - new_s + i, and
+ *     out[row][h] = sum_j w_j v_j,  w = softmax_j(scale * q[row][h] . k_j)
+ * over its tokens j <= lens[s] - new_s + i.  A row that sees no token is
+ * zeros.  One token per sequence (decode), a few, and chunks of a prompt
+ * may be mixed in one call.
+ *   tables_dev  [n_seqs][ldt] int32: page of each page_size tokens of a
+ *               sequence; tokens of a page outside the cache are left out
+ *   lens_dev    [n_seqs] int32, starts_dev [n_seqs + 1] int32 rising from 0 to n
+ *   max_new, max_len  bounds of new_s and lens[s] (known to the caller, who
+ *               holds the pages; rows and tokens past them are not
+ *               computed); ldt * page_size >= max_len
+ *   q_dev       [n][ldq] bf16, q_heads (a multiple of kv_heads, at most
+ *               64 kv_heads) heads side by side; out_dev [n][ldo] bf16;
+ *               16-byte aligned rows; out must not overlap the inputs
+ *   scale       finite
+ *   ws          wal_attn_paged_workspace_size bytes, 256-byte aligned (NULL when that is 0); its
+ *               contents need not be kept, nor cleared before a call
+ * Products q . k and w v run on the matrix cores with bf16 operands (int8
+ * codes are exact in bf16; w is rounded to bf16 after its exponential, times
+ * the row's scale for an int8 cache) and fp32 sums; maxima, sums and partial
+ * results are fp32.  The result does not depend on timing.
+ * Errors: ARG, SHAPE, ALIGN, BUFFER, DEVICE. */
+int wal_attn_paged_workspace_size(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n,
+                                  uint32_t max_new, uint32_t max_len, size_t* bytes);
+int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const int32_t* tables_dev, uint32_t ldt,
+                   const int32_t* lens_dev, const int32_t* starts_dev, uint32_t n_seqs, uint32_t n,
+                   uint32_t max_new, uint32_t max_len, const void* q_dev, uint32_t q_heads, uint32_t ldq,
+                   float scale, void* out_dev, uint32_t ldo, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* wal_attn_prompt: the same over whole prompts, packed one after another:
+ * sequence s is rows starts[s] .. starts[s + 1] of q, k and v (all bf16, 16-byte
+ * aligned rows of ldq, ldk, ldv elements, heads side by side; views of one
+ * fused buffer are fine), each row sees its own sequence's rows up to itself
+ * (causal) or all of them.  max_len bounds the sequences' lengths.
+ * Errors: ARG, SHAPE, ALIGN, DEVICE. */
+int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk, const void* v_dev,
+                    uint32_t ldv, const int32_t* starts_dev, uint32_t n_seqs, uint32_t n, uint32_t max_len,
+                    uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim, float scale, int causal,
+                    void* out_dev, uint32_t ldo, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,9 @@ WAL_SYNC_BYTES = 4352
 WAL_MAX_ROW_BLOCKS = 4096
 WAL_WS_ZERO_BYTES = WAL_SYNC_BYTES + 4 * WAL_MAX_ROW_BLOCKS
 WAL_SYNC_FALLBACK_WORD = 0
+WAL_ROPE_HALF, WAL_ROPE_INTERLEAVED = 0, 1
+WAL_ROPE_PLAIN, WAL_ROPE_LINEAR, WAL_ROPE_NTK, WAL_ROPE_PARTS = 0, 1, 2, 3
+WAL_KV_BF16, WAL_KV_INT8 = 0, 1
 
 STATUS = {0: "WAL_OK", -1: "WAL_ERR_ARG", -2: "WAL_ERR_SHAPE", -3: "WAL_ERR_CODE",
           -4: "WAL_ERR_INEXACT", -5: "WAL_ERR_BUFFER", -6: "WAL_ERR_ALIGN", -7: "WAL_ERR_FORMAT",
@@ -71,6 +74,27 @@ class wal_grouped_info(ctypes.Structure):
                 ("class_segs", ctypes.c_uint64 * WAL_MAX_CLASSES), ("sync_dev", ctypes.c_void_p)]
 
 
+class wal_rope_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_uint32), ("scaling", ctypes.c_uint32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("trained_len", ctypes.c_double), ("turns_low", ctypes.c_double),
+                ("turns_high", ctypes.c_double)]
+
+
+class wal_rotary(ctypes.Structure):
+    _fields_ = [("turns_dev", ctypes.c_void_p), ("pos_dev", ctypes.c_void_p), ("rot_dim", ctypes.c_uint32),
+                ("layout", ctypes.c_uint32), ("magnitude", ctypes.c_float)]
+
+
+class wal_kv_desc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_uint32), ("page_size", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("fmt", ctypes.c_uint32)]
+
+
+class wal_kv_info(ctypes.Structure):
+    _fields_ = [("d", wal_kv_desc), ("total_bytes", ctypes.c_uint64), ("off_k", ctypes.c_uint64),
+                ("off_v", ctypes.c_uint64), ("off_ks", ctypes.c_uint64), ("off_vs", ctypes.c_uint64)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libwal.so is not built ({LIB_PATH}); run python ternary_hybrid_bit_amd/build.py")
 _lib = ctypes.CDLL(LIB_PATH)
@@ -79,6 +103,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _U32 = ctypes.c_uint32
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 _sig = {
     "wal_status_str": (ctypes.c_char_p, [_I]),
     "wal_packed_size": (_I, [ctypes.POINTER(wal_desc), ctypes.POINTER(wal_info)]),
@@ -116,6 +141,18 @@ _sig = {
     "wal_graph_create": (_I, [_U32, _P, _P, ctypes.POINTER(_P)]),
     "wal_graph_launch": (_I, [_P, _P]),
     "wal_graph_destroy": (_I, [_P]),
+    "wal_rope_freqs": (_I, [ctypes.POINTER(wal_rope_desc), _P, ctypes.POINTER(_F)]),
+    "wal_rope": (_I, [_P, _I, _U32, _U32, _U32, _U32, ctypes.POINTER(wal_rotary), _P, _I, _U32, _P]),
+    "wal_kv_size": (_I, [ctypes.POINTER(wal_kv_desc), ctypes.POINTER(wal_kv_info)]),
+    "wal_kv_write": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _U32, _P, _U32, _I,
+                          ctypes.POINTER(wal_rotary), _P, _U32, _U32, _P, _U32, _P]),
+    "wal_kv_read": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _U32, _P, _U32, _I, _P]),
+    "wal_attn_paged_workspace_size": (_I, [ctypes.POINTER(wal_kv_desc), _U32, _U32, _U32, _U32, _U32,
+                                           ctypes.POINTER(_SZ)]),
+    "wal_attn_paged": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _P, _U32, _U32, _U32, _U32, _P, _U32, _U32,
+                            _F, _P, _U32, _P, _SZ, _P]),
+    "wal_attn_prompt": (_I, [_P, _U32, _P, _U32, _P, _U32, _P, _U32, _U32, _U32, _U32, _U32, _U32, _F, _I, _P, _U32,
+                             _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -635,3 +672,197 @@ def wal_embed_rows_mixed(W3, V3: int, W4, V4: int, inp: int, row_map, ids, out, 
            "wal_embed_rows_mixed")
     return out
 
+
+
+# ---------------------------------------------------------------------------
+# Attention: rotary positions, the paged key/value cache, attention over the
+# cache and over packed prompts.
+
+def make_rope_desc(rot_dim: int, base: float = 10000.0, scaling: int = WAL_ROPE_PLAIN, factor: float = 1.0,
+                   trained_len: float = 0.0, turns_low: float = 1.0, turns_high: float = 32.0) -> wal_rope_desc:
+    return wal_rope_desc(rot_dim, scaling, base, factor, trained_len, turns_low, turns_high)
+
+
+def wal_rope_freqs(desc: wal_rope_desc):
+    """(turns, magnitude): the frequency table as int64 numpy [rot_dim / 2] (2^-64
+    turns a position; copy it to the GPU) and the factor on rotated values."""
+    turns = np.zeros(max(int(desc.rot_dim) // 2, 1), dtype=np.int64)
+    m = ctypes.c_float()
+    _check(_lib.wal_rope_freqs(ctypes.byref(desc), turns.ctypes.data, ctypes.byref(m)), "wal_rope_freqs")
+    return turns, m.value
+
+
+def _vec(t, name: str, dtype, n: int):
+    """A contiguous 1-D device vector of at least n elements; an empty one counts too."""
+    _dev(t, name, (dtype,), n)
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be 1-D")
+    return t
+
+
+def _ld(t) -> int:
+    """Row pitch of a 2-D tensor (of its only row: its width)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _rotary(pos, turns, n: int, layout: int, magnitude: float) -> wal_rotary:
+    torch = _torch()
+    _vec(pos, "pos", torch.int32, n)
+    _vec(turns, "turns", torch.int64, 1)
+    return wal_rotary(_ptr(turns), _ptr(pos), 2 * turns.numel(), layout, magnitude)
+
+
+def _heads(t, name: str, head_dim: int) -> int:
+    if head_dim < 1 or t.shape[1] % head_dim or not t.shape[1]:
+        raise ValueError(f"{name} has {t.shape[1]} columns, not a multiple of head_dim {head_dim}")
+    return t.shape[1] // head_dim
+
+
+def wal_rope(X, out, pos, turns, head_dim: int, layout=WAL_ROPE_HALF, magnitude: float = 1.0, stream=None):
+    """out = X [n][heads * head_dim] with every head rotated at its row's
+    position; pos int32 [n], turns int64 [rot_dim / 2] (wal_rope_freqs); bf16
+    or fp32 device tensors, out may be X itself."""
+    torch = _torch()
+    acts = (torch.bfloat16, torch.float32)
+    _rows(X, "X", acts, head_dim)
+    heads = _heads(X, "X", head_dim)
+    _rows(out, "out", acts, X.shape[1], X.shape[0])
+    r = _rotary(pos, turns, X.shape[0], layout, magnitude)
+    _gpu(X=X, out=out, pos=pos, turns=turns)
+    if not X.shape[0]:   # an empty tensor has no address: nothing to do
+        return out
+    _check(_lib.wal_rope(_ptr(X), _xdtype(X), X.shape[0], heads, head_dim, _ld(X), ctypes.byref(r), _ptr(out),
+                         _xdtype(out), _ld(out), _stream(stream)), "wal_rope")
+    return out
+
+
+def make_kv_desc(n_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int = WAL_KV_BF16) -> wal_kv_desc:
+    return wal_kv_desc(n_pages, page_size, kv_heads, head_dim, fmt)
+
+
+def wal_kv_size(desc: wal_kv_desc) -> wal_kv_info:
+    """Plane offsets and total_bytes of a cache (allocate that many device bytes, contents arbitrary)."""
+    info = wal_kv_info()
+    _check(_lib.wal_kv_size(ctypes.byref(desc), ctypes.byref(info)), "wal_kv_size")
+    return info
+
+
+def _kv_cache(desc: wal_kv_desc, cache):
+    _dev_bytes(cache, "cache", int(wal_kv_size(desc).total_bytes))
+    return desc.kv_heads * desc.head_dim
+
+
+def wal_kv_write(desc: wal_kv_desc, cache, slots, K, V, pos=None, turns=None, layout=WAL_ROPE_HALF,
+                 magnitude: float = 1.0, Q=None, Q_out=None, stream=None):
+    """Writes K, V [n][kv_heads * head_dim] (bf16 or fp32) to the cache's slots
+    [n] (int32).  With pos and turns the keys are rotated first, and Q, when
+    given, is rotated into Q_out (bf16)."""
+    torch = _torch()
+    acts = (torch.bfloat16, torch.float32)
+    width = _kv_cache(desc, cache)
+    _rows(K, "K", acts, width)
+    n = K.shape[0]
+    _rows(V, "V", (K.dtype,), width, n)
+    _vec(slots, "slots", torch.int32, n)
+    if (pos is None) != (turns is None):
+        raise ValueError("pos and turns go together")
+    if (Q is None) != (Q_out is None) or (Q is not None and pos is None):
+        raise ValueError("Q needs Q_out, pos and turns")
+    r = None if pos is None else _rotary(pos, turns, n, layout, magnitude)
+    q_heads = ldq = ldqo = 0
+    if Q is not None:
+        _rows(Q, "Q", (K.dtype,), desc.head_dim, n)
+        q_heads = _heads(Q, "Q", desc.head_dim)
+        _rows(Q_out, "Q_out", (torch.bfloat16,), Q.shape[1], n)
+        ldq, ldqo = _ld(Q), _ld(Q_out)
+    _gpu(cache=cache, slots=slots, K=K, V=V, pos=pos, turns=turns, Q=Q, Q_out=Q_out)
+    if not n:
+        return
+    _check(_lib.wal_kv_write(ctypes.byref(desc), _ptr(cache), _ptr(slots), n, _ptr(K), _ld(K), _ptr(V), _ld(V),
+                             _xdtype(K), None if r is None else ctypes.byref(r), _ptr(Q), q_heads, ldq, _ptr(Q_out),
+                             ldqo, _stream(stream)), "wal_kv_write")
+
+
+def wal_kv_read(desc: wal_kv_desc, cache, slots, K=None, V=None, stream=None):
+    """Reads the cache's slots [n] into K, V [n][kv_heads * head_dim] (bf16 or
+    fp32; either may be None); returns (K, V)."""
+    torch = _torch()
+    width = _kv_cache(desc, cache)
+    if K is None and V is None:
+        raise ValueError("K or V must be given")
+    _vec(slots, "slots", torch.int32, 0)
+    n = slots.numel()
+    first = K if K is not None else V
+    for t, name in ((K, "K"), (V, "V")):
+        if t is not None:
+            _rows(t, name, (torch.bfloat16, torch.float32) if t is first else (first.dtype,), width, n)
+    _gpu(cache=cache, slots=slots, K=K, V=V)
+    if not n:
+        return K, V
+    _check(_lib.wal_kv_read(ctypes.byref(desc), _ptr(cache), _ptr(slots), n, _ptr(K), 0 if K is None else _ld(K),
+                            _ptr(V), 0 if V is None else _ld(V), _xdtype(first), _stream(stream)), "wal_kv_read")
+    return K, V
+
+
+def wal_attn_paged_workspace_size(desc: wal_kv_desc, q_heads: int, n_seqs: int, n: int, max_new: int,
+                                  max_len: int) -> int:
+    b = _SZ()
+    _check(_lib.wal_attn_paged_workspace_size(ctypes.byref(desc), q_heads, n_seqs, n, max_new, max_len,
+                                              ctypes.byref(b)), "wal_attn_paged_workspace_size")
+    return b.value
+
+
+def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=None, scale: Optional[float] = None,
+                   max_new: int = 1, max_len: int = 0, stream=None):
+    """out = attention of Q's rows over the paged cache: tables int32
+    [n_seqs][pages], lens int32 [n_seqs], starts int32 [n_seqs + 1], Q and out
+    bf16 [n][q_heads * head_dim], ws of wal_attn_paged_workspace_size bytes.
+    scale: 1 / sqrt(head_dim) unless given; max_new and max_len bound the
+    sequences' new tokens and lengths (max_len 0: what the tables hold)."""
+    torch = _torch()
+    _kv_cache(desc, cache)
+    _rows(tables, "tables", (torch.int32,), 1)
+    n_seqs = tables.shape[0]
+    _vec(lens, "lens", torch.int32, n_seqs)
+    _vec(starts, "starts", torch.int32, n_seqs + 1)
+    _rows(Q, "Q", (torch.bfloat16,), desc.head_dim)
+    n, q_heads = Q.shape[0], _heads(Q, "Q", desc.head_dim)
+    _rows(out, "out", (torch.bfloat16,), Q.shape[1], n)
+    max_len = max_len or tables.shape[1] * desc.page_size
+    if max_new < 0 or max_len < 0 or max_len > tables.shape[1] * desc.page_size:
+        raise ValueError(f"max_new {max_new}, max_len {max_len}: the tables hold {tables.shape[1] * desc.page_size}")
+    wsb = _ws_bytes(ws)
+    _gpu(cache=cache, tables=tables, lens=lens, starts=starts, Q=Q, out=out, ws=ws)
+    if not n or not n_seqs:
+        return out
+    _check(_lib.wal_attn_paged(ctypes.byref(desc), _ptr(cache), _ptr(tables), _ld(tables), _ptr(lens), _ptr(starts),
+                               n_seqs, n, max_new, max_len, _ptr(Q), q_heads, _ld(Q),
+                               desc.head_dim ** -0.5 if scale is None else scale, _ptr(out), _ld(out), _ptr(ws), wsb,
+                               _stream(stream)), "wal_attn_paged")
+    return out
+
+
+def wal_attn_prompt(Q, K, V, starts, out, head_dim: int, max_len: int, scale: Optional[float] = None,
+                    causal: bool = True, stream=None):
+    """out = attention over packed prompts: Q, out bf16 [n][q_heads * head_dim],
+    K, V bf16 [n][kv_heads * head_dim], starts int32 [n_seqs + 1]; max_len
+    bounds the sequences' lengths; scale as for wal_attn_paged."""
+    torch = _torch()
+    bf = (torch.bfloat16,)
+    _rows(Q, "Q", bf, head_dim)
+    n, q_heads = Q.shape[0], _heads(Q, "Q", head_dim)
+    _rows(K, "K", bf, head_dim, n)
+    kv_heads = _heads(K, "K", head_dim)
+    _rows(V, "V", bf, K.shape[1], n)
+    _rows(out, "out", bf, Q.shape[1], n)
+    _vec(starts, "starts", torch.int32, 1)
+    if max_len < 0:
+        raise ValueError(f"max_len {max_len}")
+    _gpu(Q=Q, K=K, V=V, starts=starts, out=out)
+    if not n:
+        return out
+    _check(_lib.wal_attn_prompt(_ptr(Q), _ld(Q), _ptr(K), _ld(K), _ptr(V), _ld(V), _ptr(starts), starts.numel() - 1,
+                                n, max_len, q_heads, kv_heads, head_dim,
+                                head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, _ptr(out), _ld(out),
+                                _stream(stream)), "wal_attn_prompt")
+    return out

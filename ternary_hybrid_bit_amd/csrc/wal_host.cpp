@@ -444,6 +444,51 @@ int wal_workspace_size(const wal_info* info, uint32_t batch, size_t* bytes) {
   return WAL_OK;
 }
 
+int wal_rope_freqs(const wal_rope_desc* d, uint64_t* turns, float* magnitude) {
+  if (!d || !turns) return WAL_ERR_ARG;
+  if (!d->rot_dim || d->rot_dim % 16 || d->rot_dim > 512) return WAL_ERR_SHAPE;
+  if (d->scaling > WAL_ROPE_PARTS || !(d->base > 1.0) || !std::isfinite(d->base)) return WAL_ERR_ARG;
+  const double factor = d->scaling == WAL_ROPE_PLAIN ? 1.0 : d->factor;
+  if (!(factor >= 1.0) || !std::isfinite(factor)) return WAL_ERR_ARG;
+  if (d->scaling == WAL_ROPE_PARTS &&
+      !(d->trained_len > 0 && d->turns_low >= 0 && d->turns_high > d->turns_low && std::isfinite(d->trained_len) &&
+        std::isfinite(d->turns_high)))
+    return WAL_ERR_ARG;
+  const double two_pi = 6.283185307179586476925, r = d->rot_dim;
+  const double base = d->scaling == WAL_ROPE_NTK ? d->base * std::pow(factor, r / (r - 2)) : d->base;
+  for (uint32_t i = 0; i < d->rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / r);   // at most 1 radian: under 2^62 in units of 2^-64 turns
+    if (d->scaling == WAL_ROPE_LINEAR) f /= factor;
+    if (d->scaling == WAL_ROPE_PARTS) {
+      double g = (d->trained_len * f / two_pi - d->turns_low) / (d->turns_high - d->turns_low);
+      g = g < 0 ? 0 : g > 1 ? 1 : g;
+      f *= g + (1 - g) / factor;
+    }
+    turns[i] = (uint64_t)std::llround(std::ldexp(f / two_pi, 64));
+  }
+  if (magnitude) *magnitude = d->scaling == WAL_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return WAL_OK;
+}
+
+int wal_kv_size(const wal_kv_desc* d, wal_kv_info* info) {
+  if (!d || !info || d->fmt > WAL_KV_INT8) return WAL_ERR_ARG;
+  if (!d->n_pages || !d->kv_heads || d->kv_heads > 256) return WAL_ERR_SHAPE;
+  if (d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1))) return WAL_ERR_SHAPE;
+  if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return WAL_ERR_SHAPE;
+  if ((uint64_t)d->n_pages * d->page_size > (1ull << 31)) return WAL_ERR_SHAPE;
+  const uint64_t rows = (uint64_t)d->n_pages * d->page_size * d->kv_heads;
+  const uint64_t plane = rows * d->head_dim * (d->fmt == WAL_KV_BF16 ? 2 : 1), scales = 4 * rows;
+  info->d = *d;
+  info->off_k = 0;
+  info->off_v = up(plane, kAlign);
+  info->off_ks = info->off_vs = info->total_bytes = 2 * up(plane, kAlign);
+  if (d->fmt == WAL_KV_INT8) {
+    info->off_vs = info->off_ks + up(scales, kAlign);
+    info->total_bytes = info->off_vs + up(scales, kAlign);
+  }
+  return WAL_OK;
+}
+
 int wal_int4_size(uint32_t V, uint32_t in, size_t* bytes) {
   if (!bytes || !V || !in) return WAL_ERR_ARG;
   if (in % 128 || (uint64_t)V * in > kMaxQElems) return WAL_ERR_SHAPE;
