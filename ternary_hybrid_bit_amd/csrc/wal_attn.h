@@ -1,0 +1,104 @@
+// What the attention kernels share (gfx950): their arguments, the cutting of a
+// call into sequences and rows, fragments of the matrix instructions.
+#pragma once
+
+#include "wal_args.h"
+#include "wal_device.h"
+
+namespace wal {
+
+enum { kPacked = 0, kPagedBf16 = 1, kPagedInt8 = 2 };
+
+struct Attn {
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* starts;
+  uint64_t ldq, ldo;
+  uint32_t n_seqs, n, q_heads, kv_heads, group;
+  float scale;                   // of the scores, times log2(e): weights are powers of two
+  uint32_t causal, max_new, max_len;
+  // paged
+  const uint8_t* cache;
+  const int32_t* tables;
+  const int32_t* lens;
+  uint64_t off_v, off_ks, off_vs;
+  uint32_t ldt, n_pages, page_shift;
+  // packed rows
+  const uint16_t* k;
+  const uint16_t* v;
+  uint64_t ldk, ldv;
+  // keys of one workgroup when the context is split, and the partial results
+  uint32_t split, n_splits, part_rows;
+  float* part;                   // [sequence][split][kv head][part_rows][dim] sums of w v
+  float2* part_ml;               // [sequence][split][kv head][part_rows] maximum, sum of w
+};
+
+constexpr uint32_t kMaxSplit = 4096;   // keys of a workgroup of attn_stream: its pages' addresses fit in 2 KB of LDS
+// Query rows of a key/value head that attn_stream takes: two tiles of 16, one where two would not fit in registers.
+constexpr uint32_t stream_rows(uint32_t dim) { return dim == 256 ? 16 : 32; }
+
+// Launches (wal_status).  attn_stream: rows of each key/value head <= 16 tiles, tiles 1 or 2;
+// attn_join adds what it wrote when a.n_splits > 1.
+int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream);
+int attn_join(const Attn& a, uint32_t dim, void* stream);
+
+}  // namespace wal
+
+namespace {
+
+using namespace wal;
+
+constexpr float kNoMax = -3.0e38f;   // a running maximum before the first key: finite, so that nothing subtracts infinities
+
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// A sequence's part of a call, cut to the rows and tokens that there are
+// whatever starts and lens hold.
+struct Seq {
+  int32_t first, rows, len, old;   // first query row, rows, tokens, tokens before the first row's own
+};
+
+__device__ __forceinline__ Seq seq_of(const Attn& a, uint32_t s, bool paged) {
+  Seq q;
+  q.first = max(a.starts[s], 0);
+  const int32_t new_s = min(a.starts[s + 1], (int32_t)a.n) - q.first;
+  q.rows = max(min(new_s, (int32_t)a.max_new), 0);
+  q.len = max(min(paged ? a.lens[s] : new_s, (int32_t)a.max_len), 0);
+  q.old = paged ? q.len - new_s : 0;
+  return q;
+}
+
+// The sequence of query row t: the last s with starts[s] <= t.
+__device__ __forceinline__ uint32_t find_seq(const int32_t* starts, uint32_t n_seqs, int32_t t) {
+  uint32_t lo = 0, hi = n_seqs;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (starts[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ bf16x8_t as_bf16x8(u32x4_t v) { return __builtin_bit_cast(bf16x8_t, v); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2_t v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// Four int8 codes to bf16, exactly: their floats' upper halves.
+__device__ __forceinline__ u32x2_t codes_to_bf16(uint32_t w) {
+  const float f0 = (float)(int8_t)w, f1 = (float)(int8_t)(w >> 8), f2 = (float)(int8_t)(w >> 16),
+              f3 = (float)(int8_t)(w >> 24);
+  return u32x2_t{__builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u),
+                 __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u)};
+}
+
+// A pair of bf16 with infinities and NaN replaced by zero; any: set if there was one.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& any) {
+  const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
+  any |= lo || hi;
+  return (lo ? 0u : w & 0xFFFFu) | (hi ? 0u : w & 0xFFFF0000u);
+}
+
+}  // namespace

@@ -7,42 +7,9 @@
 // over the keys, nothing kept of the scores.
 #include <hip/hip_runtime.h>
 
-#include "wal_args.h"
-#include "wal_device.h"
+#include "wal_attn.h"
 
 namespace {
-
-struct Attn {
-  const uint16_t* q;
-  uint16_t* out;
-  const int32_t* starts;
-  uint64_t ldq, ldo;
-  uint32_t n_seqs, n, q_heads, group;
-  float scale;
-  uint32_t causal, max_new, max_len;
-  // paged
-  const uint8_t* cache;
-  const int32_t* tables;
-  const int32_t* lens;
-  uint64_t off_v, off_ks, off_vs;
-  uint32_t ldt, n_pages, page_shift, kv_heads;
-  // packed rows
-  const uint16_t* k;
-  const uint16_t* v;
-  uint64_t ldk, ldv;
-};
-
-enum { kPacked = 0, kPagedBf16 = 1, kPagedInt8 = 2 };
-
-// The sequence of query row t: the last s with starts[s] <= t.
-__device__ __forceinline__ uint32_t find_seq(const int32_t* starts, uint32_t n_seqs, int32_t t) {
-  uint32_t lo = 0, hi = n_seqs;   // starts[lo] <= t < starts[hi]
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) / 2;
-    if (starts[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 
 template <int KIND, int D>
 __device__ __forceinline__ float element(const Attn& a, bool v, int64_t row, uint32_t h, uint32_t e) {
@@ -63,14 +30,11 @@ __global__ __launch_bounds__(64) void k_attn_row(Attn a) {
   const uint32_t t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, kvh = h / a.group;
   if (a.starts[0] > (int32_t)t || a.starts[a.n_seqs] <= (int32_t)t) return;
   const uint32_t s = find_seq(a.starts, a.n_seqs, (int32_t)t);
-  // bounds that lie are cut to the rows that there are
-  const int32_t first = max(a.starts[s], 0), new_s = min(a.starts[s + 1], (int32_t)a.n) - first;
-  int32_t len = KIND == kPacked ? new_s : max(min(a.lens[s], (int32_t)a.max_len), 0);
-  if (KIND == kPacked) len = min(len, (int32_t)a.max_len);
-  const int32_t i = (int32_t)t - first;
-  if (i < 0 || i >= (int32_t)a.max_new) return;
-  const int32_t last = KIND == kPacked ? (a.causal ? i : len - 1) : len - new_s + i;
-  const int32_t keys = min(len, last + 1);
+  const Seq q = seq_of(a, s, KIND != kPacked);
+  const int32_t first = q.first, i = (int32_t)t - first;
+  if (i < 0 || i >= q.rows) return;
+  const int32_t last = a.causal ? q.old + i : q.len - 1;
+  const int32_t keys = min(q.len, last + 1);
   for (uint32_t e = lane; e < D; e += 64) qs[e] = __uint_as_float((uint32_t)a.q[t * a.ldq + h * D + e] << 16);
   __syncthreads();
   float m = -INFINITY, l = 0.f, acc[D / 64] = {};
@@ -99,8 +63,8 @@ __global__ __launch_bounds__(64) void k_attn_row(Attn a) {
     float top = x;
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     const float mn = fmaxf(m, top);
-    const float c = mn == -INFINITY ? 1.f : expf(m - mn);
-    const float p = row >= 0 ? expf(x - mn) : 0.f;
+    const float c = mn == -INFINITY ? 1.f : exp2f(m - mn);
+    const float p = row >= 0 ? exp2f(x - mn) : 0.f;
     float sum = p;
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
     l = l * c + sum;
@@ -132,6 +96,38 @@ bool heads_ok(uint32_t q_heads, uint32_t kv_heads) {
 }
 
 constexpr uint32_t kMaxRows = 1u << 26;   // query rows, sequences and tokens of a call
+constexpr float kLog2e = 1.4426950408889634f;
+
+// How a call over the cache is cut.
+struct Plan {
+  bool stream;               // few rows for each key/value head
+  uint32_t split, n_splits, part_rows;
+  uint64_t off_ml, bytes;    // of the workspace
+};
+
+// The context is split when sequences times key/value heads leave compute units idle: into
+// enough pieces for four workgroups on each, not below 256 keys a piece, not above what a workgroup's
+// page list holds.
+Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t max_new, uint32_t max_len) {
+  Plan p{};
+  const uint32_t group = q_heads / d->kv_heads;
+  const uint64_t rows = (uint64_t)max_new * group;
+  p.stream = rows <= stream_rows(d->head_dim);
+  p.n_splits = 1;
+  p.split = kMaxSplit;
+  if (!p.stream || !rows || !n_seqs || !max_len) return p;
+  const uint64_t items = (uint64_t)n_seqs * d->kv_heads, want = (1024 + items - 1) / items;
+  uint32_t split = (uint32_t)((max_len + want - 1) / want);
+  split = split < 256 ? 256 : (split + 127) / 128 * 128;
+  p.split = split > kMaxSplit ? kMaxSplit : split;
+  p.n_splits = (max_len + p.split - 1) / p.split;
+  if (p.n_splits == 1) return p;
+  p.part_rows = (uint32_t)rows;
+  const uint64_t slots = items * p.n_splits * rows;
+  p.off_ml = slots * d->head_dim * 4;
+  p.bytes = p.off_ml + slots * 8;
+  return p;
+}
 
 }  // namespace
 
@@ -144,7 +140,7 @@ extern "C" int wal_attn_paged_workspace_size(const wal_kv_desc* d, uint32_t q_he
   if (!heads_ok(q_heads, d->kv_heads) || n_seqs > kMaxRows || n > kMaxRows || max_new > kMaxRows ||
       max_len > (1u << 30))
     return WAL_ERR_SHAPE;
-  *bytes = 0;
+  *bytes = plan_of(d, q_heads, n_seqs, max_new, max_len).bytes;
   return WAL_OK;
 }
 
@@ -184,7 +180,7 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   a.n = n;
   a.q_heads = q_heads;
   a.group = q_heads / d->kv_heads;
-  a.scale = scale;
+  a.scale = scale * kLog2e;
   a.causal = 1;
   a.max_new = max_new;
   a.max_len = max_len;
@@ -199,6 +195,17 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   a.page_shift = (uint32_t)__builtin_ctz(d->page_size);
   a.kv_heads = d->kv_heads;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  const Plan p = plan_of(d, q_heads, n_seqs, max_new, max_len);
+  if (p.stream) {
+    a.split = p.split;
+    a.n_splits = p.n_splits;
+    a.part_rows = p.part_rows;
+    a.part = static_cast<float*>(ws_dev);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws_dev) + p.off_ml);
+    if ((uint64_t)n_seqs * d->kv_heads * p.n_splits > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
+    st = attn_stream(a, d->fmt == WAL_KV_INT8, d->head_dim, max_new * a.group <= 16 ? 1 : 2, stream);
+    return st || p.n_splits == 1 ? st : attn_join(a, d->head_dim, stream);
+  }
   return d->fmt == WAL_KV_INT8 ? launch<kPagedInt8>(a, d->head_dim, s) : launch<kPagedBf16>(a, d->head_dim, s);
 }
 
@@ -235,7 +242,7 @@ extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_de
   a.n = n;
   a.q_heads = q_heads;
   a.group = q_heads / kv_heads;
-  a.scale = scale;
+  a.scale = scale * kLog2e;
   a.causal = causal ? 1 : 0;
   a.max_new = a.max_len = max_len;
   a.kv_heads = kv_heads;

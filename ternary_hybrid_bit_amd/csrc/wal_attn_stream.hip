@@ -1,0 +1,383 @@
+// Attention of a few new tokens over the paged cache for gfx950 (decode): up
+// to 32 query rows for each key/value head, a row being one token of one of
+// the query heads that share it.
+//
+// Bound by the bytes of the cache, each read once.  A workgroup takes one
+// key/value head of one sequence over `split` keys, its wavefronts taking tiles of 32
+// keys in turn.  Everything is computed transposed, so that a lane's scores
+// belong to one query row (lane & 15) and no value moves between lanes:
+//   S^T = K Q^T   v_mfma_f32_16x16x32_bf16, A = 16 keys, B = the query rows.
+//     The keys are dealt to the two A tiles of a tile of 32 so that lane
+//     group c = lane >> 4 receives the scores of keys 8 c .. 8 c + 7.
+//   O^T += V^T P^T  with exactly those keys as the B operand's K block, A = V^T:
+//     lane m of a group loads dim / 16 neighbouring elements of each of its 8 keys
+//     (whole rows across the 16 lanes), and one byte permutation per two
+//     elements turns eight keys into the operand.  No LDS is touched.
+// K and V tiles go from memory straight to registers, the next tile's loads
+// issued as soon as the current one's registers are consumed.
+//
+// The softmax is the running one, with weights 2^(x - m): m follows the true
+// maximum only when a score exceeds it by more than 8 (weights up to 2^8 lose
+// nothing in fp32 or bf16), so most tiles exchange nothing between lanes and
+// rescale nothing.
+//
+// Wavefronts join through LDS; when the context is split over workgroups, each
+// writes its sums in fp32 and k_attn_join adds them in the order of the splits.
+#include <hip/hip_runtime.h>
+
+#include "wal_attn.h"
+
+namespace {
+
+constexpr float kSlack = 8.f;
+
+template <int FMT, int D>
+struct Tile {
+  static constexpr bool kInt8 = FMT == kPagedInt8;
+  static constexpr int E = D / 16;                     // elements of a v row in a lane
+  u32x4_t k[2][kInt8 ? D / 64 : D / 32];
+  uint32_t v[8][kInt8 ? E / 4 : E / 2];
+  float ks[kInt8 ? 8 : 1], vs[kInt8 ? 8 : 1];
+};
+
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(uint32_t* d, const uint8_t* p) {
+  if constexpr (BYTES >= 16) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const u32x4_t w = reinterpret_cast<const u32x4_t*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = w[j];
+    }
+  } else if constexpr (BYTES == 8) {
+    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+    d[0] = w[0];
+    d[1] = w[1];
+  } else {
+    d[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// groups: row index of the first key of each 16 keys of the workgroup (below
+// 0: on no page of the cache).
+template <int FMT, int D>
+__device__ __forceinline__ void load_k(Tile<FMT, D>& t, const Attn& a, const int64_t* groups, uint32_t g, uint32_t lane) {
+  constexpr uint32_t eb = FMT == kPagedInt8 ? 1 : 2;
+  const uint32_t m = lane & 15, c = lane >> 4;
+  const int64_t base = max(groups[g + (m >> 3)], (int64_t)0) + 8 * ((m >> 2) & 1) + (m & 3);
+  const uint8_t* p = a.cache + (uint64_t)base * D * eb + 16 * c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int u = 0; u < (int)(D * eb / 64); ++u)
+      t.k[h][u] = *reinterpret_cast<const u32x4_t*>(p + 4 * h * D * eb + 64 * u);
+  if constexpr (FMT == kPagedInt8) {
+    const int64_t r = max(groups[g + (c >> 1)], (int64_t)0) + 8 * (c & 1);
+    load_bytes<32>(reinterpret_cast<uint32_t*>(t.ks), a.cache + a.off_ks + 4 * r);
+  }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_v(Tile<FMT, D>& t, const Attn& a, const int64_t* groups, uint32_t g, uint32_t lane) {
+  constexpr uint32_t eb = FMT == kPagedInt8 ? 1 : 2, E = D / 16;
+  const uint32_t m = lane & 15, c = lane >> 4;
+  const int64_t r = max(groups[g + (c >> 1)], (int64_t)0) + 8 * (c & 1);
+  const uint8_t* p = a.cache + a.off_v + (uint64_t)r * D * eb + E * eb * m;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load_bytes<E * eb>(t.v[i], p + i * D * eb);
+  if constexpr (FMT == kPagedInt8) load_bytes<32>(reinterpret_cast<uint32_t*>(t.vs), a.cache + a.off_vs + 4 * r);
+}
+
+// V^T as the A operand of element e: keys 8 c .. 8 c + 7 of dim E (lane & 15) + e.
+template <int FMT, int D>
+__device__ __forceinline__ bf16x8_t v_operand(const Tile<FMT, D>& t, int e) {
+  u32x4_t w;
+  if constexpr (FMT == kPagedInt8) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float x = (float)(int8_t)(t.v[2 * p][e / 4] >> (8 * (e % 4)));
+      const float y = (float)(int8_t)(t.v[2 * p + 1][e / 4] >> (8 * (e % 4)));
+      w[p] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      w[p] = __builtin_amdgcn_perm(t.v[2 * p + 1][e / 2], t.v[2 * p][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+  }
+  return as_bf16x8(w);
+}
+
+template <int FMT, int D, int NT, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
+  constexpr int E = D / 16;
+  constexpr bool kInt8 = FMT == kPagedInt8;
+  __shared__ int64_t groups[kMaxSplit / 16 + 2];
+  __shared__ float osh[NW][16][D + 4];
+  __shared__ float msh[NW][16], lsh[NW][16];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, c = lane >> 4;
+  const uint32_t kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+  const uint32_t sp = rest % a.n_splits, s = rest / a.n_splits;
+  const Seq q = seq_of(a, s, true);
+  const int32_t k0 = (int32_t)(sp * a.split), k1 = min(k0 + (int32_t)a.split, q.len);
+  const int32_t nrows = q.rows * (int32_t)a.group;
+  if (!nrows || (k0 >= k1 && (sp || a.n_splits > 1))) return;
+
+  for (uint32_t i = threadIdx.x; i < (uint32_t)(max(k1 - k0, 0) + 31) / 32 * 2; i += 64 * NW) {
+    const uint32_t key = (uint32_t)k0 + 16 * i;
+    int64_t row = -1;
+    if ((int32_t)key < k1) {
+      const uint32_t page = (uint32_t)a.tables[(uint64_t)s * a.ldt + (key >> a.page_shift)];
+      if (page < a.n_pages)
+        row = (int64_t)(((uint64_t)page * a.kv_heads + kvh) << a.page_shift) + (key & ((1u << a.page_shift) - 1));
+    }
+    groups[i] = row;
+  }
+
+  // the query rows as B operands, in the order in which the keys' elements are loaded
+  bf16x8_t qf[NT][D / 32];
+  int32_t last[NT];   // the last key that the lane's row sees
+  int64_t at[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int32_t r = 16 * t + (int32_t)n, i = r / (int32_t)a.group;
+    const bool live = r < nrows;
+    last[t] = live ? q.old + i : -1;
+    at[t] = live ? (int64_t)(kvh * a.group + r - i * (int32_t)a.group) * D : -1;
+    const uint16_t* p = a.q + (uint64_t)(q.first + (live ? i : 0)) * a.ldq + (live ? at[t] : 0);
+#pragma unroll
+    for (int st = 0; st < D / 32; ++st) {
+      const uint32_t d = kInt8 ? 64 * (st / 2) + 16 * c + 8 * (st % 2) : 32 * st + 8 * c;
+      u32x4_t w = *reinterpret_cast<const u32x4_t*>(p + d);
+      if (!live) w = u32x4_t{0, 0, 0, 0};
+      qf[t][st] = as_bf16x8(w);
+    }
+  }
+  f32x4_t o[NT][E];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = kNoMax;
+    l[t] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[t][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  __syncthreads();
+
+  Tile<FMT, D> kv;
+  uint32_t g = 2 * wave;   // the tile's first group
+  const uint32_t g_end = (uint32_t)(max(k1 - k0, 0) + 31) / 32 * 2;
+  if (g < g_end) {
+    load_k<FMT, D>(kv, a, groups, g, lane);
+    load_v<FMT, D>(kv, a, groups, g, lane);
+  }
+  for (; g < g_end; g += 2 * NW) {
+    const int32_t kb = k0 + 16 * (int32_t)g;
+    const bool there = groups[g + (c >> 1)] >= 0;
+    const bool full = kb + 31 <= q.old && __all(there);
+    f32x4_t x[NT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < D / 32; ++st) {
+        u32x4_t w;
+        if constexpr (kInt8) {
+          const u32x2_t lo = codes_to_bf16(kv.k[h][st / 2][2 * (st % 2)]), hi = codes_to_bf16(kv.k[h][st / 2][2 * (st % 2) + 1]);
+          w = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+          w = kv.k[h][st];
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          x[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), qf[t][st], x[t][h], 0, 0, 0);
+      }
+    }
+    float ks[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ks[i] = kInt8 ? kv.ks[kInt8 ? i : 0] * a.scale : a.scale;
+    const bool more = g + 2 * NW < g_end;
+    if (more) load_k<FMT, D>(kv, a, groups, g + 2 * NW, lane);
+
+    bool odd = false;   // an infinity or NaN among the values of a tile that some row sees only in part
+    if (!kInt8 && !full) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < (int)(sizeof(kv.v[0]) / 4); ++e) kv.v[i][e] = finite_pair(kv.v[i][e], odd);
+    }
+    bf16x8_t pf[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float y[8], top = kNoMax;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = x[t][i / 4][i % 4] * ks[i];
+        if (!full) y[i] = there && kb + 8 * (int32_t)c + i <= last[t] ? y[i] : -INFINITY;
+        top = fmaxf(top, y[i]);
+      }
+      if (__any(top > m[t] + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m[t], top), f = __builtin_amdgcn_exp2f(m[t] - mn);
+        m[t] = mn;
+        l[t] *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[t][e] *= f;
+      }
+      u32x4_t w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = __builtin_amdgcn_exp2f(y[i] - m[t]);
+        l[t] += y[i];
+        if constexpr (kInt8) y[i] = full || (there && kb + 8 * (int32_t)c + i <= last[t]) ? y[i] * kv.vs[i] : 0.f;
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) w[p] = pack_bf16(y[2 * p], y[2 * p + 1]);
+      pf[t] = as_bf16x8(w);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bf16x8_t vf = v_operand<FMT, D>(kv, e);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[t], o[t][e], 0, 0, 0);
+    }
+    if (!kInt8 && __any(odd)) {
+      // each row takes the infinities and NaN of the keys that it sees, and of those only
+      for (int32_t j = 0; j < 32; ++j) {
+        const int64_t row = groups[g + (j >> 4)];
+        if (row < 0 || kb + j >= k1) continue;
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.cache + a.off_v) + (uint64_t)(row + (j & 15)) * D;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t b = p[E * (4 * c + r) + e];
+              if ((b & 0x7F80u) == 0x7F80u && kb + j <= last[t]) o[t][e][r] += __uint_as_float(b << 16);
+            }
+      }
+    }
+    if (more) load_v<FMT, D>(kv, a, groups, g + 2 * NW, lane);
+  }
+
+  // the wavefronts' sums: common maximum, then one pass over rows and elements
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (t) __syncthreads();
+    if (c == 0) {
+      msh[wave][n] = m[t];
+      lsh[wave][n] = l[t];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) osh[wave][n][E * (4 * c + r) + e] = o[t][e][r];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 16 * D / 4; i += 64 * NW) {
+      const uint32_t row = i / (D / 4), d = 4 * (i % (D / 4));
+      const int32_t r = 16 * t + (int32_t)row;
+      if (r >= nrows) continue;
+      float top = kNoMax, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, msh[w][row]);
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = __builtin_amdgcn_exp2f(msh[w][row] - top);
+        sum += f * lsh[w][row];
+        acc += f * *reinterpret_cast<const f32x4_t*>(&osh[w][row][d]);
+      }
+      if (a.n_splits == 1) {
+        const int32_t tok = r / (int32_t)a.group;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t* p = a.out + (uint64_t)(q.first + tok) * a.ldo + (uint64_t)(kvh * a.group + r - tok * (int32_t)a.group) * D + d;
+        *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f)};
+      } else {
+        const uint64_t slot = (((uint64_t)s * a.n_splits + sp) * a.kv_heads + kvh) * a.part_rows + r;
+        *reinterpret_cast<f32x4_t*>(a.part + slot * D + d) = acc;
+        if (d == 0) a.part_ml[slot] = make_float2(top, sum);
+      }
+    }
+  }
+}
+
+// The splits' sums of one row: 256 threads, dim / 4 of them to a split.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join(Attn a) {
+  constexpr uint32_t kLanes = D / 4, kAtOnce = 256 / kLanes;
+  __shared__ f32x4_t osh[kAtOnce][kLanes];
+  __shared__ float lsh[kAtOnce];
+  const uint32_t t = blockIdx.x, h = blockIdx.y, kvh = h / a.group;
+  if (a.starts[0] > (int32_t)t || a.starts[a.n_seqs] <= (int32_t)t) return;
+  const uint32_t s = find_seq(a.starts, a.n_seqs, (int32_t)t);
+  const Seq q = seq_of(a, s, true);
+  const int32_t i = (int32_t)t - q.first;
+  if (i < 0 || i >= q.rows) return;
+  const uint32_t r = (uint32_t)i * a.group + h - kvh * a.group;
+  const uint32_t splits = ((uint32_t)q.len + a.split - 1) / a.split;
+  const uint64_t step = (uint64_t)a.kv_heads * a.part_rows;
+  const uint64_t slot = ((uint64_t)s * a.n_splits * a.kv_heads + kvh) * a.part_rows + r;
+  float top = kNoMax;
+  for (uint32_t p = 0; p < splits; ++p) top = fmaxf(top, a.part_ml[slot + p * step].x);
+  const uint32_t lane = threadIdx.x % kLanes, mine = threadIdx.x / kLanes;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+  for (uint32_t p = mine; p < splits; p += kAtOnce) {
+    const float2 ml = a.part_ml[slot + p * step];
+    const float f = __builtin_amdgcn_exp2f(ml.x - top);
+    sum += f * ml.y;
+    acc += f * *reinterpret_cast<const f32x4_t*>(a.part + (slot + p * step) * D + 4 * lane);
+  }
+  osh[mine][lane] = acc;
+  if (!lane) lsh[mine] = sum;
+  __syncthreads();
+  if (mine) return;
+#pragma unroll
+  for (uint32_t w = 1; w < kAtOnce; ++w) {
+    acc += osh[w][lane];
+    sum += lsh[w];
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<u32x2_t*>(a.out + (uint64_t)t * a.ldo + (uint64_t)h * D + 4 * lane) =
+      u32x2_t{pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f)};
+}
+
+template <int FMT, int D>
+void launch(const Attn& a, uint32_t tiles, hipStream_t s) {
+  const dim3 grid(a.n_splits * a.kv_heads * a.n_seqs), block(256);
+  if (tiles == 1) hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, 4>), grid, block, 0, s, a);
+  else if constexpr (stream_rows(D) > 16) hipLaunchKernelGGL((k_attn_stream<FMT, D, 2, 4>), grid, block, 0, s, a);
+}
+
+}  // namespace
+
+namespace wal {
+
+int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (int8) {
+    if (dim == 64) launch<kPagedInt8, 64>(a, tiles, s);
+    if (dim == 128) launch<kPagedInt8, 128>(a, tiles, s);
+    if (dim == 256) launch<kPagedInt8, 256>(a, tiles, s);
+  } else {
+    if (dim == 64) launch<kPagedBf16, 64>(a, tiles, s);
+    if (dim == 128) launch<kPagedBf16, 128>(a, tiles, s);
+    if (dim == 256) launch<kPagedBf16, 256>(a, tiles, s);
+  }
+  return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
+}
+
+int attn_join(const Attn& a, uint32_t dim, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid(a.n, a.q_heads), block(256);
+  if (dim == 64) hipLaunchKernelGGL(k_attn_join<64>, grid, block, 0, s, a);
+  if (dim == 128) hipLaunchKernelGGL(k_attn_join<128>, grid, block, 0, s, a);
+  if (dim == 256) hipLaunchKernelGGL(k_attn_join<256>, grid, block, 0, s, a);
+  return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
+}
+
+}  // namespace wal
