@@ -22,7 +22,7 @@ ARCH = os.environ.get("WAL_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 HIP_SOURCES = ["wal_gpu.hip", "wal_base3.hip", "wal_gemm.hip", "wal_rotate.hip", "wal_int4.hip", "wal_rope.hip",
-               "wal_attn.hip", "wal_attn_stream.hip"]
+               "wal_attn.hip", "wal_attn_stream.hip", "wal_attn_tile.hip"]
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument"]

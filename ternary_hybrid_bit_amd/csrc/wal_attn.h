@@ -41,6 +41,10 @@ constexpr uint32_t stream_rows(uint32_t dim) { return dim == 256 ? 16 : 32; }
 // attn_join adds what it wrote when a.n_splits > 1.
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream);
 int attn_join(const Attn& a, uint32_t dim, void* stream);
+// Any number of rows; kind kPacked, kPagedBf16 or kPagedInt8.  attn_tiles: how many
+// tiles of query rows (workgroups of each key/value head and split) it launches.
+int attn_tile(const Attn& a, int kind, uint32_t dim, void* stream);
+uint64_t attn_tiles(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t dim);
 
 }  // namespace wal
 

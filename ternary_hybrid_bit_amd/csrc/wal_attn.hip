@@ -1,95 +1,10 @@
-// Attention over the paged cache and over packed prompts for gfx950:
-//     out[row][h] = sum_j w_j v_j,  w = softmax_j(scale * q[row][h] . k_j).
-//
-// One wavefront takes one query row of one head and runs over its keys 64 at
-// a time, one lane per key for the scores and one lane per few elements of v
-// for the sums, with the running maximum and sum of the softmax: one pass
-// over the keys, nothing kept of the scores.
+// Entry points of the attention over the paged cache and over packed prompts:
+// checks of the arguments, the choice of kernel and the cutting of the context.
 #include <hip/hip_runtime.h>
 
 #include "wal_attn.h"
 
 namespace {
-
-template <int KIND, int D>
-__device__ __forceinline__ float element(const Attn& a, bool v, int64_t row, uint32_t h, uint32_t e) {
-  if constexpr (KIND == kPacked) {
-    const uint16_t* p = v ? a.v + row * a.ldv : a.k + row * a.ldk;
-    return __uint_as_float((uint32_t)p[h * D + e] << 16);
-  } else if constexpr (KIND == kPagedBf16) {
-    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.cache + (v ? a.off_v : 0))[row * D + e] << 16);
-  } else {
-    return (float)reinterpret_cast<const int8_t*>(a.cache + (v ? a.off_v : 0))[row * D + e];
-  }
-}
-
-template <int KIND, int D>
-__global__ __launch_bounds__(64) void k_attn_row(Attn a) {
-  __shared__ float qs[D], ps[64];
-  __shared__ int64_t rs[64];
-  const uint32_t t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, kvh = h / a.group;
-  if (a.starts[0] > (int32_t)t || a.starts[a.n_seqs] <= (int32_t)t) return;
-  const uint32_t s = find_seq(a.starts, a.n_seqs, (int32_t)t);
-  const Seq q = seq_of(a, s, KIND != kPacked);
-  const int32_t first = q.first, i = (int32_t)t - first;
-  if (i < 0 || i >= q.rows) return;
-  const int32_t last = a.causal ? q.old + i : q.len - 1;
-  const int32_t keys = min(q.len, last + 1);
-  for (uint32_t e = lane; e < D; e += 64) qs[e] = __uint_as_float((uint32_t)a.q[t * a.ldq + h * D + e] << 16);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, acc[D / 64] = {};
-  for (int32_t j0 = 0; j0 < keys; j0 += 64) {
-    const int32_t j = j0 + (int32_t)lane;
-    int64_t row = -1;
-    if (j < keys) {
-      if constexpr (KIND == kPacked) {
-        row = first + j;
-      } else {
-        const uint32_t page = (uint32_t)a.tables[(uint64_t)s * a.ldt + (j >> a.page_shift)];
-        if (page < a.n_pages)
-          row = ((int64_t)((uint64_t)page * a.kv_heads + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
-      }
-    }
-    float x = -INFINITY, vs = 1.f;
-    if (row >= 0) {
-      x = 0.f;
-      for (uint32_t e = 0; e < D; ++e) x += qs[e] * element<KIND, D>(a, false, row, kvh, e);
-      x *= a.scale;
-      if constexpr (KIND == kPagedInt8) {
-        x *= reinterpret_cast<const float*>(a.cache + a.off_ks)[row];
-        vs = reinterpret_cast<const float*>(a.cache + a.off_vs)[row];
-      }
-    }
-    float top = x;
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float mn = fmaxf(m, top);
-    const float c = mn == -INFINITY ? 1.f : exp2f(m - mn);
-    const float p = row >= 0 ? exp2f(x - mn) : 0.f;
-    float sum = p;
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    l = l * c + sum;
-    m = mn;
-    ps[lane] = p * vs;
-    rs[lane] = row;
-    __syncthreads();
-    for (int u = 0; u < D / 64; ++u) acc[u] *= c;
-    for (int r = 0; r < 64; ++r)
-      if (rs[r] >= 0)
-        for (int u = 0; u < D / 64; ++u) acc[u] += ps[r] * element<KIND, D>(a, true, rs[r], kvh, 64 * u + lane);
-    __syncthreads();
-  }
-  for (int u = 0; u < D / 64; ++u)
-    a.out[t * a.ldo + h * D + 64 * u + lane] = (uint16_t)bf16_rne(l > 0.f ? acc[u] / l : (l == 0.f ? 0.f : l));
-}
-
-template <int KIND>
-int launch(const Attn& a, uint32_t dim, hipStream_t s) {
-  const dim3 grid(a.n, a.q_heads);
-  if (dim == 64) hipLaunchKernelGGL((k_attn_row<KIND, 64>), grid, dim3(64), 0, s, a);
-  if (dim == 128) hipLaunchKernelGGL((k_attn_row<KIND, 128>), grid, dim3(64), 0, s, a);
-  if (dim == 256) hipLaunchKernelGGL((k_attn_row<KIND, 256>), grid, dim3(64), 0, s, a);
-  return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
-}
 
 bool heads_ok(uint32_t q_heads, uint32_t kv_heads) {
   return q_heads && kv_heads && q_heads % kv_heads == 0 && q_heads / kv_heads <= 64;
@@ -100,30 +15,36 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // How a call over the cache is cut.
 struct Plan {
-  bool stream;               // few rows for each key/value head
+  bool stream;               // few rows for each key/value head: attn_stream, else attn_tile
   uint32_t split, n_splits, part_rows;
   uint64_t off_ml, bytes;    // of the workspace
 };
 
-// The context is split when sequences times key/value heads leave compute units idle: into
-// enough pieces for four workgroups on each, not below 256 keys a piece, not above what a workgroup's
-// page list holds.
-Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t max_new, uint32_t max_len) {
+// The context is split when the workgroups of whole contexts leave compute units
+// idle.  Few rows: into enough pieces for four workgroups on each unit, not
+// below 256 keys a piece (its first loads), not above what a workgroup's
+// page list holds.  Many rows: two workgroups a unit, not below 512 keys, so that
+// the partial results stay small beside the products.
+Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n, uint32_t max_new,
+             uint32_t max_len) {
   Plan p{};
   const uint32_t group = q_heads / d->kv_heads;
   const uint64_t rows = (uint64_t)max_new * group;
   p.stream = rows <= stream_rows(d->head_dim);
   p.n_splits = 1;
-  p.split = kMaxSplit;
-  if (!p.stream || !rows || !n_seqs || !max_len) return p;
-  const uint64_t items = (uint64_t)n_seqs * d->kv_heads, want = (1024 + items - 1) / items;
-  uint32_t split = (uint32_t)((max_len + want - 1) / want);
-  split = split < 256 ? 256 : (split + 127) / 128 * 128;
-  p.split = split > kMaxSplit ? kMaxSplit : split;
-  p.n_splits = (max_len + p.split - 1) / p.split;
+  p.split = p.stream ? kMaxSplit : max_len;
+  if (!rows || !n_seqs || !max_len || !n) return p;
+  const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->head_dim)) * d->kv_heads;
+  const uint64_t target = p.stream ? 1024 : 512, least = p.stream ? 256 : 512;
+  const uint64_t want = (target + items - 1) / items;
+  uint64_t split = ((max_len + want - 1) / want + 127) / 128 * 128;
+  if (split < least) split = least;
+  if (p.stream && split > kMaxSplit) split = kMaxSplit;
+  p.split = (uint32_t)split;
+  p.n_splits = (uint32_t)((max_len + split - 1) / split);
   if (p.n_splits == 1) return p;
   p.part_rows = (uint32_t)rows;
-  const uint64_t slots = items * p.n_splits * rows;
+  const uint64_t slots = (uint64_t)n_seqs * d->kv_heads * p.n_splits * rows;
   p.off_ml = slots * d->head_dim * 4;
   p.bytes = p.off_ml + slots * 8;
   return p;
@@ -140,7 +61,7 @@ extern "C" int wal_attn_paged_workspace_size(const wal_kv_desc* d, uint32_t q_he
   if (!heads_ok(q_heads, d->kv_heads) || n_seqs > kMaxRows || n > kMaxRows || max_new > kMaxRows ||
       max_len > (1u << 30))
     return WAL_ERR_SHAPE;
-  *bytes = plan_of(d, q_heads, n_seqs, max_new, max_len).bytes;
+  *bytes = plan_of(d, q_heads, n_seqs, n, max_new, max_len).bytes;
   return WAL_OK;
 }
 
@@ -194,19 +115,16 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   a.n_pages = d->n_pages;
   a.page_shift = (uint32_t)__builtin_ctz(d->page_size);
   a.kv_heads = d->kv_heads;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const Plan p = plan_of(d, q_heads, n_seqs, max_new, max_len);
-  if (p.stream) {
-    a.split = p.split;
-    a.n_splits = p.n_splits;
-    a.part_rows = p.part_rows;
-    a.part = static_cast<float*>(ws_dev);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws_dev) + p.off_ml);
-    if ((uint64_t)n_seqs * d->kv_heads * p.n_splits > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
-    st = attn_stream(a, d->fmt == WAL_KV_INT8, d->head_dim, max_new * a.group <= 16 ? 1 : 2, stream);
-    return st || p.n_splits == 1 ? st : attn_join(a, d->head_dim, stream);
-  }
-  return d->fmt == WAL_KV_INT8 ? launch<kPagedInt8>(a, d->head_dim, s) : launch<kPagedBf16>(a, d->head_dim, s);
+  const Plan p = plan_of(d, q_heads, n_seqs, n, max_new, max_len);
+  const bool int8 = d->fmt == WAL_KV_INT8;
+  a.split = p.split;
+  a.n_splits = p.n_splits;
+  a.part_rows = p.part_rows;
+  a.part = static_cast<float*>(ws_dev);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws_dev) + p.off_ml);
+  st = p.stream ? attn_stream(a, int8, d->head_dim, max_new * a.group <= 16 ? 1 : 2, stream)
+                : attn_tile(a, int8 ? kPagedInt8 : kPagedBf16, d->head_dim, stream);
+  return st || p.n_splits == 1 ? st : attn_join(a, d->head_dim, stream);
 }
 
 extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk, const void* v_dev,
@@ -246,5 +164,6 @@ extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_de
   a.causal = causal ? 1 : 0;
   a.max_new = a.max_len = max_len;
   a.kv_heads = kv_heads;
-  return launch<kPacked>(a, head_dim, static_cast<hipStream_t>(stream));
+  a.n_splits = 1;
+  return attn_tile(a, kPacked, head_dim, stream);
 }
