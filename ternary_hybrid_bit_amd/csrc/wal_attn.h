@@ -15,7 +15,8 @@ struct Attn {
   const int32_t* starts;
   uint64_t ldq, ldo;
   uint32_t n_seqs, n, q_heads, kv_heads, group;
-  float scale;                   // of the scores, times log2(e): weights are powers of two
+  float scale;                   // of the scores, times log2(e): weights are powers of two; above 0,
+  uint32_t q_sign;               // its sign goes to the queries (exclusive or on bf16 pairs)
   uint32_t causal, max_new, max_len;
   // paged
   const uint8_t* cache;

@@ -13,6 +13,13 @@ bool heads_ok(uint32_t q_heads, uint32_t kv_heads) {
 constexpr uint32_t kMaxRows = 1u << 26;   // query rows, sequences and tokens of a call
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The kernels multiply scores by a positive number only: masked ones are -infinity, so a
+// scale of zero becomes one too small to tell weights apart.
+void set_scale(Attn& a, float scale) {
+  a.scale = fmaxf(fabsf(scale * kLog2e), 1e-30f);
+  a.q_sign = scale < 0.f ? 0x80008000u : 0u;
+}
+
 // How a call over the cache is cut.
 struct Plan {
   bool stream;               // few rows for each key/value head: attn_stream, else attn_tile
@@ -101,7 +108,7 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   a.n = n;
   a.q_heads = q_heads;
   a.group = q_heads / d->kv_heads;
-  a.scale = scale * kLog2e;
+  set_scale(a, scale);
   a.causal = 1;
   a.max_new = max_new;
   a.max_len = max_len;
@@ -160,7 +167,7 @@ extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_de
   a.n = n;
   a.q_heads = q_heads;
   a.group = q_heads / kv_heads;
-  a.scale = scale * kLog2e;
+  set_scale(a, scale);
   a.causal = causal ? 1 : 0;
   a.max_new = a.max_len = max_len;
   a.kv_heads = kv_heads;

@@ -148,7 +148,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
     for (int st = 0; st < D / 32; ++st) {
       const uint32_t d = kInt8 ? 64 * (st / 2) + 16 * c + 8 * (st % 2) : 32 * st + 8 * c;
       u32x4_t w = *reinterpret_cast<const u32x4_t*>(p + d);
-      if (!live) w = u32x4_t{0, 0, 0, 0};
+      w = live ? w ^ a.q_sign : u32x4_t{0, 0, 0, 0};
       qf[t][st] = as_bf16x8(w);
     }
   }

@@ -54,21 +54,36 @@ struct Stage {
   static constexpr int kPasses = kKeys / kRows;
   static_assert(kKeys % kRows == 0, "whole passes");
   u32x4_t k[kPasses], v[kPasses];
-  float scale;             // int8: key scale (threads 0..63) or value scale (64..127)
+  float scale;             // int8: key scale (threads 0..63) or value scale (64..127), 0 on no page
   int32_t page[kPasses];   // of the next tile
   int32_t page_scale;
 };
+
+// 16 bytes of bf16 with infinities and NaN replaced by zero; any: whether there was one.
+__device__ __forceinline__ u32x4_t finite_piece(u32x4_t w, bool& any) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 0xFFFF in the halves whose exponent is all ones
+    const uint32_t e = ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u, f = (e >> 15) * 0xFFFFu;
+    odd |= f;
+    w[i] &= ~f;
+  }
+  any = any || odd;
+  return w;
+}
 
 template <int KIND, int D, int QT, int NW>
 __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   using St = Stage<KIND, D, NW>;
   constexpr bool kInt8 = KIND == kPagedInt8, kPaged = KIND != kPacked;
   constexpr int kRowBytes = 2 * D, kMT = D / 32;
-  constexpr uint32_t kTileRows = 32 * QT * NW;
+  constexpr uint32_t kTileRows = 32 * QT * NW, kElem = kInt8 ? 1 : 2;
   __shared__ __attribute__((aligned(256))) uint8_t ksh[2][kKeys * kRowBytes], vsh[2][kKeys * kRowBytes];
-  __shared__ float ssh[2][2][kKeys];
-  __shared__ int32_t there[2][4];
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, hh = lane >> 5;
+  __shared__ __attribute__((aligned(16))) float ssh[2][2][kKeys];
+  __shared__ int32_t there[2][4], odd[2];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t n = lane & 31, hh = lane >> 5;
   const uint32_t kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
   const uint32_t sp = rest % a.n_splits;
   uint32_t tile = rest / a.n_splits, s = 0;
@@ -128,50 +143,64 @@ __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_t
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) {
       u32x4_t w = *reinterpret_cast<const u32x4_t*>(p + 16 * st);
-      if (!live) w = u32x4_t{0, 0, 0, 0};
+      w = live ? w ^ a.q_sign : u32x4_t{0, 0, 0, 0};
       qf[t][st] = as_bf16x8(w);
     }
   }
   wave_last = min(wave_last, q.len - 1);
 
+  // Tiles from here on hold keys that some of the workgroup's rows do not see.
+  // There infinities and NaN among the values are taken out of the product (a weight of zero would
+  // make NaN of them) and given to the rows that do see them afterwards.
+  const int32_t edge = a.causal ? q.old + row0 / (int32_t)a.group : q.len - 1;
+
   St st;
   const uint32_t prow = tid / St::kPieces, ppiece = tid % St::kPieces;
   const uint32_t pmask = (1u << a.page_shift) - 1;
+  // bytes of a page of one plane, and from the plane's start to the head's rows of page 0
+  const uint32_t page_bytes = (a.kv_heads << a.page_shift) * (D * kElem), head_bytes = (kvh << a.page_shift) * (D * kElem);
+  const uint8_t* kbase = kPaged ? a.cache + head_bytes + 16 * ppiece
+                                : reinterpret_cast<const uint8_t*>(a.k + (uint64_t)q.first * a.ldk + kvh * D) + 16 * ppiece;
+  const uint8_t* vbase = kPaged ? kbase + a.off_v
+                                : reinterpret_cast<const uint8_t*>(a.v + (uint64_t)q.first * a.ldv + kvh * D) + 16 * ppiece;
   auto key_of = [&](int32_t kb, uint32_t row) { return (uint32_t)min(kb + (int32_t)row, kend - 1); };
+  const int32_t* tab = a.tables + (uint64_t)s * a.ldt;
   auto load_pages = [&](int32_t kb) {
     if constexpr (kPaged) {
-      const int32_t* tab = a.tables + (uint64_t)s * a.ldt;
 #pragma unroll
       for (int p = 0; p < St::kPasses; ++p) st.page[p] = tab[key_of(kb, prow + p * St::kRows) >> a.page_shift];
       if constexpr (kInt8) st.page_scale = tab[key_of(kb, lane) >> a.page_shift];
     }
   };
-  auto row_of = [&](int32_t page, uint32_t key) {   // a page outside the cache: any row of it, masked later
-    const uint32_t pg = (uint32_t)page < a.n_pages ? (uint32_t)page : 0u;
-    return (((uint64_t)pg * a.kv_heads + kvh) << a.page_shift) + (key & pmask);
-  };
-  bool here[St::kPasses];
+  auto page_or_0 = [&](int32_t page) { return (uint32_t)page < a.n_pages ? (uint32_t)page : 0u; };   // (masked later)
+  uint32_t here = 0;   // bit p: pass p's row lies on a page of the cache
   auto load_rows = [&](int32_t kb) {
+    here = 0;
 #pragma unroll
     for (int p = 0; p < St::kPasses; ++p) {
       const uint32_t key = key_of(kb, prow + p * St::kRows);
       if constexpr (kPaged) {
-        here[p] = (uint32_t)st.page[p] < a.n_pages;
-        const uint64_t at = row_of(st.page[p], key) * (D * (kInt8 ? 1 : 2)) + 16 * ppiece;
-        st.k[p] = *reinterpret_cast<const u32x4_t*>(a.cache + at);
-        st.v[p] = *reinterpret_cast<const u32x4_t*>(a.cache + a.off_v + at);
+        here |= ((uint32_t)st.page[p] < a.n_pages ? 1u : 0u) << p;
+        const uint64_t at = (uint64_t)page_or_0(st.page[p]) * page_bytes + (key & pmask) * (D * kElem);
+        st.k[p] = *reinterpret_cast<const u32x4_t*>(kbase + at);
+        st.v[p] = *reinterpret_cast<const u32x4_t*>(vbase + at);
       } else {
-        const uint64_t at = (uint64_t)(q.first + (int32_t)key);
-        st.k[p] = *reinterpret_cast<const u32x4_t*>(a.k + at * a.ldk + kvh * D + 8 * ppiece);
-        st.v[p] = *reinterpret_cast<const u32x4_t*>(a.v + at * a.ldv + kvh * D + 8 * ppiece);
+        st.k[p] = *reinterpret_cast<const u32x4_t*>(kbase + 2 * ((uint64_t)key * (uint32_t)a.ldk));
+        st.v[p] = *reinterpret_cast<const u32x4_t*>(vbase + 2 * ((uint64_t)key * (uint32_t)a.ldv));
       }
     }
     if constexpr (kInt8) {
-      if (wave < 2)
-        st.scale = reinterpret_cast<const float*>(a.cache + (wave ? a.off_vs : a.off_ks))[row_of(st.page_scale, key_of(kb, lane))];
+      if (wave < 2) {
+        const uint64_t row = (uint64_t)page_or_0(st.page_scale) * (a.kv_heads << a.page_shift) + (kvh << a.page_shift) +
+                             (key_of(kb, lane) & pmask);
+        st.scale = reinterpret_cast<const float*>(a.cache + (wave ? a.off_vs : a.off_ks))[row];
+        if ((uint32_t)st.page_scale >= a.n_pages) st.scale = 0.f;
+      }
     }
   };
-  auto store_rows = [&](int b) {
+  auto store_rows = [&](int b, int32_t kb) {
+    bool any = false;
+    const bool at_edge = kb + kKeys - 1 > edge;
 #pragma unroll
     for (int p = 0; p < St::kPasses; ++p) {
       const uint32_t row = prow + p * St::kRows;
@@ -187,11 +216,20 @@ __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_t
         }
       } else {
         *reinterpret_cast<u32x4_t*>(kd + 16 * k_piece<D>(row, ppiece)) = st.k[p];
+        if (at_edge) st.v[p] = finite_piece(st.v[p], any);
+        if (kPaged && !(here >> p & 1)) st.v[p] = u32x4_t{0, 0, 0, 0};
         *reinterpret_cast<u32x4_t*>(vd + 16 * v_piece<D>(row, ppiece)) = st.v[p];
       }
-      if (kPaged && ppiece == 0 && (row & 15) == 0) there[b][row >> 4] = here[p];
+      if (kPaged && ppiece == 0 && (row & 15) == 0) there[b][row >> 4] = here >> p & 1;
     }
-    if (kInt8 && wave < 2) ssh[b][wave][lane] = st.scale;
+    if (kInt8 && wave < 2) {
+      if (wave == 1 && !(fabsf(st.scale) < INFINITY) && at_edge) {
+        any = true;
+        st.scale = 0.f;
+      }
+      ssh[b][wave][lane] = st.scale;
+    }
+    if (any) odd[b] = kb + 1;   // the tile's mark: nothing to clear
   };
 
   // LDS addresses of the wavefront's operands
@@ -216,114 +254,140 @@ __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_t
       for (int i = 0; i < 16; ++i) o[t][x][i] = 0.f;
   }
 
+  auto compute = [&](int b, int32_t kb) {
+    bool full = kb + kKeys - 1 <= wave_first;
+    if constexpr (kPaged) full = full && there[b][0] && there[b][1] && there[b][2] && there[b][3];
+    f32x16_t x[QT][2];
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[t][h][i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bf16x8_t kf = as_bf16x8(*reinterpret_cast<const u32x4_t*>(&ksh[b][kat[d] + 32 * h * kRowBytes]));
+#pragma unroll
+        for (int t = 0; t < QT; ++t) x[t][h] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[t][d], x[t][h], 0, 0, 0);
+      }
+    // value i of x belongs to key 16 (i / 8) + 8 hh + i % 8 of the tile
+    if constexpr (kInt8) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&ssh[b][0][16 * (i >> 3) + (i & 7) + 8 * hh]);
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[t][i >> 4][(i & 15) + u] *= ks[u];
+      }
+    }
+    if (__builtin_amdgcn_readfirstlane(!full)) {
+      uint32_t pages = 0xFu;
+      if constexpr (kPaged) pages = (there[b][0] ? 1u : 0u) | (there[b][1] ? 2u : 0u) | (there[b][2] ? 4u : 0u) | (there[b][3] ? 8u : 0u);
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        const int32_t most = last[t] - kb - 8 * (int32_t)hh;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int32_t upto = pages >> g & 1 ? most - 16 * g : -1;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[t][g >> 1][8 * (g & 1) + i] = i <= upto ? x[t][g >> 1][8 * (g & 1) + i] : -INFINITY;
+        }
+      }
+    }
+    u32x4_t pf[QT][4];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      float top = kNoMax;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) top = fmaxf(top, x[t][i >> 4][i & 15]);
+      top *= a.scale;
+      if (__any(top > m[t] + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m[t], top), f = __builtin_amdgcn_exp2f(m[t] - mn);
+        m[t] = mn;
+        l[t] *= f;
+#pragma unroll
+        for (int e = 0; e < kMT; ++e) o[t][e] *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        float y[4];
+        f32x4_t vs;
+        if constexpr (kInt8) vs = *reinterpret_cast<const f32x4_t*>(&ssh[b][1][16 * (i >> 3) + (i & 7) + 8 * hh]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          y[u] = __builtin_amdgcn_exp2f(fmaf(x[t][i >> 4][(i & 15) + u], a.scale, -m[t]));
+          l[t] += y[u];
+          if constexpr (kInt8) y[u] *= vs[u];
+        }
+        pf[t][i >> 3][(i & 7) >> 1] = pack_bf16(y[0], y[1]);
+        pf[t][i >> 3][((i & 7) >> 1) + 1] = pack_bf16(y[2], y[3]);
+      }
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int e = 0; e < kMT; ++e) {
+        union { s16x4_t h[2]; u32x4_t w; } vf;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          vf.h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4_t*)(&vsh[b][vat[e] + (16 * ks + 4 * u) * kRowBytes]));
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          o[t][e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf.w), as_bf16x8(pf[t][ks]), o[t][e], 0, 0, 0);
+      }
+    if (__builtin_amdgcn_readfirstlane(odd[b] == kb + 1)) {
+      // each row takes the infinities and NaN of the keys that it sees, and of those only (from memory: it is rare)
+      for (int32_t j = 0; j < kKeys && kb + j < kend; ++j) {
+        if (kPaged && !there[b][j >> 4]) continue;
+        const uint32_t key = (uint32_t)(kb + j);
+        const uint8_t* p;
+        uint64_t row = 0;
+        if constexpr (kPaged) {
+          row = (uint64_t)page_or_0(tab[key >> a.page_shift]) * (a.kv_heads << a.page_shift) + (kvh << a.page_shift) + (key & pmask);
+          p = a.cache + a.off_v + row * (D * kElem);
+        } else {
+          p = reinterpret_cast<const uint8_t*>(a.v + (uint64_t)(q.first + (int32_t)key) * a.ldv + kvh * D);
+        }
+        float vs = 0.f;
+        if constexpr (kInt8) vs = reinterpret_cast<const float*>(a.cache + a.off_vs)[row];
+#pragma unroll
+        for (int e = 0; e < kMT; ++e)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t d = 32 * e + 8 * (i >> 2) + 4 * hh + (i & 3);
+            float y;
+            if constexpr (kInt8) y = vs;
+            else y = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[d] << 16);
+            y = fabsf(y) < INFINITY ? 0.f : y;
+#pragma unroll
+            for (int t = 0; t < QT; ++t) o[t][e][i] += kb + j <= last[t] ? y : 0.f;
+          }
+      }
+    }
+  };
+
+  if (tid < 2) odd[tid] = 0;
+  __syncthreads();
   if (k0 < kend) {
     load_pages(k0);
     load_rows(k0);
     load_pages(k0 + kKeys);
-    store_rows(0);
+    store_rows(0, k0);
     load_rows(k0 + kKeys);
     load_pages(k0 + 2 * kKeys);
   }
   __syncthreads();
   int b = 0;
   for (int32_t kb = k0; kb < kend; kb += kKeys, b ^= 1) {
-    if (kb <= wave_last) {
-      bool full = kb + kKeys - 1 <= wave_first;
-      if constexpr (kPaged) full = full && there[b][0] && there[b][1] && there[b][2] && there[b][3];
-      f32x16_t x[QT][2];
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[t][h][i] = 0.f;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bf16x8_t kf = as_bf16x8(*reinterpret_cast<const u32x4_t*>(&ksh[b][kat[d] + 32 * h * kRowBytes]));
-#pragma unroll
-          for (int t = 0; t < QT; ++t) x[t][h] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[t][d], x[t][h], 0, 0, 0);
-        }
-      u32x4_t pf[QT][4];
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        float top = kNoMax;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float y = x[t][i >> 4][i & 15];
-          const int key = 16 * (i >> 3) + (i & 7);   // and 8 hh
-          if constexpr (kInt8) y *= ssh[b][0][key + 8 * hh] * a.scale;
-          else y *= a.scale;
-          if (!full) {
-            bool ok = kb + key + 8 * (int32_t)hh <= last[t];
-            if constexpr (kPaged) ok = ok && there[b][i >> 3];
-            y = ok ? y : -INFINITY;
-          }
-          x[t][i >> 4][i & 15] = y;
-          top = fmaxf(top, y);
-        }
-        if (__any(top > m[t] + kSlack)) {
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float mn = fmaxf(m[t], top), f = __builtin_amdgcn_exp2f(m[t] - mn);
-          m[t] = mn;
-          l[t] *= f;
-#pragma unroll
-          for (int e = 0; e < kMT; ++e) o[t][e] *= f;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float y[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float z = x[t][i >> 4][(i & 15) + u];
-            y[u] = __builtin_amdgcn_exp2f(z - m[t]);
-            l[t] += y[u];
-            if constexpr (kInt8) {
-              const float vs = ssh[b][1][16 * (i >> 3) + (i & 7) + u + 8 * hh];
-              y[u] = full || z != -INFINITY ? y[u] * vs : 0.f;
-            }
-          }
-          pf[t][i >> 3][(i & 7) >> 1] = pack_bf16(y[0], y[1]);
-        }
-      }
-      bool odd = false;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int e = 0; e < kMT; ++e) {
-          union { s16x4_t h[2]; u32x4_t w; } vf;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            vf.h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t*)(&vsh[b][vat[e] + (16 * ks + 4 * u) * kRowBytes]));
-          if (!kInt8 && !full) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) vf.w[u] = finite_pair(vf.w[u], odd);
-          }
-#pragma unroll
-          for (int t = 0; t < QT; ++t)
-            o[t][e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf.w), as_bf16x8(pf[t][ks]), o[t][e], 0, 0, 0);
-        }
-      if (!kInt8 && __any(odd)) {
-        // each row takes the infinities and NaN of the keys that it sees, and of those only
-        for (int32_t j = 0; j < kKeys; ++j) {
-          if (kb + j >= kend || (kPaged && !there[b][j >> 4])) continue;
-#pragma unroll
-          for (int e = 0; e < kMT; ++e)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t d = 32 * e + 8 * (i >> 2) + 4 * hh + (i & 3);
-              const uint32_t w = *reinterpret_cast<const uint16_t*>(&vsh[b][j * kRowBytes + 16 * v_piece<D>(j, d >> 3) + 2 * (d & 7)]);
-#pragma unroll
-              for (int t = 0; t < QT; ++t)
-                if ((w & 0x7F80u) == 0x7F80u && kb + j <= last[t]) o[t][e][i] += __uint_as_float(w << 16);
-            }
-        }
-      }
-    }
+    if (kb <= wave_last) compute(b, kb);
     if (kb + kKeys < kend) {
-      store_rows(b ^ 1);
+      store_rows(b ^ 1, kb + kKeys);
       if (kb + 2 * kKeys < kend) {
         load_rows(kb + 2 * kKeys);
         load_pages(kb + 3 * kKeys);
