@@ -177,11 +177,22 @@ def _c(a, dtype):
     return None if a is None else np.ascontiguousarray(a, dtype=dtype)
 
 
+_raw_stream = None
+
+
 def _stream(stream=None) -> Optional[int]:
+    """The given stream, or torch's current one on its current device."""
+    global _raw_stream
     if stream is not None:
         return int(stream)
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        import torch
+        of, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if of is None or device is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:   # the same number without building a Stream object, which costs as much as a launch
+            _raw_stream = lambda: of(device())  # noqa: E731
+    return _raw_stream()
 
 
 # ---------------------------------------------------------------------------
@@ -692,47 +703,97 @@ def wal_rope_freqs(desc: wal_rope_desc):
     return turns, m.value
 
 
-def _vec(t, name: str, dtype, n: int):
-    """A contiguous 1-D device vector of at least n elements; an empty one counts too."""
-    _dev(t, name, (dtype,), n)
-    if t.dim() != 1:
+# These calls run once per layer and token, a few microseconds on the GPU each, so
+# their checks are written out flat: one pass over each tensor's attributes.
+class _Types:
+    """torch's types, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.tensor, self.bf16, self.i32, self.i64 = torch.Tensor, torch.bfloat16, torch.int32, torch.int64
+        self.acts, self.only_bf16 = (torch.bfloat16, torch.float32), (torch.bfloat16,)
+        self.only_i32 = (torch.int32,)
+
+
+_types_made = None
+
+
+def _types() -> _Types:
+    global _types_made
+    if _types_made is None:
+        _types_made = _Types()
+    return _types_made
+
+
+def _mat(T, t, name: str, dtypes, cols: int, rows: int = 0):
+    """A 2-D device matrix of one of the dtypes with at least so many columns
+    and rows, unit stride along its rows, rows apart: (rows, columns, row pitch)."""
+    if not isinstance(t, T.tensor):
+        raise TypeError(f"{name} must be a torch tensor on the GPU, not {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected one of {[str(d) for d in dtypes]}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D [rows][ld]")
+    n, c = shape
+    if c < cols:
+        raise ValueError(f"{name} has {c} columns; at least {cols} are needed")
+    if n < rows:
+        raise ValueError(f"{name} has {n} rows; at least {rows} are needed")
+    ld, step = t.stride()
+    if step != 1 and c > 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    if n <= 1:
+        ld = c if ld < c else ld   # the pitch of an only row means nothing
+    elif ld < c:
+        raise ValueError(f"{name} rows overlap (stride {ld} < {c})")
+    return n, c, ld
+
+
+def _vec(T, t, name: str, dtype, n: int) -> int:
+    """A contiguous 1-D device vector of at least n elements: its length."""
+    if not isinstance(t, T.tensor):
+        raise TypeError(f"{name} must be a torch tensor on the GPU, not {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    shape = t.shape
+    if len(shape) != 1:
         raise ValueError(f"{name} must be 1-D")
-    return t
+    if shape[0] < n:
+        raise ValueError(f"{name} holds {shape[0]} elements; at least {n} are needed")
+    if shape[0] > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    return shape[0]
 
 
-def _ld(t) -> int:
-    """Row pitch of a 2-D tensor (of its only row: its width)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _whole_heads(cols: int, name: str, head_dim: int) -> int:
+    if head_dim < 1 or cols % head_dim or not cols:
+        raise ValueError(f"{name} has {cols} columns, not a multiple of head_dim {head_dim}")
+    return cols // head_dim
 
 
-def _rotary(pos, turns, n: int, layout: int, magnitude: float) -> wal_rotary:
-    torch = _torch()
-    _vec(pos, "pos", torch.int32, n)
-    _vec(turns, "turns", torch.int64, 1)
-    return wal_rotary(_ptr(turns), _ptr(pos), 2 * turns.numel(), layout, magnitude)
-
-
-def _heads(t, name: str, head_dim: int) -> int:
-    if head_dim < 1 or t.shape[1] % head_dim or not t.shape[1]:
-        raise ValueError(f"{name} has {t.shape[1]} columns, not a multiple of head_dim {head_dim}")
-    return t.shape[1] // head_dim
+def _rotary(T, pos, turns, n: int, layout: int, magnitude: float) -> wal_rotary:
+    _vec(T, pos, "pos", T.i32, n)
+    pairs = _vec(T, turns, "turns", T.i64, 1)
+    return wal_rotary(turns.data_ptr(), pos.data_ptr(), 2 * pairs, layout, magnitude)
 
 
 def wal_rope(X, out, pos, turns, head_dim: int, layout=WAL_ROPE_HALF, magnitude: float = 1.0, stream=None):
     """out = X [n][heads * head_dim] with every head rotated at its row's
     position; pos int32 [n], turns int64 [rot_dim / 2] (wal_rope_freqs); bf16
     or fp32 device tensors, out may be X itself."""
-    torch = _torch()
-    acts = (torch.bfloat16, torch.float32)
-    _rows(X, "X", acts, head_dim)
-    heads = _heads(X, "X", head_dim)
-    _rows(out, "out", acts, X.shape[1], X.shape[0])
-    r = _rotary(pos, turns, X.shape[0], layout, magnitude)
-    _gpu(X=X, out=out, pos=pos, turns=turns)
-    if not X.shape[0]:   # an empty tensor has no address: nothing to do
-        return out
-    _check(_lib.wal_rope(_ptr(X), _xdtype(X), X.shape[0], heads, head_dim, _ld(X), ctypes.byref(r), _ptr(out),
-                         _xdtype(out), _ld(out), _stream(stream)), "wal_rope")
+    T = _types()
+    n, cols, ldx = _mat(T, X, "X", T.acts, head_dim)
+    heads = _whole_heads(cols, "X", head_dim)
+    _, _, ldo = _mat(T, out, "out", T.acts, cols, n)
+    r = _rotary(T, pos, turns, n, layout, magnitude)
+    if not (X.is_cuda and out.is_cuda and pos.is_cuda and turns.is_cuda):
+        _gpu(X=X, out=out, pos=pos, turns=turns)
+    if n:   # an empty tensor has no address: nothing to do
+        st = _lib.wal_rope(X.data_ptr(), X.dtype is T.bf16, n, heads, head_dim, ldx, r, out.data_ptr(),
+                           out.dtype is T.bf16, ldo, _stream(stream))
+        if st:
+            _check(st, "wal_rope")
     return out
 
 
@@ -747,9 +808,22 @@ def wal_kv_size(desc: wal_kv_desc) -> wal_kv_info:
     return info
 
 
-def _kv_cache(desc: wal_kv_desc, cache):
-    _dev_bytes(cache, "cache", int(wal_kv_size(desc).total_bytes))
-    return desc.kv_heads * desc.head_dim
+def _kv_cache(T, desc: wal_kv_desc, cache):
+    """The cache's buffer, as large as its descriptor says (whose other
+    limits the library checks): the width of a token's keys."""
+    width = desc.kv_heads * desc.head_dim
+    tokens = desc.n_pages * desc.page_size
+    int8 = desc.fmt == WAL_KV_INT8
+    need = 2 * (-(-(tokens * width * (1 if int8 else 2)) // 256) * 256)
+    if int8:
+        need += 2 * (-(-(tokens * desc.kv_heads * 4) // 256) * 256)
+    if not isinstance(cache, T.tensor):
+        raise TypeError(f"cache must be a torch tensor on the GPU, not {type(cache).__name__}")
+    if cache.numel() * cache.element_size() < need:
+        raise ValueError(f"cache holds {cache.numel() * cache.element_size()} bytes; at least {need} are needed")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    return width
 
 
 def wal_kv_write(desc: wal_kv_desc, cache, slots, K, V, pos=None, turns=None, layout=WAL_ROPE_HALF,
@@ -757,50 +831,55 @@ def wal_kv_write(desc: wal_kv_desc, cache, slots, K, V, pos=None, turns=None, la
     """Writes K, V [n][kv_heads * head_dim] (bf16 or fp32) to the cache's slots
     [n] (int32).  With pos and turns the keys are rotated first, and Q, when
     given, is rotated into Q_out (bf16)."""
-    torch = _torch()
-    acts = (torch.bfloat16, torch.float32)
-    width = _kv_cache(desc, cache)
-    _rows(K, "K", acts, width)
-    n = K.shape[0]
-    _rows(V, "V", (K.dtype,), width, n)
-    _vec(slots, "slots", torch.int32, n)
+    T = _types()
+    width = _kv_cache(T, desc, cache)
+    n, _, ldk = _mat(T, K, "K", T.acts, width)
+    same = (K.dtype,)
+    _, _, ldv = _mat(T, V, "V", same, width, n)
+    _vec(T, slots, "slots", T.i32, n)
     if (pos is None) != (turns is None):
         raise ValueError("pos and turns go together")
     if (Q is None) != (Q_out is None) or (Q is not None and pos is None):
         raise ValueError("Q needs Q_out, pos and turns")
-    r = None if pos is None else _rotary(pos, turns, n, layout, magnitude)
+    r = None if pos is None else _rotary(T, pos, turns, n, layout, magnitude)
     q_heads = ldq = ldqo = 0
+    q = q_out = None
     if Q is not None:
-        _rows(Q, "Q", (K.dtype,), desc.head_dim, n)
-        q_heads = _heads(Q, "Q", desc.head_dim)
-        _rows(Q_out, "Q_out", (torch.bfloat16,), Q.shape[1], n)
-        ldq, ldqo = _ld(Q), _ld(Q_out)
-    _gpu(cache=cache, slots=slots, K=K, V=V, pos=pos, turns=turns, Q=Q, Q_out=Q_out)
-    if not n:
-        return
-    _check(_lib.wal_kv_write(ctypes.byref(desc), _ptr(cache), _ptr(slots), n, _ptr(K), _ld(K), _ptr(V), _ld(V),
-                             _xdtype(K), None if r is None else ctypes.byref(r), _ptr(Q), q_heads, ldq, _ptr(Q_out),
-                             ldqo, _stream(stream)), "wal_kv_write")
+        _, cols, ldq = _mat(T, Q, "Q", same, desc.head_dim, n)
+        q_heads = _whole_heads(cols, "Q", desc.head_dim)
+        _, _, ldqo = _mat(T, Q_out, "Q_out", T.only_bf16, cols, n)
+        q, q_out = Q.data_ptr(), Q_out.data_ptr()
+    if not (cache.is_cuda and slots.is_cuda and K.is_cuda and V.is_cuda and (r is None or (pos.is_cuda and turns.is_cuda))
+            and (Q is None or (Q.is_cuda and Q_out.is_cuda))):
+        _gpu(cache=cache, slots=slots, K=K, V=V, pos=pos, turns=turns, Q=Q, Q_out=Q_out)
+    if n:
+        st = _lib.wal_kv_write(desc, cache.data_ptr(), slots.data_ptr(), n, K.data_ptr(), ldk, V.data_ptr(), ldv,
+                               K.dtype is T.bf16, r, q, q_heads, ldq, q_out, ldqo, _stream(stream))
+        if st:
+            _check(st, "wal_kv_write")
 
 
 def wal_kv_read(desc: wal_kv_desc, cache, slots, K=None, V=None, stream=None):
     """Reads the cache's slots [n] into K, V [n][kv_heads * head_dim] (bf16 or
     fp32; either may be None); returns (K, V)."""
-    torch = _torch()
-    width = _kv_cache(desc, cache)
+    T = _types()
+    width = _kv_cache(T, desc, cache)
     if K is None and V is None:
         raise ValueError("K or V must be given")
-    _vec(slots, "slots", torch.int32, 0)
-    n = slots.numel()
+    n = _vec(T, slots, "slots", T.i32, 0)
     first = K if K is not None else V
-    for t, name in ((K, "K"), (V, "V")):
-        if t is not None:
-            _rows(t, name, (torch.bfloat16, torch.float32) if t is first else (first.dtype,), width, n)
-    _gpu(cache=cache, slots=slots, K=K, V=V)
-    if not n:
-        return K, V
-    _check(_lib.wal_kv_read(ctypes.byref(desc), _ptr(cache), _ptr(slots), n, _ptr(K), 0 if K is None else _ld(K),
-                            _ptr(V), 0 if V is None else _ld(V), _xdtype(first), _stream(stream)), "wal_kv_read")
+    ldk = ldv = 0
+    if K is not None:
+        _, _, ldk = _mat(T, K, "K", T.acts, width, n)
+    if V is not None:
+        _, _, ldv = _mat(T, V, "V", T.acts if K is None else (first.dtype,), width, n)
+    if not (cache.is_cuda and slots.is_cuda and first.is_cuda and (V is None or V.is_cuda)):
+        _gpu(cache=cache, slots=slots, K=K, V=V)
+    if n:
+        st = _lib.wal_kv_read(desc, cache.data_ptr(), slots.data_ptr(), n, None if K is None else K.data_ptr(), ldk,
+                              None if V is None else V.data_ptr(), ldv, first.dtype is T.bf16, _stream(stream))
+        if st:
+            _check(st, "wal_kv_read")
     return K, V
 
 
@@ -819,26 +898,33 @@ def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=No
     bf16 [n][q_heads * head_dim], ws of wal_attn_paged_workspace_size bytes.
     scale: 1 / sqrt(head_dim) unless given; max_new and max_len bound the
     sequences' new tokens and lengths (max_len 0: what the tables hold)."""
-    torch = _torch()
-    _kv_cache(desc, cache)
-    _rows(tables, "tables", (torch.int32,), 1)
-    n_seqs = tables.shape[0]
-    _vec(lens, "lens", torch.int32, n_seqs)
-    _vec(starts, "starts", torch.int32, n_seqs + 1)
-    _rows(Q, "Q", (torch.bfloat16,), desc.head_dim)
-    n, q_heads = Q.shape[0], _heads(Q, "Q", desc.head_dim)
-    _rows(out, "out", (torch.bfloat16,), Q.shape[1], n)
-    max_len = max_len or tables.shape[1] * desc.page_size
-    if max_new < 0 or max_len < 0 or max_len > tables.shape[1] * desc.page_size:
-        raise ValueError(f"max_new {max_new}, max_len {max_len}: the tables hold {tables.shape[1] * desc.page_size}")
-    wsb = _ws_bytes(ws)
-    _gpu(cache=cache, tables=tables, lens=lens, starts=starts, Q=Q, out=out, ws=ws)
-    if not n or not n_seqs:
-        return out
-    _check(_lib.wal_attn_paged(ctypes.byref(desc), _ptr(cache), _ptr(tables), _ld(tables), _ptr(lens), _ptr(starts),
-                               n_seqs, n, max_new, max_len, _ptr(Q), q_heads, _ld(Q),
-                               desc.head_dim ** -0.5 if scale is None else scale, _ptr(out), _ld(out), _ptr(ws), wsb,
-                               _stream(stream)), "wal_attn_paged")
+    T = _types()
+    _kv_cache(T, desc, cache)
+    dim = desc.head_dim
+    n_seqs, pages, ldt = _mat(T, tables, "tables", T.only_i32, 1)
+    _vec(T, lens, "lens", T.i32, n_seqs)
+    _vec(T, starts, "starts", T.i32, n_seqs + 1)
+    n, cols, ldq = _mat(T, Q, "Q", T.only_bf16, dim)
+    q_heads = _whole_heads(cols, "Q", dim)
+    _, _, ldo = _mat(T, out, "out", T.only_bf16, cols, n)
+    holds = pages * desc.page_size
+    max_len = max_len or holds
+    if max_new < 0 or max_len < 0 or max_len > holds:
+        raise ValueError(f"max_new {max_new}, max_len {max_len}: the tables hold {holds}")
+    wsp, wsb = None, 0
+    if ws is not None:
+        wsb = _ws_bytes(ws)
+        wsp = ws.data_ptr()
+    if not (cache.is_cuda and tables.is_cuda and lens.is_cuda and starts.is_cuda and Q.is_cuda and out.is_cuda
+            and (ws is None or ws.is_cuda)):
+        _gpu(cache=cache, tables=tables, lens=lens, starts=starts, Q=Q, out=out, ws=ws)
+    if n and n_seqs:
+        st = _lib.wal_attn_paged(desc, cache.data_ptr(), tables.data_ptr(), ldt, lens.data_ptr(), starts.data_ptr(),
+                                 n_seqs, n, max_new, max_len, Q.data_ptr(), q_heads, ldq,
+                                 dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo, wsp, wsb,
+                                 _stream(stream))
+        if st:
+            _check(st, "wal_attn_paged")
     return out
 
 
@@ -847,22 +933,23 @@ def wal_attn_prompt(Q, K, V, starts, out, head_dim: int, max_len: int, scale: Op
     """out = attention over packed prompts: Q, out bf16 [n][q_heads * head_dim],
     K, V bf16 [n][kv_heads * head_dim], starts int32 [n_seqs + 1]; max_len
     bounds the sequences' lengths; scale as for wal_attn_paged."""
-    torch = _torch()
-    bf = (torch.bfloat16,)
-    _rows(Q, "Q", bf, head_dim)
-    n, q_heads = Q.shape[0], _heads(Q, "Q", head_dim)
-    _rows(K, "K", bf, head_dim, n)
-    kv_heads = _heads(K, "K", head_dim)
-    _rows(V, "V", bf, K.shape[1], n)
-    _rows(out, "out", bf, Q.shape[1], n)
-    _vec(starts, "starts", torch.int32, 1)
+    T = _types()
+    n, cols, ldq = _mat(T, Q, "Q", T.only_bf16, head_dim)
+    q_heads = _whole_heads(cols, "Q", head_dim)
+    _, kv_cols, ldk = _mat(T, K, "K", T.only_bf16, head_dim, n)
+    kv_heads = _whole_heads(kv_cols, "K", head_dim)
+    _, _, ldv = _mat(T, V, "V", T.only_bf16, kv_cols, n)
+    _, _, ldo = _mat(T, out, "out", T.only_bf16, cols, n)
+    n_seqs = _vec(T, starts, "starts", T.i32, 1) - 1
     if max_len < 0:
         raise ValueError(f"max_len {max_len}")
-    _gpu(Q=Q, K=K, V=V, starts=starts, out=out)
-    if not n:
-        return out
-    _check(_lib.wal_attn_prompt(_ptr(Q), _ld(Q), _ptr(K), _ld(K), _ptr(V), _ld(V), _ptr(starts), starts.numel() - 1,
-                                n, max_len, q_heads, kv_heads, head_dim,
-                                head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, _ptr(out), _ld(out),
-                                _stream(stream)), "wal_attn_prompt")
+    if not (Q.is_cuda and K.is_cuda and V.is_cuda and starts.is_cuda and out.is_cuda):
+        _gpu(Q=Q, K=K, V=V, starts=starts, out=out)
+    if n:
+        st = _lib.wal_attn_prompt(Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, starts.data_ptr(), n_seqs,
+                                  n, max_len, q_heads, kv_heads, head_dim,
+                                  head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, out.data_ptr(),
+                                  ldo, _stream(stream))
+        if st:
+            _check(st, "wal_attn_prompt")
     return out
