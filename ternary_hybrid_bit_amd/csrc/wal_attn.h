@@ -38,6 +38,11 @@ constexpr uint32_t kMaxSplit = 4096;   // keys of a workgroup of attn_stream: it
 // Query rows of a key/value head that attn_stream takes: two tiles of 16, one where two would not fit in registers.
 constexpr uint32_t stream_rows(uint32_t dim) { return dim == 256 ? 16 : 32; }
 
+// Few short sequences with one tile of rows: eight wavefronts to a workgroup instead of four, and no split.
+constexpr bool stream_wide(uint32_t n_seqs, uint32_t kv_heads, uint32_t max_len) {
+  return max_len <= 1024 && (uint64_t)n_seqs * kv_heads <= 256;
+}
+
 // Launches (wal_status).  attn_stream: rows of each key/value head <= 16 tiles, tiles 1 or 2;
 // attn_join adds what it wrote when a.n_splits > 1.
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream);
@@ -99,11 +104,12 @@ __device__ __forceinline__ u32x2_t codes_to_bf16(uint32_t w) {
                  __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u)};
 }
 
-// A pair of bf16 with infinities and NaN replaced by zero; any: set if there was one.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& any) {
-  const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
-  any |= lo || hi;
-  return (lo ? 0u : w & 0xFFFFu) | (hi ? 0u : w & 0xFFFF0000u);
+// A pair of bf16 with infinities and NaN replaced by zero; odd: not 0 if there was one.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, uint32_t& odd) {
+  // 0xFFFF in the halves whose exponent is all ones
+  const uint32_t e = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u, f = (e >> 15) * 0xFFFFu;
+  odd |= f;
+  return w & ~f;
 }
 
 }  // namespace

@@ -28,10 +28,19 @@ struct Plan {
 };
 
 // The context is split when the workgroups of whole contexts leave compute units
-// idle.  Few rows: into enough pieces for four workgroups on each unit, not
-// below 256 keys a piece (its first loads), not above what a workgroup's
-// page list holds.  Many rows: two workgroups a unit, not below 512 keys, so that
-// the partial results stay small beside the products.
+// idle, or, over several sequences of lengths that the host does not know,
+// would leave them waiting for the longest.
+//  * Few rows, one sequence: two workgroups for each unit, not below 256 keys a
+//    piece (131,001 bf16 tokens, 8 key/value heads: 96 us and 5 us for the joining at 512
+//    pieces, 97 + 6 at 1024, 102 + 12 at 4096).
+//  * Few rows, several sequences: pieces of a twelfth of a workgroup slot's share, not
+//    below 512 keys (64 sequences up to 8192, int8: 97 us at 768 keys a piece, 100 at
+//    1024, 107 at 2048, 115 at 4096, 101 at 512).
+//  * Many rows: two workgroups a unit, not below 512 keys, so that the partial
+//    results stay small beside the products.
+// A piece of attn_stream is never above what a workgroup's page list holds.
+// Few short sequences are not split at all (517 tokens: 9.1 us with eight
+// wavefronts a workgroup, 6.5 + 3.0 us and a launch in pieces of 256 keys).
 Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n, uint32_t max_new,
              uint32_t max_len) {
   Plan p{};
@@ -42,7 +51,9 @@ Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n
   p.split = p.stream ? kMaxSplit : max_len;
   if (!rows || !n_seqs || !max_len || !n) return p;
   const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->head_dim)) * d->kv_heads;
-  const uint64_t target = p.stream ? 1024 : 512, least = p.stream ? 256 : 512;
+  if (p.stream && rows <= 16 && stream_wide(n_seqs, d->kv_heads, max_len)) return p;
+  const bool even = !p.stream || n_seqs == 1;
+  const uint64_t target = even ? 512 : 6144, least = p.stream && even ? 256 : 512;
   const uint64_t want = (target + items - 1) / items;
   uint64_t split = ((max_len + want - 1) / want + 127) / 128 * 128;
   if (split < least) split = least;
@@ -50,6 +61,10 @@ Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n
   p.split = (uint32_t)split;
   p.n_splits = (uint32_t)((max_len + split - 1) / split);
   if (p.n_splits == 1) return p;
+  // Workgroups go to the shader engines in turn: with an even number of splits
+  // to a sequence some engines would get the ends of the contexts again and again,
+  // where shorter sequences have nothing to do.
+  if (n_seqs > 1) p.n_splits |= 1;
   p.part_rows = (uint32_t)rows;
   const uint64_t slots = (uint64_t)n_seqs * d->kv_heads * p.n_splits * rows;
   p.off_ml = slots * d->head_dim * 4;

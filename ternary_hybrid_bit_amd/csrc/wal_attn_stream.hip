@@ -88,6 +88,19 @@ __device__ __forceinline__ void load_v(Tile<FMT, D>& t, const Attn& a, const int
   if constexpr (FMT == kPagedInt8) load_bytes<32>(reinterpret_cast<uint32_t*>(t.vs), a.cache + a.off_vs + 4 * r);
 }
 
+// Keeps what is computed from loaded registers behind this point: hoisted to
+// just after the loads it would wait for them there.
+template <int N>
+__device__ __forceinline__ void here(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
+}
+template <int N>
+__device__ __forceinline__ void here(u32x4_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
+}
+
 // V^T as the A operand of element e: keys 8 c .. 8 c + 7 of dim E (lane & 15) + e.
 template <int FMT, int D>
 __device__ __forceinline__ bf16x8_t v_operand(const Tile<FMT, D>& t, int e) {
@@ -107,14 +120,19 @@ __device__ __forceinline__ bf16x8_t v_operand(const Tile<FMT, D>& t, int e) {
   return as_bf16x8(w);
 }
 
+// Wavefronts a SIMD that the register allocator aims at.
+constexpr int stream_waves(int dim, int tiles) {
+  return dim * tiles <= 128 ? 3 : 2;
+}
+
 template <int FMT, int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
+__global__ __launch_bounds__(64 * NW, stream_waves(D, NT)) void k_attn_stream(Attn a) {
   constexpr int E = D / 16;
   constexpr bool kInt8 = FMT == kPagedInt8;
   __shared__ int64_t groups[kMaxSplit / 16 + 2];
   __shared__ float osh[NW][16][D + 4];
   __shared__ float msh[NW][16], lsh[NW][16];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, c = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, c = lane >> 4;
   const uint32_t kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
   const uint32_t sp = rest % a.n_splits, s = rest / a.n_splits;
   const Seq q = seq_of(a, s, true);
@@ -173,7 +191,9 @@ __global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
   for (; g < g_end; g += 2 * NW) {
     const int32_t kb = k0 + 16 * (int32_t)g;
     const bool there = groups[g + (c >> 1)] >= 0;
-    const bool full = kb + 31 <= q.old && __all(there);
+    const bool full = __builtin_amdgcn_readfirstlane(kb + 31 <= q.old && __all(there));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) here(kv.k[h]);
     f32x4_t x[NT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -193,29 +213,37 @@ __global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
           x[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), qf[t][st], x[t][h], 0, 0, 0);
       }
     }
-    float ks[8];
+    if constexpr (kInt8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ks[i] = kInt8 ? kv.ks[kInt8 ? i : 0] * a.scale : a.scale;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[t][i / 4][i % 4] *= kv.ks[i];
+    }
     const bool more = g + 2 * NW < g_end;
     if (more) load_k<FMT, D>(kv, a, groups, g + 2 * NW, lane);
 
-    bool odd = false;   // an infinity or NaN among the values of a tile that some row sees only in part
-    if (!kInt8 && !full) {
+    uint32_t odd = 0;   // an infinity or NaN among the values of a tile that some row sees only in part
+    if (!full) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int t = 0; t < NT; ++t) {
+        const int32_t upto = there ? last[t] - kb - 8 * (int32_t)c : -1;
 #pragma unroll
-        for (int e = 0; e < (int)(sizeof(kv.v[0]) / 4); ++e) kv.v[i][e] = finite_pair(kv.v[i][e], odd);
+        for (int i = 0; i < 8; ++i) x[t][i / 4][i % 4] = i <= upto ? x[t][i / 4][i % 4] : -INFINITY;
+      }
+      if constexpr (!kInt8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < (int)(sizeof(kv.v[0]) / 4); ++e) kv.v[i][e] = finite_pair(kv.v[i][e], odd);
+      }
     }
     bf16x8_t pf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float y[8], top = kNoMax;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = x[t][i / 4][i % 4] * ks[i];
-        if (!full) y[i] = there && kb + 8 * (int32_t)c + i <= last[t] ? y[i] : -INFINITY;
-        top = fmaxf(top, y[i]);
-      }
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, x[t][i / 4][i % 4]);
+      top *= a.scale;
       if (__any(top > m[t] + kSlack)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -228,21 +256,29 @@ __global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
       u32x4_t w;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        y[i] = __builtin_amdgcn_exp2f(y[i] - m[t]);
+        y[i] = __builtin_amdgcn_exp2f(fmaf(x[t][i / 4][i % 4], a.scale, -m[t]));
         l[t] += y[i];
-        if constexpr (kInt8) y[i] = full || (there && kb + 8 * (int32_t)c + i <= last[t]) ? y[i] * kv.vs[i] : 0.f;
+      }
+      if constexpr (kInt8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float z = y[i] * kv.vs[i];
+          y[i] = y[i] == 0.f ? 0.f : z;   // a key that is not seen, whatever its scale
+        }
       }
 #pragma unroll
       for (int p = 0; p < 4; ++p) w[p] = pack_bf16(y[2 * p], y[2 * p + 1]);
       pf[t] = as_bf16x8(w);
     }
 #pragma unroll
+    for (int i = 0; i < 8; ++i) here(kv.v[i]);
+#pragma unroll
     for (int e = 0; e < E; ++e) {
       const bf16x8_t vf = v_operand<FMT, D>(kv, e);
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[t], o[t][e], 0, 0, 0);
     }
-    if (!kInt8 && __any(odd)) {
+    if (!kInt8 && !full && __any(odd != 0)) {
       // each row takes the infinities and NaN of the keys that it sees, and of those only
       for (int32_t j = 0; j < 32; ++j) {
         const int64_t row = groups[g + (j >> 4)];
@@ -305,52 +341,88 @@ __global__ __launch_bounds__(64 * NW) void k_attn_stream(Attn a) {
   }
 }
 
-// The splits' sums of one row: 256 threads, dim / 4 of them to a split.
-template <int D>
+// The splits' sums of a row, added in the order of the splits (of kGroups strided parts of
+// them, then of the parts): dim / 4 lanes to a row and part, 256 threads.  Many rows:
+// one part, several rows to a workgroup; few rows: one row, several parts.
+template <int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(Attn a) {
-  constexpr uint32_t kLanes = D / 4, kAtOnce = 256 / kLanes;
-  __shared__ f32x4_t osh[kAtOnce][kLanes];
-  __shared__ float lsh[kAtOnce];
-  const uint32_t t = blockIdx.x, h = blockIdx.y, kvh = h / a.group;
-  if (a.starts[0] > (int32_t)t || a.starts[a.n_seqs] <= (int32_t)t) return;
-  const uint32_t s = find_seq(a.starts, a.n_seqs, (int32_t)t);
+  constexpr uint32_t kLanes = D / 4, kGroups = 256 / kLanes / ROWS;
+  __shared__ f32x4_t osh[ROWS][kGroups][kLanes];
+  __shared__ float lsh[ROWS][kGroups], tsh[4];
+  const uint32_t lane = threadIdx.x % kLanes, part = threadIdx.x / kLanes % kGroups, mine = threadIdx.x / kLanes / kGroups;
+  const uint64_t row = (uint64_t)blockIdx.x * ROWS + mine;
+  const uint32_t t = (uint32_t)(row / a.q_heads), h = (uint32_t)(row - (uint64_t)t * a.q_heads), kvh = h / a.group;
+  const bool inside = t < a.n && a.starts[0] <= (int32_t)t && a.starts[a.n_seqs] > (int32_t)t;
+  const uint32_t s = inside ? find_seq(a.starts, a.n_seqs, (int32_t)t) : 0;
   const Seq q = seq_of(a, s, true);
   const int32_t i = (int32_t)t - q.first;
-  if (i < 0 || i >= q.rows) return;
-  const uint32_t r = (uint32_t)i * a.group + h - kvh * a.group;
-  const uint32_t splits = ((uint32_t)q.len + a.split - 1) / a.split;
+  const bool live = inside && i >= 0 && i < q.rows;
+  const uint32_t r = live ? (uint32_t)i * a.group + h - kvh * a.group : 0;
+  const uint32_t splits = live ? ((uint32_t)q.len + a.split - 1) / a.split : 0;
   const uint64_t step = (uint64_t)a.kv_heads * a.part_rows;
   const uint64_t slot = ((uint64_t)s * a.n_splits * a.kv_heads + kvh) * a.part_rows + r;
+  const float2* ml = a.part_ml + slot;
+  // the row's maximum
   float top = kNoMax;
-  for (uint32_t p = 0; p < splits; ++p) top = fmaxf(top, a.part_ml[slot + p * step].x);
-  const uint32_t lane = threadIdx.x % kLanes, mine = threadIdx.x / kLanes;
+  if constexpr (ROWS == 1) {
+    for (uint32_t p = threadIdx.x; p < splits; p += 256) top = fmaxf(top, ml[p * step].x);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if ((threadIdx.x & 63) == 0) tsh[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(tsh[0], tsh[1]), fmaxf(tsh[2], tsh[3]));
+  } else {
+    for (uint32_t p = lane; p < splits; p += kLanes) top = fmaxf(top, ml[p * step].x);
+#pragma unroll
+    for (int d = 1; d < (int)kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  }
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  for (uint32_t p = mine; p < splits; p += kAtOnce) {
-    const float2 ml = a.part_ml[slot + p * step];
-    const float f = __builtin_amdgcn_exp2f(ml.x - top);
-    sum += f * ml.y;
-    acc += f * *reinterpret_cast<const f32x4_t*>(a.part + (slot + p * step) * D + 4 * lane);
+  const float* from = a.part + slot * D + 4 * lane;
+  const uint64_t stride = step * D;
+#pragma unroll 4
+  for (uint32_t p = part; p < splits; p += kGroups) {
+    const float2 w = ml[p * step];
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(from + p * stride);
+    const float f = __builtin_amdgcn_exp2f(w.x - top);
+    sum += f * w.y;
+    acc += f * x;
   }
-  osh[mine][lane] = acc;
-  if (!lane) lsh[mine] = sum;
-  __syncthreads();
-  if (mine) return;
+  if constexpr (kGroups > 1) {
+    osh[mine][part][lane] = acc;
+    if (!lane) lsh[mine][part] = sum;
+    __syncthreads();
+    if (part) return;
 #pragma unroll
-  for (uint32_t w = 1; w < kAtOnce; ++w) {
-    acc += osh[w][lane];
-    sum += lsh[w];
+    for (uint32_t w = 1; w < kGroups; ++w) {
+      acc += osh[mine][w][lane];
+      sum += lsh[mine][w];
+    }
   }
+  if (!live) return;
   const float f = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<u32x2_t*>(a.out + (uint64_t)t * a.ldo + (uint64_t)h * D + 4 * lane) =
       u32x2_t{pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f)};
 }
 
+// Few rows up to twice the compute units' number.
+template <int D>
+void join(const Attn& a, hipStream_t s) {
+  constexpr int kMany = 1024 / D;
+  const uint64_t n = (uint64_t)a.n * a.q_heads;
+  if (n <= 512) hipLaunchKernelGGL((k_attn_join<D, 1>), dim3((uint32_t)n), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_attn_join<D, kMany>), dim3((uint32_t)((n + kMany - 1) / kMany)), dim3(256), 0, s, a);
+}
+
 template <int FMT, int D>
 void launch(const Attn& a, uint32_t tiles, hipStream_t s) {
-  const dim3 grid(a.n_splits * a.kv_heads * a.n_seqs), block(256);
-  if (tiles == 1) hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, 4>), grid, block, 0, s, a);
-  else if constexpr (stream_rows(D) > 16) hipLaunchKernelGGL((k_attn_stream<FMT, D, 2, 4>), grid, block, 0, s, a);
+  const dim3 grid(a.n_splits * a.kv_heads * a.n_seqs);
+  if (tiles == 1 && stream_wide(a.n_seqs, a.kv_heads, a.max_len))
+    hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, 8>), grid, dim3(512), 0, s, a);
+  else if (tiles == 1)
+    hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, 4>), grid, dim3(256), 0, s, a);
+  else if constexpr (stream_rows(D) > 16)
+    hipLaunchKernelGGL((k_attn_stream<FMT, D, 2, 4>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -373,10 +445,9 @@ int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* st
 
 int attn_join(const Attn& a, uint32_t dim, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(a.n, a.q_heads), block(256);
-  if (dim == 64) hipLaunchKernelGGL(k_attn_join<64>, grid, block, 0, s, a);
-  if (dim == 128) hipLaunchKernelGGL(k_attn_join<128>, grid, block, 0, s, a);
-  if (dim == 256) hipLaunchKernelGGL(k_attn_join<256>, grid, block, 0, s, a);
+  if (dim == 64) join<64>(a, s);
+  if (dim == 128) join<128>(a, s);
+  if (dim == 256) join<256>(a, s);
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
 

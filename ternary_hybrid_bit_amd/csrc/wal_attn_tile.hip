@@ -59,20 +59,6 @@ struct Stage {
   int32_t page_scale;
 };
 
-// 16 bytes of bf16 with infinities and NaN replaced by zero; any: whether there was one.
-__device__ __forceinline__ u32x4_t finite_piece(u32x4_t w, bool& any) {
-  uint32_t odd = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // 0xFFFF in the halves whose exponent is all ones
-    const uint32_t e = ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u, f = (e >> 15) * 0xFFFFu;
-    odd |= f;
-    w[i] &= ~f;
-  }
-  any = any || odd;
-  return w;
-}
-
 template <int KIND, int D, int QT, int NW>
 __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   using St = Stage<KIND, D, NW>;
@@ -199,7 +185,7 @@ __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_t
     }
   };
   auto store_rows = [&](int b, int32_t kb) {
-    bool any = false;
+    uint32_t any = 0;
     const bool at_edge = kb + kKeys - 1 > edge;
 #pragma unroll
     for (int p = 0; p < St::kPasses; ++p) {
@@ -216,7 +202,10 @@ __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_t
         }
       } else {
         *reinterpret_cast<u32x4_t*>(kd + 16 * k_piece<D>(row, ppiece)) = st.k[p];
-        if (at_edge) st.v[p] = finite_piece(st.v[p], any);
+        if (at_edge) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.v[p][i] = finite_pair(st.v[p][i], any);
+        }
         if (kPaged && !(here >> p & 1)) st.v[p] = u32x4_t{0, 0, 0, 0};
         *reinterpret_cast<u32x4_t*>(vd + 16 * v_piece<D>(row, ppiece)) = st.v[p];
       }
@@ -224,7 +213,7 @@ __global__ __launch_bounds__(64 * NW, QT == 1 && D <= 128 ? 2 : 1) void k_attn_t
     }
     if (kInt8 && wave < 2) {
       if (wave == 1 && !(fabsf(st.scale) < INFINITY) && at_edge) {
-        any = true;
+        any = 1;
         st.scale = 0.f;
       }
       ssh[b][wave][lane] = st.scale;
