@@ -678,8 +678,8 @@ int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const int32_t* t
 
 /* wal_attn_prompt: the same over whole prompts, packed one after another:
  * sequence s is rows starts[s] .. starts[s + 1] of q, k and v (all bf16, 16-byte
- * aligned rows of ldq, ldk, ldv elements, heads side by side; views of one
- * fused buffer are fine), each row sees its own sequence's rows up to itself
+ * aligned rows of ldq, ldk, ldv elements, heads side by side, ldk and ldv at
+ * most 2^26; views of one fused buffer are fine), each row sees its own sequence's rows up to itself
  * (causal) or all of them.  max_len bounds the sequences' lengths.
  * Errors: ARG, SHAPE, ALIGN, DEVICE. */
 int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk, const void* v_dev,

@@ -50,7 +50,7 @@ int attn_join(const Attn& a, uint32_t dim, void* stream);
 // Any number of rows; kind kPacked, kPagedBf16 or kPagedInt8.  attn_tiles: how many
 // tiles of query rows (workgroups of each key/value head and split) it launches.
 int attn_tile(const Attn& a, int kind, uint32_t dim, void* stream);
-uint64_t attn_tiles(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t dim);
+uint64_t attn_tiles(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t kv_heads, uint32_t dim);
 
 }  // namespace wal
 

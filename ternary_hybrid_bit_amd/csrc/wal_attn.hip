@@ -11,6 +11,7 @@ bool heads_ok(uint32_t q_heads, uint32_t kv_heads) {
 }
 
 constexpr uint32_t kMaxRows = 1u << 26;   // query rows, sequences and tokens of a call
+constexpr uint32_t kMaxPitch = 1u << 26;  // elements from a row of keys to the next: 16 rows in 32 bits of bytes
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The kernels multiply scores by a positive number only: masked ones are -infinity, so a
@@ -50,7 +51,7 @@ Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n
   p.n_splits = 1;
   p.split = p.stream ? kMaxSplit : max_len;
   if (!rows || !n_seqs || !max_len || !n) return p;
-  const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->head_dim)) * d->kv_heads;
+  const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->kv_heads, d->head_dim)) * d->kv_heads;
   if (p.stream && rows <= 16 && stream_wide(n_seqs, d->kv_heads, max_len)) return p;
   const bool even = !p.stream || n_seqs == 1;
   const uint64_t target = even ? 512 : 6144, least = p.stream && even ? 256 : 512;
@@ -155,7 +156,7 @@ extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_de
                                void* out_dev, uint32_t ldo, void* stream) {
   if (!starts_dev || !(scale - scale == 0.f)) return WAL_ERR_ARG;
   if (!heads_ok(q_heads, kv_heads) || kv_heads > 256 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
-      n_seqs > kMaxRows || n > kMaxRows || max_len > kMaxRows)
+      n_seqs > kMaxRows || n > kMaxRows || max_len > kMaxRows || ldk > kMaxPitch || ldv > kMaxPitch)
     return WAL_ERR_SHAPE;
   const uint64_t width = (uint64_t)q_heads * head_dim, kvw = (uint64_t)kv_heads * head_dim;
   int st;
