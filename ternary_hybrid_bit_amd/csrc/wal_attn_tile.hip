@@ -4,7 +4,7 @@
 // Bound by the matrix cores.  A workgroup takes 32 QT NW query rows of one key/value
 // head (a row is one token of one of the query heads that share the head, token by
 // token, so that the rows of a workgroup see nearly the same keys) and runs over
-// tiles of 64 keys, staged in LDS by all its wavefronts: from memory to registers
+// tiles of 64 keys (32 of wide heads), staged in LDS by all its wavefronts: from memory to registers
 // while the tile before is computed, from there to the other of two LDS
 // buffers (int8 codes become bf16, exactly, on the way).  As in the kernel
 // for few rows everything is transposed, so that a lane's scores belong to one
@@ -30,7 +30,8 @@
 namespace {
 
 constexpr float kSlack = 8.f;
-constexpr int kKeys = 64;
+// Keys of a tile: 64, or 32 where 64 of them would not leave room for the rows in registers.
+constexpr int tile_keys(int dim) { return dim > 128 ? 32 : 64; }
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
@@ -62,7 +63,14 @@ __device__ __forceinline__ bool find_work(const Attn& a, uint32_t tile_rows, uin
   const uint32_t rest = blockIdx.x / a.kv_heads;
   w.sp = rest % a.n_splits;
   uint32_t tile = rest / a.n_splits;
-  for (uint32_t base = 0;; base += 64) {
+  const int32_t group = (int32_t)a.group;
+  if (a.n_seqs == 1) {
+    w.s = 0;
+    w.q = seq_of(a, 0, PAGED);
+    const uint32_t own = (uint32_t)(w.q.rows * group + (int32_t)tile_rows - 1) / tile_rows;
+    if (tile >= own) return false;
+    tile = own - 1 - tile;
+  } else for (uint32_t base = 0;; base += 64) {
     if (base >= a.n_seqs) return false;
     uint32_t mine = 0;
     if (base + lane < a.n_seqs) mine = ((uint32_t)seq_of(a, base + lane, PAGED).rows * a.group + tile_rows - 1) / tile_rows;
@@ -83,8 +91,7 @@ __device__ __forceinline__ bool find_work(const Attn& a, uint32_t tile_rows, uin
     }
     tile -= (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
   }
-  w.q = seq_of(a, w.s, PAGED);
-  const int32_t group = (int32_t)a.group;
+  if (a.n_seqs > 1) w.q = seq_of(a, w.s, PAGED);
   w.nrows = w.q.rows * group;
   w.row0 = (int32_t)(tile * tile_rows);
   const int32_t row_end = min(w.row0 + (int32_t)tile_rows, w.nrows);
@@ -104,6 +111,7 @@ __device__ __forceinline__ bool find_work(const Attn& a, uint32_t tile_rows, uin
 template <int KIND, int D, int NW>
 struct Stage {
   static constexpr bool kInt8 = KIND == kPagedInt8, kPaged = KIND != kPacked;
+  static constexpr int kKeys = tile_keys(D);
   static constexpr uint32_t kElem = kInt8 ? 1 : 2;
   static constexpr uint32_t kPieces = D * kElem / 16;       // 16-byte pieces of a row in memory
   static constexpr uint32_t kWaveRows = 64 / kPieces, kRows = NW * kWaveRows;
@@ -177,22 +185,29 @@ struct Stage {
     const float s = reinterpret_cast<const float*>(a.cache + (wave ? a.off_vs : a.off_ks))[row];
     return on_page(page) ? s : 0.f;
   }
+  // A lane's place in a tile in LDS in pass 0; in pass p the row is p kRows further, which changes the exchange of K's
+  // pieces only if kRows is no multiple of 16.
   template <bool V>
-  __device__ __forceinline__ void put(uint8_t* tile, const u32x4_t (&r)[kPasses]) const {
+  __device__ __forceinline__ uint32_t place() const {
+    const uint32_t row = (uint32_t)wrow + lane / kPieces, piece = lane % kPieces * (kInt8 ? 2 : 1);
+    return row * kRowBytes + 16 * (V ? v_piece<D>(row, piece) : k_piece<D>(row, piece));
+  }
+  template <bool V>
+  __device__ __forceinline__ void put(uint8_t* tile, uint32_t at, const u32x4_t (&r)[kPasses]) const {
+    static_assert(D != 64 || kRows % 16 == 0, "rows of 64 elements share their exchange in pairs");
+    if (kSpare && wrow >= kKeys) return;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      const uint32_t row = (uint32_t)wrow + p * kRows + lane / kPieces, piece = lane % kPieces;
-      if (kSpare && row >= kKeys) return;
-      uint8_t* d = tile + row * kRowBytes;
+      uint8_t* d = tile + p * kRows * kRowBytes;
+      const uint32_t to = V ? at ^ 16 * (4 * (p * kRows % 4)) : at ^ 16 * (p * kRows % 16);
       if constexpr (kInt8) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const u32x2_t x = codes_to_bf16(r[p][2 * u]), y = codes_to_bf16(r[p][2 * u + 1]);
-          *reinterpret_cast<u32x4_t*>(d + 16 * (V ? v_piece<D>(row, 2 * piece + u) : k_piece<D>(row, 2 * piece + u))) =
-              u32x4_t{x[0], x[1], y[0], y[1]};
+          *reinterpret_cast<u32x4_t*>(d + (to ^ 16 * u)) = u32x4_t{x[0], x[1], y[0], y[1]};
         }
       } else {
-        *reinterpret_cast<u32x4_t*>(d + 16 * (V ? v_piece<D>(row, piece) : k_piece<D>(row, piece))) = r[p];
+        *reinterpret_cast<u32x4_t*>(d + to) = r[p];
       }
     }
   }
@@ -214,12 +229,12 @@ struct Stage {
       }
     }
   }
-  __device__ __forceinline__ void put_scale(float (*tile)[kKeys], int32_t* odd, float s, int32_t kb) const {
+  __device__ __forceinline__ void put_scale(float (*tile)[tile_keys(D)], int32_t* odd, float s, int32_t kb) const {
     if (wave == 1 && at_edge(kb) && !(fabsf(s) < INFINITY)) {
       s = 0.f;
       *odd = kb + 1;
     }
-    tile[wave][lane] = s;
+    if (lane < kKeys) tile[wave][lane] = s;
   }
 };
 
@@ -249,10 +264,10 @@ __device__ __forceinline__ void ahead() {
 template <int KIND, int D>
 struct Rows32 {
   static constexpr bool kInt8 = KIND == kPagedInt8, kPaged = KIND != kPacked;
-  static constexpr int kMT = D / 32, kRowBytes = 2 * D;
+  static constexpr int kKeys = tile_keys(D), kMT = D / 32, kRowBytes = 2 * D;
   bf16x8_t qf[D / 16];          // B operands: the rows
-  uint32_t pf[4][4];            // B operands: the weights of a tile
-  f32x16_t x[2], o[kMT];
+  uint32_t pf[kKeys / 16][4];   // B operands: the weights of a tile
+  f32x16_t x[kKeys / 32], o[kMT];
   float m, l;
   int32_t last, row;            // the last key that the lane's row sees; its row (below 0: none)
   int32_t first_sees, last_sees;   // the last keys that the first and the last of the 32 rows see
@@ -292,6 +307,16 @@ struct Rows32 {
 #pragma unroll
       for (int i2 = 0; i2 < 16; ++i2) o[e][i2] = 0.f;
   }
+  // Wide heads fill both halves of the register file: the sums stay in the accumulation registers, where the products
+  // add to them, the rows in the others (left to itself the allocator moves the sums to and fro in every tile).
+  __device__ __forceinline__ void keep_places() {
+    if constexpr (D > 128) {
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) asm volatile("" : "+v"(qf[d]));
+#pragma unroll
+      for (int e = 0; e < kMT; ++e) asm volatile("" : "+a"(o[e]));
+    }
+  }
   __device__ __forceinline__ bf16x8_t k_operand(const uint8_t* tile, int d, int h) const {
     const uint32_t low = (D == 64 ? 112u : 240u) & (32 * d), high = 32 * d - low;   // the pieces' exchanged bits
     return as_bf16x8(*reinterpret_cast<const u32x4_t*>(tile + (kat ^ low) + high + 32 * h * kRowBytes));
@@ -308,34 +333,34 @@ struct Rows32 {
   // value i of x belongs to key 16 (i / 8) + 8 hh + i % 8 of the tile
   __device__ __forceinline__ void score_products(const uint8_t* tile) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kKeys / 32; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[h][i] = 0.f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) x[h] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_operand(tile, d, h), qf[d], x[h], 0, 0, 0);
+      for (int h = 0; h < kKeys / 32; ++h) x[h] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_operand(tile, d, h), qf[d], x[h], 0, 0, 0);
   }
   __device__ __forceinline__ void sum_products(const uint8_t* tile) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
+    for (int ks = 0; ks < kKeys / 16; ++ks)
 #pragma unroll
       for (int e = 0; e < kMT; ++e)
         o[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand(tile, ks, e), p_operand(ks), o[e], 0, 0, 0);
   }
   __device__ __forceinline__ void scores(const uint8_t* tile) {
     score_products(tile);
-    ahead<0, D / 8>();
+    ahead<0, D / 16 * (kKeys / 32)>();
   }
   __device__ __forceinline__ void sums(const uint8_t* tile) {
     sum_products(tile);
-    ahead<4 * kMT, 0>();
+    ahead<kKeys / 16 * kMT, 0>();
   }
   template <int NW>
-  __device__ __forceinline__ void weights(const Attn& a, const float (*scales)[kKeys], const Stage<KIND, D, NW>& st, int32_t kb) {
+  __device__ __forceinline__ void weights(const Attn& a, const float (*scales)[tile_keys(D)], const Stage<KIND, D, NW>& st, int32_t kb) {
     if constexpr (kInt8) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
+      for (int i = 0; i < kKeys / 2; i += 4) {
         const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&scales[0][16 * (i >> 3) + (i & 7) + 8 * hh]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) x[i >> 4][(i & 15) + u] *= ks[u];
@@ -344,7 +369,7 @@ struct Rows32 {
     if (__builtin_amdgcn_readfirstlane(kb + kKeys - 1 > first_sees || !st.all_there)) {
       const int32_t most = last - kb - 8 * (int32_t)hh;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < kKeys / 16; ++g) {
         int32_t upto = most - 16 * g;
         if constexpr (kPaged)
           if (!st.all_there && (kb + 16 * g >= st.w.kend || !st.on_page(st.tab[(uint32_t)(kb + 16 * g) >> a.page_shift]))) upto = -1;
@@ -354,7 +379,7 @@ struct Rows32 {
     }
     float top4[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) top4[i / 2 & 3] = fmaxf(fmaxf(top4[i / 2 & 3], x[i >> 4][i & 15]), x[i >> 4][(i & 15) + 1]);
+    for (int i = 0; i < kKeys / 2; i += 2) top4[i / 2 & 3] = fmaxf(fmaxf(top4[i / 2 & 3], x[i >> 4][i & 15]), x[i >> 4][(i & 15) + 1]);
     float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale;
     if (__any(top > m + kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -366,7 +391,7 @@ struct Rows32 {
     }
     float sum[4] = {};
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
+    for (int i = 0; i < kKeys / 2; i += 4) {
       float y[4];
       f32x4_t vs;
       if constexpr (kInt8) vs = *reinterpret_cast<const f32x4_t*>(&scales[1][16 * (i >> 3) + (i & 7) + 8 * hh]);
@@ -385,6 +410,7 @@ struct Rows32 {
   template <int NW>
   __device__ __forceinline__ void odd_values(const Attn& a, const Work& w, const Stage<KIND, D, NW>& st, int32_t kb) {
     for (int32_t j = kb; j < kb + kKeys && j < w.kend; ++j) {
+      keep_places();
       const uint8_t* p;
       float vs = 0.f;
       if constexpr (kPaged) {
@@ -408,18 +434,27 @@ struct Rows32 {
   }
   __device__ __forceinline__ void finish(const Attn& a, const Work& w) {
     l += __shfl_xor(l, 32);
-    if (row < 0) return;
     if (a.n_splits == 1) {
-      const int32_t i = row / (int32_t)a.group;
+      const int32_t at = max(row, 0), i = at / (int32_t)a.group;
       const float f = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* p = a.out + (uint64_t)(w.q.first + i) * a.ldo + (uint64_t)(w.kvh * a.group + row - i * (int32_t)a.group) * D + 4 * hh;
+      uint16_t* p = a.out + (uint64_t)(w.q.first + i) * a.ldo + (uint64_t)(w.kvh * a.group + at - i * (int32_t)a.group) * D + 8 * hh;
 #pragma unroll
       for (int e = 0; e < kMT; ++e)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<u32x2_t*>(p + 32 * e + 8 * u) =
-              u32x2_t{pack_bf16(o[e][4 * u] * f, o[e][4 * u + 1] * f), pack_bf16(o[e][4 * u + 2] * f, o[e][4 * u + 3] * f)};
-    } else {
+        for (int u = 0; u < 4; u += 2) {
+          // the halves of a row exchange four elements: eight neighbours, 16 bytes, in each
+          uint32_t x[2], y[2];
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            x[v] = pack_bf16(o[e][4 * u + 2 * v] * f, o[e][4 * u + 2 * v + 1] * f);
+            y[v] = pack_bf16(o[e][4 * u + 4 + 2 * v] * f, o[e][4 * u + 4 + 2 * v + 1] * f);
+            const auto z = __builtin_amdgcn_permlane32_swap(x[v], y[v], false, false);
+            x[v] = z[0];
+            y[v] = z[1];
+          }
+          if (row >= 0) *reinterpret_cast<u32x4_t*>(p + 32 * e + 8 * u) = u32x4_t{x[0], x[1], y[0], y[1]};
+        }
+    } else if (row >= 0) {
       const uint64_t slot = (((uint64_t)w.s * a.n_splits + w.sp) * a.kv_heads + w.kvh) * a.part_rows + row;
       float* p = a.part + slot * D + 4 * hh;
 #pragma unroll
@@ -448,6 +483,7 @@ template <int KIND, int D>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   using St = Stage<KIND, D, 4>;
   constexpr bool kInt8 = KIND == kPagedInt8;
+  constexpr int kKeys = tile_keys(D);
   __shared__ __attribute__((aligned(256))) uint8_t ksh[2][kKeys * 2 * D], vsh[2][kKeys * 2 * D];
   __shared__ __attribute__((aligned(16))) float ssh[2][2][kKeys];
   __shared__ int32_t odd[2];
@@ -455,13 +491,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   Work w;
   if (!find_work<KIND != kPacked>(a, 128, lane, w)) return;
   Rows32<KIND, D> r;
-  r.begin(a, w, wave, lane);
   const St st(a, w, lane, wave);
   u32x4_t kr[St::kPasses], vr[St::kPasses];
   int32_t next_page[St::kPasses] = {}, next_scale = 0;
   bool there[St::kPasses];
   float scale = 0.f;
   const uint32_t klane = st.lane_offset((uint32_t)a.ldk), vlane = st.lane_offset((uint32_t)a.ldv);
+  const uint32_t kplace = st.template place<false>(), vplace = st.template place<true>();
   const void* kplane = St::kPaged ? static_cast<const void*>(a.cache) : a.k;
   const void* vplane = St::kPaged ? static_cast<const void*>(a.cache + a.off_v) : a.v;
   auto load = [&](int32_t kb) {
@@ -478,9 +514,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
     st.load_pages(next_page, next_scale, kb + kKeys);
   };
   auto store = [&](int b, int32_t kb) {
-    st.template put<false>(ksh[b], kr);
+    st.template put<false>(ksh[b], kplace, kr);
     st.clean_v(&odd[b], vr, there, kb);
-    st.template put<true>(vsh[b], vr);
+    st.template put<true>(vsh[b], vplace, vr);
     if (kInt8 && wave < 2) st.put_scale(ssh[b], &odd[b], scale, kb);
   };
   if (tid < 2) odd[tid] = 0;
@@ -488,6 +524,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   if (w.k0 < w.kend) {
     st.load_pages(next_page, next_scale, w.k0);
     load(w.k0);
+  }
+  r.begin(a, w, wave, lane);   // with the first keys on their way
+  if (w.k0 < w.kend) {
     store(0, w.k0);
     load(w.k0 + kKeys);
   }
@@ -496,8 +535,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   for (int32_t kb = w.k0; kb < w.kend; kb += kKeys, b ^= 1) {
     if (kb <= r.last_sees) {
       r.scores(ksh[b]);
+      r.keep_places();
       r.weights(a, ssh[b], st, kb);
+      r.keep_places();
       r.sums(vsh[b]);
+      r.keep_places();
       if (st.at_edge(kb) && __builtin_amdgcn_readfirstlane(odd[b] == kb + 1)) r.odd_values(a, w, st, kb);
     }
     if (kb + kKeys < w.kend) {
@@ -519,6 +561,7 @@ template <int KIND, int D>
 __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
   using St = Stage<KIND, D, 8>;
   constexpr bool kInt8 = KIND == kPagedInt8;
+  constexpr int kKeys = tile_keys(D);
   __shared__ __attribute__((aligned(256))) uint8_t ksh[2][kKeys * 2 * D], vsh[2][kKeys * 2 * D];
   __shared__ __attribute__((aligned(16))) float ssh[4][2][kKeys];
   __shared__ int32_t odd[4];
@@ -527,7 +570,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
   Work w;
   if (!find_work<KIND != kPacked>(a, 256, lane, w)) return;
   Rows32<KIND, D> r;
-  r.begin(a, w, wave, lane);
   const St st(a, w, lane, wave);
   u32x4_t kr[St::kPasses], vr[St::kPasses];
   int32_t next_page[St::kPasses] = {}, next_scale = 0;
@@ -536,6 +578,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
   float scale = 0.f;
   const int32_t tiles = max(w.kend - w.k0 + kKeys - 1, 0) / kKeys;
   const uint32_t klane = st.lane_offset((uint32_t)a.ldk), vlane = st.lane_offset((uint32_t)a.ldv);
+  const uint32_t kplace = st.template place<false>(), vplace = st.template place<true>();
   const void* kplane = St::kPaged ? static_cast<const void*>(a.cache) : a.k;
   const void* vplane = St::kPaged ? static_cast<const void*>(a.cache + a.off_v) : a.v;
   auto key0 = [&](int32_t tile) { return w.k0 + tile * kKeys; };
@@ -583,13 +626,16 @@ __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
   for (uint32_t i = tid; i < kKeys * 2 * D / 16; i += 512) reinterpret_cast<u32x4_t*>(vsh[1])[i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 16; ++i) r.pf[i / 4][i % 4] = 0;
-  __syncthreads();
   if (tiles) {
     st.load_pages(next_page, next_scale, w.k0);
     cut(0);
     load(0, false);
     load_rest(0);
-    st.template put<false>(ksh[0], kr);
+  }
+  r.begin(a, w, wave, lane);   // with the first keys on their way
+  lds_barrier();
+  if (tiles) {
+    st.template put<false>(ksh[0], kplace, kr);
     if (kInt8 && wave < 2) st.put_scale(ssh[0], &odd[0], scale, w.k0);
     cut(1);
     load(1, true);
@@ -602,8 +648,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
     st.clean_v(&odd[j & 3], vr, vthere, kb);
     if (kInt8 && wave < 2) st.put_scale(ssh[(j + 1) & 3], &odd[(j + 1) & 3], scale, kb + kKeys);
     cut(j + 2);
-    st.template put<false>(ksh[(j + 1) & 1], kr);
-    st.template put<true>(vsh[j & 1], vr);
+    st.template put<false>(ksh[(j + 1) & 1], kplace, kr);
+    st.template put<true>(vsh[j & 1], vplace, vr);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
     r.sum_products(vsh[(j + 1) & 1]);
