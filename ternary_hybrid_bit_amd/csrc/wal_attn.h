@@ -48,8 +48,9 @@ constexpr bool stream_wide(uint32_t n_seqs, uint32_t kv_heads, uint32_t max_len)
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream);
 int attn_join(const Attn& a, uint32_t dim, void* stream);
 // Any number of rows; kind kPacked, kPagedBf16 or kPagedInt8.  attn_tiles: how many
-// tiles of query rows (workgroups of each key/value head and split) it launches.
+// tiles of query rows (workgroups of each key/value head and split) it launches, attn_tile_rows: of how many rows.
 int attn_tile(const Attn& a, int kind, uint32_t dim, void* stream);
+uint32_t attn_tile_rows(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t kv_heads, uint32_t dim);
 uint64_t attn_tiles(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t kv_heads, uint32_t dim);
 
 }  // namespace wal

@@ -28,39 +28,60 @@ struct Plan {
   uint64_t off_ml, bytes;    // of the workspace
 };
 
-// The context is split when the workgroups of whole contexts leave compute units
-// idle, or, over several sequences of lengths that the host does not know,
-// would leave them waiting for the longest.
+// Keys of a piece of the context, max_len or more: whole.  The context is
+// split when the workgroups of whole contexts leave compute units idle, or, over
+// several sequences of lengths that the host does not know, would leave them
+// waiting for the longest.
 //  * Few rows, one sequence: two workgroups for each unit, not below 256 keys a
 //    piece (131,001 bf16 tokens, 8 key/value heads: 96 us and 5 us for the joining at 512
 //    pieces, 97 + 6 at 1024, 102 + 12 at 4096).
-//  * Few rows, several sequences: pieces of a twelfth of a workgroup slot's share, not
-//    below 512 keys (64 sequences up to 8192, int8: 97 us at 768 keys a piece, 100 at
-//    1024, 107 at 2048, 115 at 4096, 101 at 512).
-//  * Many rows: two workgroups a unit, not below 512 keys, so that the partial
-//    results stay small beside the products.
-// A piece of attn_stream is never above what a workgroup's page list holds.
-// Few short sequences are not split at all (517 tokens: 9.1 us with eight
-// wavefronts a workgroup, 6.5 + 3.0 us and a launch in pieces of 256 keys).
+//  * Few rows, several sequences: 6144 pieces in all, not below 512 keys (64
+//    sequences up to 8192, int8: 97 us at 768 keys a piece, 100 at 1024, 107 at
+//    2048, 115 at 4096, 101 at 512).  A piece of attn_stream is never above
+//    what a workgroup's page list holds.  Few short contexts are not split at all (517 tokens: 9.1
+//    us with eight wavefronts a workgroup, 6.5 + 3.0 us and a launch in pieces of 256 keys).
+//  * Many rows, one sequence: into as many pieces as give the fewest rounds of
+//    workgroups over the places for them, not below 512 keys, the joining counted as 1.5 % of
+//    the products (2048 tokens over 32768, 256 workgroups: 1140 us whole, 1161 in two pieces).
+//  * Many rows, several sequences: pieces of 1024 keys unless there are workgroups enough
+//    for four rounds (13 sequences up to 4100, 260 workgroups: 63 us whole, 55 in pieces of 2048
+//    keys, 49 of 1024, 52 of 512).
+uint32_t piece(bool stream, uint32_t dim, uint32_t n_seqs, uint64_t items, uint32_t tile_rows, uint32_t max_len) {
+  const auto up128 = [](uint64_t keys) { return (keys + 127) / 128 * 128; };
+  if (stream) {
+    const uint64_t target = n_seqs > 1 ? 6144 : 512, least = n_seqs > 1 ? 512 : 256;
+    const uint64_t want = (target + items - 1) / items, keys = up128((max_len + want - 1) / want);
+    return (uint32_t)(keys < least ? least : keys > kMaxSplit ? kMaxSplit : keys);
+  }
+  const uint64_t places = tile_rows == 256 || dim > 128 ? 256 : 512;   // one workgroup on a compute unit, or two
+  if (n_seqs > 1) return items >= 4 * places ? max_len : 1024;
+  uint32_t best = max_len;
+  double least = 1e30;
+  for (uint64_t n = 1; n <= 64; ++n) {
+    const uint64_t keys = n == 1 ? max_len : up128((max_len + n - 1) / n);
+    if (n > 1 && keys < 512) break;
+    const double cost = (double)((items * n + places - 1) / places) / (double)n + (n > 1 ? 0.015 : 0.0);
+    if (cost < least * 0.999) {
+      least = cost;
+      best = (uint32_t)keys;
+    }
+  }
+  return best;
+}
+
 Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n, uint32_t max_new,
              uint32_t max_len) {
   Plan p{};
-  const uint32_t group = q_heads / d->kv_heads;
+  const uint32_t group = q_heads / d->kv_heads, dim = d->head_dim;
   const uint64_t rows = (uint64_t)max_new * group;
-  p.stream = rows <= stream_rows(d->head_dim);
+  p.stream = rows <= stream_rows(dim);
   p.n_splits = 1;
   p.split = p.stream ? kMaxSplit : max_len;
   if (!rows || !n_seqs || !max_len || !n) return p;
-  const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->kv_heads, d->head_dim)) * d->kv_heads;
   if (p.stream && rows <= 16 && stream_wide(n_seqs, d->kv_heads, max_len)) return p;
-  const bool even = !p.stream || n_seqs == 1;
-  const uint64_t target = even ? 512 : 6144, least = p.stream && even ? 256 : 512;
-  const uint64_t want = (target + items - 1) / items;
-  uint64_t split = ((max_len + want - 1) / want + 127) / 128 * 128;
-  if (split < least) split = least;
-  if (p.stream && split > kMaxSplit) split = kMaxSplit;
-  p.split = (uint32_t)split;
-  p.n_splits = (uint32_t)((max_len + split - 1) / split);
+  const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->kv_heads, dim)) * d->kv_heads;
+  p.split = piece(p.stream, dim, n_seqs, items, attn_tile_rows(n_seqs, n, max_new, group, d->kv_heads, dim), max_len);
+  p.n_splits = (max_len + p.split - 1) / p.split;
   if (p.n_splits == 1) return p;
   // Workgroups go to the shader engines in turn: with an even number of splits
   // to a sequence some engines would get the ends of the contexts again and again,
@@ -68,7 +89,7 @@ Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n
   if (n_seqs > 1) p.n_splits |= 1;
   p.part_rows = (uint32_t)rows;
   const uint64_t slots = (uint64_t)n_seqs * d->kv_heads * p.n_splits * rows;
-  p.off_ml = slots * d->head_dim * 4;
+  p.off_ml = slots * dim * 4;
   p.bytes = p.off_ml + slots * 8;
   return p;
 }

@@ -4,7 +4,7 @@
 // Bound by the matrix cores.  A workgroup takes 32 QT NW query rows of one key/value
 // head (a row is one token of one of the query heads that share the head, token by
 // token, so that the rows of a workgroup see nearly the same keys) and runs over
-// tiles of 64 keys (32 of wide heads), staged in LDS by all its wavefronts: from memory to registers
+// tiles of 64 keys, staged in LDS by all its wavefronts: from memory to registers
 // while the tile before is computed, from there to the other of two LDS
 // buffers (int8 codes become bf16, exactly, on the way).  As in the kernel
 // for few rows everything is transposed, so that a lane's scores belong to one
@@ -30,8 +30,7 @@
 namespace {
 
 constexpr float kSlack = 8.f;
-// Keys of a tile: 64, or 32 where 64 of them would not leave room for the rows in registers.
-constexpr int tile_keys(int dim) { return dim > 128 ? 32 : 64; }
+constexpr int kKeys = 64;   // of a tile
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
@@ -111,7 +110,6 @@ __device__ __forceinline__ bool find_work(const Attn& a, uint32_t tile_rows, uin
 template <int KIND, int D, int NW>
 struct Stage {
   static constexpr bool kInt8 = KIND == kPagedInt8, kPaged = KIND != kPacked;
-  static constexpr int kKeys = tile_keys(D);
   static constexpr uint32_t kElem = kInt8 ? 1 : 2;
   static constexpr uint32_t kPieces = D * kElem / 16;       // 16-byte pieces of a row in memory
   static constexpr uint32_t kWaveRows = 64 / kPieces, kRows = NW * kWaveRows;
@@ -229,12 +227,12 @@ struct Stage {
       }
     }
   }
-  __device__ __forceinline__ void put_scale(float (*tile)[tile_keys(D)], int32_t* odd, float s, int32_t kb) const {
+  __device__ __forceinline__ void put_scale(float (*tile)[kKeys], int32_t* odd, float s, int32_t kb) const {
     if (wave == 1 && at_edge(kb) && !(fabsf(s) < INFINITY)) {
       s = 0.f;
       *odd = kb + 1;
     }
-    if (lane < kKeys) tile[wave][lane] = s;
+    tile[wave][lane] = s;
   }
 };
 
@@ -264,7 +262,7 @@ __device__ __forceinline__ void ahead() {
 template <int KIND, int D>
 struct Rows32 {
   static constexpr bool kInt8 = KIND == kPagedInt8, kPaged = KIND != kPacked;
-  static constexpr int kKeys = tile_keys(D), kMT = D / 32, kRowBytes = 2 * D;
+  static constexpr int kMT = D / 32, kRowBytes = 2 * D;
   bf16x8_t qf[D / 16];          // B operands: the rows
   uint32_t pf[kKeys / 16][4];   // B operands: the weights of a tile
   f32x16_t x[kKeys / 32], o[kMT];
@@ -357,7 +355,7 @@ struct Rows32 {
     ahead<kKeys / 16 * kMT, 0>();
   }
   template <int NW>
-  __device__ __forceinline__ void weights(const Attn& a, const float (*scales)[tile_keys(D)], const Stage<KIND, D, NW>& st, int32_t kb) {
+  __device__ __forceinline__ void weights(const Attn& a, const float (*scales)[kKeys], const Stage<KIND, D, NW>& st, int32_t kb) {
     if constexpr (kInt8) {
 #pragma unroll
       for (int i = 0; i < kKeys / 2; i += 4) {
@@ -483,7 +481,6 @@ template <int KIND, int D>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   using St = Stage<KIND, D, 4>;
   constexpr bool kInt8 = KIND == kPagedInt8;
-  constexpr int kKeys = tile_keys(D);
   __shared__ __attribute__((aligned(256))) uint8_t ksh[2][kKeys * 2 * D], vsh[2][kKeys * 2 * D];
   __shared__ __attribute__((aligned(16))) float ssh[2][2][kKeys];
   __shared__ int32_t odd[2];
@@ -561,7 +558,6 @@ template <int KIND, int D>
 __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
   using St = Stage<KIND, D, 8>;
   constexpr bool kInt8 = KIND == kPagedInt8;
-  constexpr int kKeys = tile_keys(D);
   __shared__ __attribute__((aligned(256))) uint8_t ksh[2][kKeys * 2 * D], vsh[2][kKeys * 2 * D];
   __shared__ __attribute__((aligned(16))) float ssh[4][2][kKeys];
   __shared__ int32_t odd[4];
@@ -677,14 +673,9 @@ uint64_t tiles_of(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group,
   return each * n_seqs < all ? each * n_seqs : all;
 }
 
-uint32_t tile_rows(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t kv_heads, uint32_t dim) {
-  if (dim > 128) return 128;
-  return tiles_of(n_seqs, n, max_new, group, 256) * kv_heads >= 256 ? 256 : 128;
-}
-
 template <int KIND, int D>
 int launch(const Attn& a, hipStream_t s) {
-  const uint32_t rows = tile_rows(a.n_seqs, a.n, a.max_new, a.group, a.kv_heads, D);
+  const uint32_t rows = attn_tile_rows(a.n_seqs, a.n, a.max_new, a.group, a.kv_heads, D);
   const uint64_t blocks = attn_tiles(a.n_seqs, a.n, a.max_new, a.group, a.kv_heads, D) * a.kv_heads * a.n_splits;
   if (blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
   if constexpr (D <= 128) {
@@ -708,8 +699,14 @@ int launch(const Attn& a, uint32_t dim, hipStream_t s) {
 
 namespace wal {
 
+// Eight wavefronts of 32 rows when that gives every compute unit a workgroup (prompt of 8192 tokens, 32 query and 8
+// key/value heads of 128: 515 us, and 590 with four), else four; wide heads have room for four only.
+uint32_t attn_tile_rows(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t kv_heads, uint32_t dim) {
+  return dim <= 128 && tiles_of(n_seqs, n, max_new, group, 256) * kv_heads >= 256 ? 256 : 128;
+}
+
 uint64_t attn_tiles(uint32_t n_seqs, uint32_t n, uint32_t max_new, uint32_t group, uint32_t kv_heads, uint32_t dim) {
-  return tiles_of(n_seqs, n, max_new, group, tile_rows(n_seqs, n, max_new, group, kv_heads, dim));
+  return tiles_of(n_seqs, n, max_new, group, attn_tile_rows(n_seqs, n, max_new, group, kv_heads, dim));
 }
 
 int attn_tile(const Attn& a, int kind, uint32_t dim, void* stream) {
