@@ -1,0 +1,128 @@
+"""An attention layer over packed matrices: the q, k, v and o products with
+rotary positions, the paged cache and the attention between them.
+
+``AttentionLayer`` is the shortest complete use of wal_rope_freqs,
+wal_kv_write, wal_attn_paged and wal_attn_prompt: forward() takes the new
+tokens of any sequences, whole prompts, chunks of them and single tokens
+alike.  examples/attention_layer.py runs one.
+
+Everything on the GPU is libwal's; this module keeps the page lists.
+"""
+from __future__ import annotations
+
+from typing import List, Sequence, Tuple
+
+import numpy as np
+
+from . import (WAL_KV_BF16, WAL_MAX_BATCH, WAL_ROPE_HALF, make_kv_desc, make_rope_desc, wal_attn_paged,
+               wal_attn_paged_workspace_size, wal_attn_prompt, wal_gemm_prefill, wal_gemm_small, wal_kv_size,
+               wal_kv_write, wal_prefill_workspace_size, wal_rope, wal_rope_freqs, wal_workspace_size)
+
+
+class AttentionLayer:
+    """q, k, v, o: (info, packed bytes on the GPU) of the layer's matrices; the
+    heads' size is head_dim.  The cache holds n_pages pages of page_size
+    tokens for max_seqs sequences."""
+
+    def __init__(self, q, k, v, o, head_dim: int, n_pages: int, max_seqs: int, page_size: int = 64,
+                 fmt: int = WAL_KV_BF16, rope=None, layout: int = WAL_ROPE_HALF):
+        import torch
+        self.torch, self.dev = torch, q[1].device
+        self.mats, self.head_dim, self.layout = (q, k, v, o), head_dim, layout
+        self.q_heads, self.kv_heads = q[0].d.out // head_dim, k[0].d.out // head_dim
+        turns, self.magnitude = wal_rope_freqs(rope if rope is not None else make_rope_desc(head_dim, base=1e6))
+        self.turns = torch.from_numpy(turns).to(self.dev)
+        self.desc = make_kv_desc(n_pages, page_size, self.kv_heads, head_dim, fmt)
+        self.cache = torch.empty(wal_kv_size(self.desc).total_bytes, dtype=torch.uint8, device=self.dev)
+        self.free = list(range(n_pages))
+        self.pages: List[List[int]] = [[] for _ in range(max_seqs)]
+        self.lens = [0] * max_seqs
+        self.ws = None
+
+    def _workspace(self, n: int):
+        """One zeroed buffer, grown when a call needs more (products want their first words zero once)."""
+        if self.ws is None or self.ws.numel() < n:
+            self.ws = self.torch.zeros(max(n, 16), dtype=self.torch.uint8, device=self.dev)
+        return self.ws
+
+    def _product(self, m, X):
+        info, W = m
+        Y = self.torch.empty((X.shape[0], info.d.out), device=self.dev)
+        if X.shape[0] <= WAL_MAX_BATCH:
+            return wal_gemm_small(info, W, X, Y, ws=self._workspace(wal_workspace_size(info, X.shape[0])))
+        return wal_gemm_prefill(info, W, X, Y, ws=self._workspace(wal_prefill_workspace_size(info, X.shape[0])))
+
+    def _append(self, seqs: Sequence[int], new: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
+        """Pages for the new tokens: their cache slots and positions."""
+        size, slots, pos = self.desc.page_size, [], []
+        for s, n in zip(seqs, new):
+            t = np.arange(self.lens[s], self.lens[s] + n)
+            while len(self.pages[s]) * size < self.lens[s] + n:
+                self.pages[s].append(self.free.pop())
+            slots.append(np.asarray(self.pages[s], np.int64)[t // size] * size + t % size if n else t)
+            pos.append(t)
+            self.lens[s] += n
+        return np.concatenate(slots).astype(np.int32), np.concatenate(pos).astype(np.int32)
+
+    def release(self, s: int):
+        self.free += self.pages[s]
+        self.pages[s], self.lens[s] = [], 0
+
+    def attend(self, Q, K, V, seqs: Sequence[int], new: Sequence[int]):
+        """The part between the products: Q, K, V (fp32 or bf16) of new[i] tokens of
+        sequence seqs[i] each, one after another -> bf16 [n][q_heads * head_dim]."""
+        torch = self.torch
+        slots, pos = self._append(seqs, new)
+        lens = [self.lens[s] for s in seqs]
+        tables = np.zeros((len(seqs), max(1, max(len(self.pages[s]) for s in seqs))), np.int32)
+        for i, s in enumerate(seqs):
+            tables[i, :len(self.pages[s])] = self.pages[s]
+        slots, pos, lens_dev, starts, tables = self._put(slots, pos, lens, np.cumsum([0] + list(new)), tables)
+        q, out = (torch.empty(Q.shape, dtype=torch.bfloat16, device=self.dev) for _ in range(2))
+        wal_kv_write(self.desc, self.cache, slots, K, V, pos=pos, turns=self.turns, layout=self.layout,
+                     magnitude=self.magnitude, Q=Q, Q_out=q)
+        max_new, max_len = max(new), max(lens)
+        ws = self._workspace(wal_attn_paged_workspace_size(self.desc, self.q_heads, len(seqs), Q.shape[0], max_new,
+                                                           max_len))
+        return wal_attn_paged(self.desc, self.cache, tables, lens_dev, starts, q, out, ws, max_new=max_new,
+                              max_len=max_len)
+
+    def _put(self, *arrays):
+        """int32 arrays to the GPU in one copy."""
+        arrays = [np.asarray(x, np.int32) for x in arrays]
+        flat = self.torch.from_numpy(np.concatenate([x.ravel() for x in arrays])).to(self.dev)
+        at = np.cumsum([0] + [x.size for x in arrays])
+        return [flat[i:j].view(x.shape) for x, i, j in zip(arrays, at[:-1], at[1:])]
+
+    def forward(self, X, seqs: Sequence[int], new: Sequence[int]):
+        """X bf16 [n][hidden] -> fp32 [n][hidden], the new tokens of the sequences kept in the cache."""
+        Q, K, V = (self._product(m, X) for m in self.mats[:3])
+        return self._product(self.mats[3], self.attend(Q, K, V, seqs, new))
+
+    def prompt(self, X, lens: Sequence[int]):
+        """The same for whole prompts that need no cache (scoring): X bf16, prompts one after another."""
+        torch = self.torch
+        Q, K, V = (self._product(m, X) for m in self.mats[:3])
+        pos = torch.from_numpy(np.concatenate([np.arange(n) for n in lens]).astype(np.int32)).to(self.dev)
+        q, k = (torch.empty(t.shape, dtype=torch.bfloat16, device=self.dev) for t in (Q, K))
+        for t, r in ((Q, q), (K, k)):
+            wal_rope(t, r, pos, self.turns, self.head_dim, layout=self.layout, magnitude=self.magnitude)
+        starts = torch.tensor(np.cumsum([0] + list(lens)), dtype=torch.int32, device=self.dev)
+        out = torch.empty_like(q)
+        wal_attn_prompt(q, k, V.to(torch.bfloat16), starts, out, self.head_dim, max(lens))
+        return self._product(self.mats[3], out)
+
+
+def packed_layer(seed: int, hidden: int, q_heads: int, kv_heads: int, head_dim: int, rank: int = 16):
+    """Random packed q, k, v, o of a layer, on the GPU."""
+    import torch
+
+    import synth
+
+    from . import pack_matrix
+    out = []
+    for i, (rows, cols) in enumerate([(q_heads * head_dim, hidden)] + 2 * [(kv_heads * head_dim, hidden)]
+                                     + [(hidden, q_heads * head_dim)]):
+        blob, info = pack_matrix(synth.make_matrix(seed, i, rows, cols, k=8, n_paths=1, rank=rank))
+        out.append((info, torch.from_numpy(blob).to("cuda")))
+    return out

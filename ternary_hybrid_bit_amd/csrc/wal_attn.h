@@ -29,9 +29,9 @@ struct Attn {
   const uint16_t* v;
   uint64_t ldk, ldv;
   // keys of one workgroup when the context is split, and the partial results
-  uint32_t split, n_splits, part_rows;
-  float* part;                   // [sequence][split][kv head][part_rows][dim] sums of w v
-  float2* part_ml;               // [sequence][split][kv head][part_rows] maximum, sum of w
+  uint32_t split, n_splits;
+  float* part;                   // [split][kv head][n * group][dim] sums of w v
+  float2* part_ml;               // [split][kv head][n * group] maximum, sum of w
 };
 
 constexpr uint32_t kMaxSplit = 4096;   // keys of a workgroup of attn_stream: its pages' addresses fit in 2 KB of LDS
@@ -63,6 +63,11 @@ constexpr float kNoMax = -3.0e38f;   // a running maximum before the first key: 
 
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// Place of a row's partial result: row (first row of the sequence + token) * group + query head of the group.
+__device__ __forceinline__ uint64_t part_row(const Attn& a, uint32_t split, uint32_t kvh, uint64_t row) {
+  return ((uint64_t)split * a.kv_heads + kvh) * ((uint64_t)a.n * a.group) + row;
+}
 
 // A sequence's part of a call, cut to the rows and tokens that there are
 // whatever starts and lens hold.

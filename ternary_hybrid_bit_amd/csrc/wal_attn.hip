@@ -12,6 +12,7 @@ bool heads_ok(uint32_t q_heads, uint32_t kv_heads) {
 
 constexpr uint32_t kMaxRows = 1u << 26;   // query rows, sequences and tokens of a call
 constexpr uint32_t kMaxPitch = 1u << 26;  // elements from a row of keys to the next: 16 rows in 32 bits of bytes
+constexpr uint64_t kMaxPartBytes = 1ull << 28;   // partial results of a call with many rows: fewer pieces beyond
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The kernels multiply scores by a positive number only: masked ones are -infinity, so a
@@ -24,7 +25,7 @@ void set_scale(Attn& a, float scale) {
 // How a call over the cache is cut.
 struct Plan {
   bool stream;               // few rows for each key/value head: attn_stream, else attn_tile
-  uint32_t split, n_splits, part_rows;
+  uint32_t split, n_splits;
   uint64_t off_ml, bytes;    // of the workspace
 };
 
@@ -81,16 +82,19 @@ Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n
   if (p.stream && rows <= 16 && stream_wide(n_seqs, d->kv_heads, max_len)) return p;
   const uint64_t items = (p.stream ? n_seqs : attn_tiles(n_seqs, n, max_new, group, d->kv_heads, dim)) * d->kv_heads;
   p.split = piece(p.stream, dim, n_seqs, items, attn_tile_rows(n_seqs, n, max_new, group, d->kv_heads, dim), max_len);
+  const uint64_t all = (uint64_t)n * q_heads;   // rows of a split's partial results
+  if (!p.stream) {
+    const uint64_t most = kMaxPartBytes / (all * dim * 4), keys = most > 1 ? (max_len + most - 1) / most : max_len;
+    if (p.split < keys) p.split = (uint32_t)((keys + 127) / 128 * 128);
+  }
   p.n_splits = (max_len + p.split - 1) / p.split;
   if (p.n_splits == 1) return p;
   // Workgroups go to the shader engines in turn: with an even number of splits
   // to a sequence some engines would get the ends of the contexts again and again,
   // where shorter sequences have nothing to do.
   if (n_seqs > 1) p.n_splits |= 1;
-  p.part_rows = (uint32_t)rows;
-  const uint64_t slots = (uint64_t)n_seqs * d->kv_heads * p.n_splits * rows;
-  p.off_ml = slots * dim * 4;
-  p.bytes = p.off_ml + slots * 8;
+  p.off_ml = p.n_splits * all * dim * 4;
+  p.bytes = p.off_ml + p.n_splits * all * 8;
   return p;
 }
 
@@ -163,7 +167,6 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   const bool int8 = d->fmt == WAL_KV_INT8;
   a.split = p.split;
   a.n_splits = p.n_splits;
-  a.part_rows = p.part_rows;
   a.part = static_cast<float*>(ws_dev);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws_dev) + p.off_ml);
   st = p.stream ? attn_stream(a, int8, d->head_dim, max_new * a.group <= 16 ? 1 : 2, stream)

@@ -333,7 +333,7 @@ __global__ __launch_bounds__(64 * NW, stream_waves(D, NT)) void k_attn_stream(At
         uint16_t* p = a.out + (uint64_t)(q.first + tok) * a.ldo + (uint64_t)(kvh * a.group + r - tok * (int32_t)a.group) * D + d;
         *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f)};
       } else {
-        const uint64_t slot = (((uint64_t)s * a.n_splits + sp) * a.kv_heads + kvh) * a.part_rows + r;
+        const uint64_t slot = part_row(a, sp, kvh, (uint64_t)q.first * a.group + r);
         *reinterpret_cast<f32x4_t*>(a.part + slot * D + d) = acc;
         if (d == 0) a.part_ml[slot] = make_float2(top, sum);
       }
@@ -357,10 +357,9 @@ __global__ __launch_bounds__(256) void k_attn_join(Attn a) {
   const Seq q = seq_of(a, s, true);
   const int32_t i = (int32_t)t - q.first;
   const bool live = inside && i >= 0 && i < q.rows;
-  const uint32_t r = live ? (uint32_t)i * a.group + h - kvh * a.group : 0;
   const uint32_t splits = live ? ((uint32_t)q.len + a.split - 1) / a.split : 0;
-  const uint64_t step = (uint64_t)a.kv_heads * a.part_rows;
-  const uint64_t slot = ((uint64_t)s * a.n_splits * a.kv_heads + kvh) * a.part_rows + r;
+  const uint64_t step = (uint64_t)a.n * a.q_heads;
+  const uint64_t slot = live ? part_row(a, 0, kvh, (uint64_t)t * a.group + h - kvh * a.group) : 0;
   const float2* ml = a.part_ml + slot;
   // the row's maximum
   float top = kNoMax;

@@ -453,7 +453,7 @@ struct Rows32 {
           if (row >= 0) *reinterpret_cast<u32x4_t*>(p + 32 * e + 8 * u) = u32x4_t{x[0], x[1], y[0], y[1]};
         }
     } else if (row >= 0) {
-      const uint64_t slot = (((uint64_t)w.s * a.n_splits + w.sp) * a.kv_heads + w.kvh) * a.part_rows + row;
+      const uint64_t slot = part_row(a, w.sp, w.kvh, (uint64_t)w.q.first * a.group + row);
       float* p = a.part + slot * D + 4 * hh;
 #pragma unroll
       for (int e = 0; e < kMT; ++e)
