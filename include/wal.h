@@ -662,13 +662,16 @@ int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const int32_t* slot
  *               64 kv_heads) heads side by side; out_dev [n][ldo] bf16;
  *               16-byte aligned rows; out must not overlap the inputs
  *   scale       finite
- *   ws          wal_attn_paged_workspace_size bytes, 256-byte aligned (NULL when that is 0); its
- *               contents need not be kept, nor cleared before a call
+ *   ws          wal_attn_paged_workspace_size bytes, 256-byte aligned (NULL when
+ *               that is 0).  Its first WAL_ATTN_WS_ZERO_BYTES bytes are zero
+ *               before the first call; every call leaves them so, whatever its
+ *               sizes.  Calls that may overlap in time need workspaces of their own
  * Products q . k and w v run on the matrix cores with bf16 operands (int8
  * codes are exact in bf16; w is rounded to bf16 after its exponential, times
  * the row's scale for an int8 cache) and fp32 sums; maxima, sums and partial
  * results are fp32.  The result does not depend on timing.
  * Errors: ARG, SHAPE, ALIGN, BUFFER, DEVICE. */
+#define WAL_ATTN_WS_ZERO_BYTES 65536
 int wal_attn_paged_workspace_size(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n,
                                   uint32_t max_new, uint32_t max_len, size_t* bytes);
 int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const int32_t* tables_dev, uint32_t ldt,

@@ -33,6 +33,7 @@ WAL_SYNC_FALLBACK_WORD = 0
 WAL_ROPE_HALF, WAL_ROPE_INTERLEAVED = 0, 1
 WAL_ROPE_PLAIN, WAL_ROPE_LINEAR, WAL_ROPE_NTK, WAL_ROPE_PARTS = 0, 1, 2, 3
 WAL_KV_BF16, WAL_KV_INT8 = 0, 1
+WAL_ATTN_WS_ZERO_BYTES = 65536
 
 STATUS = {0: "WAL_OK", -1: "WAL_ERR_ARG", -2: "WAL_ERR_SHAPE", -3: "WAL_ERR_CODE",
           -4: "WAL_ERR_INEXACT", -5: "WAL_ERR_BUFFER", -6: "WAL_ERR_ALIGN", -7: "WAL_ERR_FORMAT",
@@ -895,7 +896,8 @@ def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=No
                    max_new: int = 1, max_len: int = 0, stream=None):
     """out = attention of Q's rows over the paged cache: tables int32
     [n_seqs][pages], lens int32 [n_seqs], starts int32 [n_seqs + 1], Q and out
-    bf16 [n][q_heads * head_dim], ws of wal_attn_paged_workspace_size bytes.
+    bf16 [n][q_heads * head_dim], ws of wal_attn_paged_workspace_size bytes, the
+    first WAL_ATTN_WS_ZERO_BYTES of them zero before its first call (torch.zeros).
     scale: 1 / sqrt(head_dim) unless given; max_new and max_len bound the
     sequences' new tokens and lengths (max_len 0: what the tables hold)."""
     T = _types()

@@ -37,20 +37,21 @@ class AttentionLayer:
         self.free = list(range(n_pages))
         self.pages: List[List[int]] = [[] for _ in range(max_seqs)]
         self.lens = [0] * max_seqs
-        self.ws = None
+        self.ws = {}
 
-    def _workspace(self, n: int):
-        """One zeroed buffer, grown when a call needs more (products want their first words zero once)."""
-        if self.ws is None or self.ws.numel() < n:
-            self.ws = self.torch.zeros(max(n, 16), dtype=self.torch.uint8, device=self.dev)
-        return self.ws
+    def _workspace(self, what: str, n: int):
+        """A zeroed buffer for the products and one for the attention, each of which keeps its own first
+        words zero between calls; grown when a call needs more."""
+        if what not in self.ws or self.ws[what].numel() < n:
+            self.ws[what] = self.torch.zeros(max(n, 16), dtype=self.torch.uint8, device=self.dev)
+        return self.ws[what]
 
     def _product(self, m, X):
         info, W = m
         Y = self.torch.empty((X.shape[0], info.d.out), device=self.dev)
         if X.shape[0] <= WAL_MAX_BATCH:
-            return wal_gemm_small(info, W, X, Y, ws=self._workspace(wal_workspace_size(info, X.shape[0])))
-        return wal_gemm_prefill(info, W, X, Y, ws=self._workspace(wal_prefill_workspace_size(info, X.shape[0])))
+            return wal_gemm_small(info, W, X, Y, ws=self._workspace("product", wal_workspace_size(info, X.shape[0])))
+        return wal_gemm_prefill(info, W, X, Y, ws=self._workspace("prompt", wal_prefill_workspace_size(info, X.shape[0])))
 
     def _append(self, seqs: Sequence[int], new: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
         """Pages for the new tokens: their cache slots and positions."""
@@ -82,8 +83,8 @@ class AttentionLayer:
         wal_kv_write(self.desc, self.cache, slots, K, V, pos=pos, turns=self.turns, layout=self.layout,
                      magnitude=self.magnitude, Q=Q, Q_out=q)
         max_new, max_len = max(new), max(lens)
-        ws = self._workspace(wal_attn_paged_workspace_size(self.desc, self.q_heads, len(seqs), Q.shape[0], max_new,
-                                                           max_len))
+        ws = self._workspace("attention", wal_attn_paged_workspace_size(self.desc, self.q_heads, len(seqs),
+                                                                        Q.shape[0], max_new, max_len))
         return wal_attn_paged(self.desc, self.cache, tables, lens_dev, starts, q, out, ws, max_new=max_new,
                               max_len=max_len)
 

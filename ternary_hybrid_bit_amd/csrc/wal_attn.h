@@ -32,9 +32,13 @@ struct Attn {
   uint32_t split, n_splits;
   float* part;                   // [split][kv head][n * group][dim] sums of w v
   float2* part_ml;               // [split][kv head][n * group] maximum, sum of w
+  uint32_t* counters;            // [n_seqs][kv head] pieces done, 0 between calls: attn_stream joins itself (else NULL)
+  uint32_t ones_done;            // contexts of one piece are not partial results
 };
 
 constexpr uint32_t kMaxSplit = 4096;   // keys of a workgroup of attn_stream: its pages' addresses fit in 2 KB of LDS
+constexpr int kJoinHere = 16;          // pieces that attn_stream joins itself
+constexpr uint32_t kCounters = 16384;  // sequences times key/value heads of such a call
 // Query rows of a key/value head that attn_stream takes: two tiles of 16, one where two would not fit in registers.
 constexpr uint32_t stream_rows(uint32_t dim) { return dim == 256 ? 16 : 32; }
 
@@ -44,7 +48,7 @@ constexpr bool stream_wide(uint32_t n_seqs, uint32_t kv_heads, uint32_t max_len)
 }
 
 // Launches (wal_status).  attn_stream: rows of each key/value head <= 16 tiles, tiles 1 or 2;
-// attn_join adds what it wrote when a.n_splits > 1.
+// attn_join adds what it wrote when a.n_splits > 1 and a.counters is NULL.
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream);
 int attn_join(const Attn& a, uint32_t dim, void* stream);
 // Any number of rows; kind kPacked, kPagedBf16 or kPagedInt8.  attn_tiles: how many

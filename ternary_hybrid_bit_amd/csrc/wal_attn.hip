@@ -26,7 +26,8 @@ void set_scale(Attn& a, float scale) {
 struct Plan {
   bool stream;               // few rows for each key/value head: attn_stream, else attn_tile
   uint32_t split, n_splits;
-  uint64_t off_ml, bytes;    // of the workspace
+  bool join_here;            // attn_stream joins the pieces itself
+  uint64_t off_part, off_ml, bytes;   // of the workspace: counters, sums, maxima and sums of weights
 };
 
 // Keys of a piece of the context, max_len or more: whole.  The context is
@@ -34,12 +35,12 @@ struct Plan {
 // several sequences of lengths that the host does not know, would leave them
 // waiting for the longest.
 //  * Few rows, one sequence: two workgroups for each unit, not below 256 keys a
-//    piece (131,001 bf16 tokens, 8 key/value heads: 96 us and 5 us for the joining at 512
-//    pieces, 97 + 6 at 1024, 102 + 12 at 4096).
-//  * Few rows, several sequences: 6144 pieces in all, not below 512 keys (64
-//    sequences up to 8192, int8: 97 us at 768 keys a piece, 100 at 1024, 107 at
-//    2048, 115 at 4096, 101 at 512).  A piece of attn_stream is never above
-//    what a workgroup's page list holds.  Few short contexts are not split at all (517 tokens: 9.1
+//    piece (131,001 bf16 tokens, 8 key/value heads: 97 us at 512 pieces, 100 at 1024, 109 at 4096).
+//  * Few rows, several sequences: 6144 pieces in all, not below 256 keys, or 768 of
+//    wide heads, whose workgroups have a compute unit to themselves (64 sequences up to
+//    8192, int8: 102 us at 768 keys a piece, 108 at 2048 and at 512; 8 sequences up to 2048:
+//    13.7 us at 256, 17.6 at 512; 4 sequences up to 16000, heads of 256: 34 us at 768, 46 at
+//    512).  A piece of attn_stream is never above what a workgroup's page list holds.  Few short contexts are not split at all (517 tokens: 9.1
 //    us with eight wavefronts a workgroup, 6.5 + 3.0 us and a launch in pieces of 256 keys).
 //  * Many rows, one sequence: into as many pieces as give the fewest rounds of
 //    workgroups over the places for them, not below 512 keys, the joining counted as 1.5 % of
@@ -50,7 +51,7 @@ struct Plan {
 uint32_t piece(bool stream, uint32_t dim, uint32_t n_seqs, uint64_t items, uint32_t tile_rows, uint32_t max_len) {
   const auto up128 = [](uint64_t keys) { return (keys + 127) / 128 * 128; };
   if (stream) {
-    const uint64_t target = n_seqs > 1 ? 6144 : 512, least = n_seqs > 1 ? 512 : 256;
+    const uint64_t target = n_seqs > 1 ? 6144 : 512, least = dim > 128 ? 768 : 256;
     const uint64_t want = (target + items - 1) / items, keys = up128((max_len + want - 1) / want);
     return (uint32_t)(keys < least ? least : keys > kMaxSplit ? kMaxSplit : keys);
   }
@@ -93,7 +94,9 @@ Plan plan_of(const wal_kv_desc* d, uint32_t q_heads, uint32_t n_seqs, uint32_t n
   // to a sequence some engines would get the ends of the contexts again and again,
   // where shorter sequences have nothing to do.
   if (n_seqs > 1) p.n_splits |= 1;
-  p.off_ml = p.n_splits * all * dim * 4;
+  p.join_here = p.stream && p.n_splits <= (uint32_t)kJoinHere && (uint64_t)n_seqs * d->kv_heads <= kCounters;
+  p.off_part = 4 * kCounters;
+  p.off_ml = p.off_part + p.n_splits * all * dim * 4;
   p.bytes = p.off_ml + p.n_splits * all * 8;
   return p;
 }
@@ -167,11 +170,14 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   const bool int8 = d->fmt == WAL_KV_INT8;
   a.split = p.split;
   a.n_splits = p.n_splits;
-  a.part = static_cast<float*>(ws_dev);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws_dev) + p.off_ml);
+  uint8_t* ws_bytes_dev = static_cast<uint8_t*>(ws_dev);
+  a.part = reinterpret_cast<float*>(ws_bytes_dev + p.off_part);
+  a.part_ml = reinterpret_cast<float2*>(ws_bytes_dev + p.off_ml);
+  a.counters = p.join_here ? static_cast<uint32_t*>(ws_dev) : nullptr;
+  a.ones_done = p.stream;
   st = p.stream ? attn_stream(a, int8, d->head_dim, max_new * a.group <= 16 ? 1 : 2, stream)
                 : attn_tile(a, int8 ? kPagedInt8 : kPagedBf16, d->head_dim, stream);
-  return st || p.n_splits == 1 ? st : attn_join(a, d->head_dim, stream);
+  return st || p.n_splits == 1 || p.join_here ? st : attn_join(a, d->head_dim, stream);
 }
 
 extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk, const void* v_dev,

@@ -21,8 +21,9 @@
 // nothing in fp32 or bf16), so most tiles exchange nothing between lanes and
 // rescale nothing.
 //
-// Wavefronts join through LDS; when the context is split over workgroups, each
-// writes its sums in fp32 and k_attn_join adds them in the order of the splits.
+// Wavefronts join through LDS.  When the context is split over workgroups, each
+// writes its sums in fp32; up to kJoinHere pieces are added up, in their order, by the workgroup
+// that finishes last, more by k_attn_join.
 #include <hip/hip_runtime.h>
 
 #include "wal_attn.h"
@@ -120,13 +121,34 @@ __device__ __forceinline__ bf16x8_t v_operand(const Tile<FMT, D>& t, int e) {
   return as_bf16x8(w);
 }
 
+// Cache policy of a load or store that every compute unit of the GPU sees.
+constexpr int kAgent = 16;
+
+// The partial results of a sequence's rows in a piece (the whole of them below 2^32 bytes).
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t part_rsrc(const Attn& a, const Seq& q, uint32_t kvh, uint32_t piece, int32_t rows) {
+  return rsrc(a.part + part_row(a, piece, kvh, (uint64_t)q.first * a.group) * D, 4u * D * (uint32_t)rows);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ml_rsrc(const Attn& a, const Seq& q, uint32_t kvh, uint32_t piece, int32_t rows) {
+  return rsrc(a.part_ml + part_row(a, piece, kvh, (uint64_t)q.first * a.group), 8u * (uint32_t)rows);
+}
+
+// Four elements of query row r of the sequence and head: the sums over the sum of the weights.
+template <int D>
+__device__ __forceinline__ void store_row(const Attn& a, const Seq& q, uint32_t kvh, int32_t r, uint32_t d, f32x4_t acc, float sum) {
+  const int32_t tok = r / (int32_t)a.group;
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* p = a.out + (uint64_t)(q.first + tok) * a.ldo + (uint64_t)(kvh * a.group + r - tok * (int32_t)a.group) * D + d;
+  *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f)};
+}
+
 // Wavefronts a SIMD that the register allocator aims at.
-constexpr int stream_waves(int dim, int tiles) {
-  return dim * tiles <= 128 ? 3 : 2;
+constexpr int stream_waves(int fmt, int dim, int tiles) {
+  return dim * tiles <= 128 ? 3 : dim == 256 && fmt == kPagedBf16 ? 1 : 2;
 }
 
 template <int FMT, int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW, stream_waves(D, NT)) void k_attn_stream(Attn a) {
+__global__ __launch_bounds__(64 * NW, stream_waves(FMT, D, NT)) void k_attn_stream(Attn a) {
   constexpr int E = D / 16;
   constexpr bool kInt8 = FMT == kPagedInt8;
   __shared__ int64_t groups[kMaxSplit / 16 + 2];
@@ -138,7 +160,8 @@ __global__ __launch_bounds__(64 * NW, stream_waves(D, NT)) void k_attn_stream(At
   const Seq q = seq_of(a, s, true);
   const int32_t k0 = (int32_t)(sp * a.split), k1 = min(k0 + (int32_t)a.split, q.len);
   const int32_t nrows = q.rows * (int32_t)a.group;
-  if (!nrows || (k0 >= k1 && (sp || a.n_splits > 1))) return;
+  const int32_t pieces = max((q.len + (int32_t)a.split - 1) / (int32_t)a.split, 1);   // that have keys (an empty context: one)
+  if (!nrows || (int32_t)sp >= pieces) return;
 
   for (uint32_t i = threadIdx.x; i < (uint32_t)(max(k1 - k0, 0) + 31) / 32 * 2; i += 64 * NW) {
     const uint32_t key = (uint32_t)k0 + 16 * i;
@@ -327,17 +350,54 @@ __global__ __launch_bounds__(64 * NW, stream_waves(D, NT)) void k_attn_stream(At
         sum += f * lsh[w][row];
         acc += f * *reinterpret_cast<const f32x4_t*>(&osh[w][row][d]);
       }
-      if (a.n_splits == 1) {
-        const int32_t tok = r / (int32_t)a.group;
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-        uint16_t* p = a.out + (uint64_t)(q.first + tok) * a.ldo + (uint64_t)(kvh * a.group + r - tok * (int32_t)a.group) * D + d;
-        *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f)};
+      if (pieces == 1) {
+        store_row<D>(a, q, kvh, r, d, acc, sum);
+      } else if (a.counters) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc), part_rsrc<D>(a, q, kvh, sp, nrows), 4 * (r * D + d), 0, kAgent);
+        if (d == 0)
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, make_float2(top, sum)), ml_rsrc(a, q, kvh, sp, nrows), 8 * r, 0, kAgent);
       } else {
         const uint64_t slot = part_row(a, sp, kvh, (uint64_t)q.first * a.group + r);
         *reinterpret_cast<f32x4_t*>(a.part + slot * D + d) = acc;
         if (d == 0) a.part_ml[slot] = make_float2(top, sum);
       }
     }
+  }
+  if (pieces == 1 || !a.counters) return;
+
+  // The workgroup that counts itself last adds up the pieces, in their order.  Partial results go past the caches of one
+  // chiplet (kAgent) both ways: a fence would write a whole cache back for every piece.
+  __shared__ uint32_t before;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  uint32_t* counter = a.counters + (uint64_t)s * a.kv_heads + kvh;
+  if (threadIdx.x == 0) before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (before != (uint32_t)pieces - 1) return;
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // for the next call
+  for (uint32_t i = threadIdx.x; i < (uint32_t)nrows * (D / 4); i += 64 * NW) {
+    const uint32_t r = i / (D / 4), d = 4 * (i % (D / 4));
+    u32x2_t w[kJoinHere];
+    u32x4_t v[kJoinHere];
+#pragma unroll
+    for (int p = 0; p < kJoinHere; ++p)
+      if (p < pieces) {
+        w[p] = __builtin_amdgcn_raw_buffer_load_b64(ml_rsrc(a, q, kvh, p, nrows), 8 * r, 0, kAgent);
+        v[p] = __builtin_amdgcn_raw_buffer_load_b128(part_rsrc<D>(a, q, kvh, p, nrows), 4 * (r * D + d), 0, kAgent);
+      }
+    float top = kNoMax, sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < kJoinHere; ++p)
+      if (p < pieces) top = fmaxf(top, __uint_as_float(w[p][0]));
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < kJoinHere; ++p)
+      if (p < pieces) {
+        const float f = __builtin_amdgcn_exp2f(__uint_as_float(w[p][0]) - top);
+        sum += f * __uint_as_float(w[p][1]);
+        acc += f * __builtin_bit_cast(f32x4_t, v[p]);
+      }
+    store_row<D>(a, q, kvh, (int32_t)r, d, acc, sum);
   }
 }
 
@@ -356,8 +416,10 @@ __global__ __launch_bounds__(256) void k_attn_join(Attn a) {
   const uint32_t s = inside ? find_seq(a.starts, a.n_seqs, (int32_t)t) : 0;
   const Seq q = seq_of(a, s, true);
   const int32_t i = (int32_t)t - q.first;
-  const bool live = inside && i >= 0 && i < q.rows;
-  const uint32_t splits = live ? ((uint32_t)q.len + a.split - 1) / a.split : 0;
+  bool live = inside && i >= 0 && i < q.rows;
+  uint32_t splits = ((uint32_t)q.len + a.split - 1) / a.split;
+  if (a.ones_done && splits <= 1) live = false;   // attn_stream wrote the row itself
+  if (!live) splits = 0;
   const uint64_t step = (uint64_t)a.n * a.q_heads;
   const uint64_t slot = live ? part_row(a, 0, kvh, (uint64_t)t * a.group + h - kvh * a.group) : 0;
   const float2* ml = a.part_ml + slot;
@@ -416,8 +478,9 @@ void join(const Attn& a, hipStream_t s) {
 template <int FMT, int D>
 void launch(const Attn& a, uint32_t tiles, hipStream_t s) {
   const dim3 grid(a.n_splits * a.kv_heads * a.n_seqs);
-  if (tiles == 1 && stream_wide(a.n_seqs, a.kv_heads, a.max_len))
-    hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, 8>), grid, dim3(512), 0, s, a);
+  constexpr bool kRoom = D < 256 || FMT == kPagedInt8;   // for the registers of two wavefronts a SIMD
+  if (kRoom && tiles == 1 && stream_wide(a.n_seqs, a.kv_heads, a.max_len))
+    hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, kRoom ? 8 : 4>), grid, dim3(512), 0, s, a);
   else if (tiles == 1)
     hipLaunchKernelGGL((k_attn_stream<FMT, D, 1, 4>), grid, dim3(256), 0, s, a);
   else if constexpr (stream_rows(D) > 16)

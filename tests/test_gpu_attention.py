@@ -286,7 +286,9 @@ class Paged:
         new, most = self.max_new + slack[0], min(self.max_len + slack[1], self.tables.shape[1] * self.page)
         n = w.wal_attn_paged_workspace_size(d, self.group * self.heads, len(self.seqs), self.Q.shape[0], new, most)
         if ws is None:
-            ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device=dev())   # contents must not matter
+            ws = torch.full((max(n, w.WAL_ATTN_WS_ZERO_BYTES),), 0xFF, dtype=torch.uint8, device=dev())
+            ws[:w.WAL_ATTN_WS_ZERO_BYTES] = 0    # the rest must not matter
+        self.ws = ws
         self.args = (i32(self.tables), i32([n for n, _ in self.seqs]), i32(self.starts))
         w.wal_attn_paged(d, self.cache, *self.args, self.Q, out, ws, scale=scale, max_new=new, max_len=most,
                          stream=stream)
@@ -355,6 +357,25 @@ def test_scales(wal, seqs, scale, gain):
     print(f"scale {scale} gain {gain} {seqs}", flush=True)
     p = Paged(wal, seqs, 4, 2, 64, 16, BF16, seed=7, gain=gain)
     p.check(p.call(scale=scale), scale=scale)
+
+
+def test_one_workspace_for_calls_of_all_sizes(wal):
+    """Calls of changing sizes on one workspace, in every order: each leaves its first bytes zero for the next, whose
+    partial results lie elsewhere."""
+    cases = [Paged(wal, [(3000, 1), (40, 1), (1100, 1), (0, 1)], 4, 2, 128, 16, BF16, seed=21),
+             Paged(wal, [(2500, 2), (2100, 1)], 8, 1, 64, 64, INT8, seed=22),
+             Paged(wal, [(9001, 40)], 4, 1, 128, 64, BF16, seed=23), Paged(wal, [(30000, 1)], 4, 2, 128, 64, INT8, seed=24),
+             Paged(wal, [(1500 + 7 * i, 1) for i in range(40)], 2, 2, 64, 16, BF16, seed=25)]
+    size = max(wal.wal_attn_paged_workspace_size(p.d, p.group * p.heads, len(p.seqs), p.Q.shape[0], p.max_new, p.max_len)
+               for p in cases)
+    ws = torch.zeros(size, dtype=torch.uint8, device=dev())
+    want = [p.call().clone() for p in cases]
+    for order in ([0, 1, 2, 3, 4], [4, 0, 3, 1, 2], [2, 2, 4, 4, 1, 0, 3]):
+        for i in order:
+            assert torch.equal(cases[i].call(ws=ws), want[i]), (order, i)
+            assert not ws[:wal.WAL_ATTN_WS_ZERO_BYTES].any()
+    for p, w in zip(cases, want):
+        p.check(w)
 
 
 def test_bounds_larger_than_the_sequences(wal):
@@ -439,7 +460,7 @@ def test_prompt_equals_chunks_over_the_cache(wal):
         j = np.arange(at, at + c)
         wal.wal_kv_write(d, cache, i32(pages[j // page] * page + j % page), K[at:at + c], V[at:at + c])
         at += c
-        ws = torch.empty(max(16, wal.wal_attn_paged_workspace_size(d, 8, 1, c, c, at)), dtype=torch.uint8, device=dev())
+        ws = torch.zeros(max(16, wal.wal_attn_paged_workspace_size(d, 8, 1, c, c, at)), dtype=torch.uint8, device=dev())
         wal.wal_attn_paged(d, cache, i32(pages[None]), i32([at]), i32([0, c]), Q[at - c:at], out[at - c:at], ws,
                            max_new=c, max_len=at)
     q, k, v = (host(x).reshape(n, -1, dim) for x in (Q, K, V))
