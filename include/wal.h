@@ -661,7 +661,9 @@ int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const int32_t* slot
  *   q_dev       [n][ldq] bf16, q_heads (a multiple of kv_heads, at most
  *               64 kv_heads) heads side by side; out_dev [n][ldo] bf16;
  *               16-byte aligned rows; out must not overlap the inputs
- *   scale       finite
+ *   scale       finite, also times log2(e)
+ *   n, n_seqs and max_new are at most 2^24, max_len at most 2^30, n * q_heads
+ *               below 2^31
  *   ws          wal_attn_paged_workspace_size bytes, 256-byte aligned (NULL when
  *               that is 0).  Its first WAL_ATTN_WS_ZERO_BYTES bytes are zero
  *               before the first call; every call leaves them so, whatever its

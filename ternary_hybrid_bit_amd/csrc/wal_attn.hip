@@ -10,13 +10,14 @@ bool heads_ok(uint32_t q_heads, uint32_t kv_heads) {
   return q_heads && kv_heads && q_heads % kv_heads == 0 && q_heads / kv_heads <= 64;
 }
 
-constexpr uint32_t kMaxRows = 1u << 26;   // query rows, sequences and tokens of a call
+constexpr uint32_t kMaxRows = 1u << 24;   // query rows and sequences of a call: times 64 heads of a group in 31 bits
 constexpr uint32_t kMaxPitch = 1u << 26;  // elements from a row of keys to the next: 16 rows in 32 bits of bytes
 constexpr uint64_t kMaxPartBytes = 1ull << 28;   // partial results of a call with many rows: fewer pieces beyond
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The kernels multiply scores by a positive number only: masked ones are -infinity, so a
 // scale of zero becomes one too small to tell weights apart.
+bool scale_ok(float scale) { return fabsf(scale * kLog2e) < INFINITY; }
 void set_scale(Attn& a, float scale) {
   a.scale = fmaxf(fabsf(scale * kLog2e), 1e-30f);
   a.q_sign = scale < 0.f ? 0x80008000u : 0u;
@@ -45,9 +46,10 @@ struct Plan {
 //  * Many rows, one sequence: into as many pieces as give the fewest rounds of
 //    workgroups over the places for them, not below 512 keys, the joining counted as 1.5 % of
 //    the products (2048 tokens over 32768, 256 workgroups: 1140 us whole, 1161 in two pieces).
-//  * Many rows, several sequences: pieces of 1024 keys unless there are workgroups enough
-//    for four rounds (13 sequences up to 4100, 260 workgroups: 63 us whole, 55 in pieces of 2048
-//    keys, 49 of 1024, 52 of 512).
+//  * Many rows, several sequences: pieces that fill the places once if all contexts were
+//    the longest, from 128 to 1024 keys, unless there are workgroups enough for four rounds (13 sequences up to
+//    4100, 260 workgroups: 63 us whole, 55 in pieces of 2048 keys, 49 of 1024, 52 of 512; 6
+//    sequences up to 800, heads of 256: 42 us whole, 24 in pieces of 128 keys, 35 of 512).
 uint32_t piece(bool stream, uint32_t dim, uint32_t n_seqs, uint64_t items, uint32_t tile_rows, uint32_t max_len) {
   const auto up128 = [](uint64_t keys) { return (keys + 127) / 128 * 128; };
   if (stream) {
@@ -56,7 +58,11 @@ uint32_t piece(bool stream, uint32_t dim, uint32_t n_seqs, uint64_t items, uint3
     return (uint32_t)(keys < least ? least : keys > kMaxSplit ? kMaxSplit : keys);
   }
   const uint64_t places = tile_rows == 256 || dim > 128 ? 256 : 512;   // one workgroup on a compute unit, or two
-  if (n_seqs > 1) return items >= 4 * places ? max_len : 1024;
+  if (n_seqs > 1) {
+    if (items >= 4 * places) return max_len;
+    const uint64_t keys = up128(max_len * items / places);
+    return (uint32_t)(keys < 128 ? 128 : keys > 1024 ? 1024 : keys);
+  }
   uint32_t best = max_len;
   double least = 1e30;
   for (uint64_t n = 1; n <= 64; ++n) {
@@ -110,7 +116,7 @@ extern "C" int wal_attn_paged_workspace_size(const wal_kv_desc* d, uint32_t q_he
   if (st) return st;
   if (!bytes) return WAL_ERR_ARG;
   if (!heads_ok(q_heads, d->kv_heads) || n_seqs > kMaxRows || n > kMaxRows || max_new > kMaxRows ||
-      max_len > (1u << 30))
+      max_len > (1u << 30) || (uint64_t)n * q_heads > 0x7FFFFFFFull)
     return WAL_ERR_SHAPE;
   *bytes = plan_of(d, q_heads, n_seqs, n, max_new, max_len).bytes;
   return WAL_OK;
@@ -127,7 +133,7 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   if (st) return st;
   if ((st = wal_attn_paged_workspace_size(d, q_heads, n_seqs, n, max_new, max_len, &need))) return st;
   if (!cache_dev || !tables_dev || !lens_dev || !starts_dev || (need && !ws_dev)) return WAL_ERR_ARG;
-  if (!(scale - scale == 0.f) || (uint64_t)ldt * d->page_size < max_len) return WAL_ERR_ARG;
+  if (!scale_ok(scale) || (uint64_t)ldt * d->page_size < max_len) return WAL_ERR_ARG;
   const uint64_t width = (uint64_t)q_heads * d->head_dim;
   if ((st = check_rows(q_dev, ldq, width, WAL_X_BF16)) || (st = check_rows(out_dev, ldo, width, WAL_X_BF16))) return st;
   if (!aligned(cache_dev, 256) || !aligned(tables_dev, 4) || !aligned(lens_dev, 4) || !aligned(starts_dev, 4) ||
@@ -184,7 +190,7 @@ extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_de
                                uint32_t ldv, const int32_t* starts_dev, uint32_t n_seqs, uint32_t n, uint32_t max_len,
                                uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim, float scale, int causal,
                                void* out_dev, uint32_t ldo, void* stream) {
-  if (!starts_dev || !(scale - scale == 0.f)) return WAL_ERR_ARG;
+  if (!starts_dev || !scale_ok(scale)) return WAL_ERR_ARG;
   if (!heads_ok(q_heads, kv_heads) || kv_heads > 256 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
       n_seqs > kMaxRows || n > kMaxRows || max_len > kMaxRows || ldk > kMaxPitch || ldv > kMaxPitch)
     return WAL_ERR_SHAPE;

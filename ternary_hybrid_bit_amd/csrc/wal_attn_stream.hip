@@ -493,6 +493,7 @@ namespace wal {
 
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((uint64_t)a.n_splits * a.kv_heads * a.n_seqs > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
   if (int8) {
     if (dim == 64) launch<kPagedInt8, 64>(a, tiles, s);
     if (dim == 128) launch<kPagedInt8, 128>(a, tiles, s);

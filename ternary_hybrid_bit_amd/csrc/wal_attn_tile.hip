@@ -130,6 +130,9 @@ struct Stage {
         page_bytes((a_.kv_heads << a_.page_shift) * (D * kElem)), head_bytes((w_.kvh << a_.page_shift) * (D * kElem)),
         tab(kPaged ? a_.tables + (uint64_t)w_.s * a_.ldt : nullptr) {
     all_there = true;
+  }
+  // Looks through the workgroup's pages (with a barrier).
+  __device__ __forceinline__ void look_at_pages() {
     if constexpr (kPaged) {
       int bad = 0;
       if (w.k0 < w.kend)
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
   Work w;
   if (!find_work<KIND != kPacked>(a, 128, lane, w)) return;
   Rows32<KIND, D> r;
-  const St st(a, w, lane, wave);
+  St st(a, w, lane, wave);
   u32x4_t kr[St::kPasses], vr[St::kPasses];
   int32_t next_page[St::kPasses] = {}, next_scale = 0;
   bool there[St::kPasses];
@@ -517,12 +520,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
     if (kInt8 && wave < 2) st.put_scale(ssh[b], &odd[b], scale, kb);
   };
   if (tid < 2) odd[tid] = 0;
-  lds_barrier();
   if (w.k0 < w.kend) {
     st.load_pages(next_page, next_scale, w.k0);
     load(w.k0);
   }
   r.begin(a, w, wave, lane);   // with the first keys on their way
+  st.look_at_pages();
+  lds_barrier();
   if (w.k0 < w.kend) {
     store(0, w.k0);
     load(w.k0 + kKeys);
@@ -566,7 +570,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
   Work w;
   if (!find_work<KIND != kPacked>(a, 256, lane, w)) return;
   Rows32<KIND, D> r;
-  const St st(a, w, lane, wave);
+  St st(a, w, lane, wave);
   u32x4_t kr[St::kPasses], vr[St::kPasses];
   int32_t next_page[St::kPasses] = {}, next_scale = 0;
   bool kthere[St::kPasses] = {}, vthere[St::kPasses] = {};
@@ -629,6 +633,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_pair(Attn a) {
     load_rest(0);
   }
   r.begin(a, w, wave, lane);   // with the first keys on their way
+  st.look_at_pages();
   lds_barrier();
   if (tiles) {
     st.template put<false>(ksh[0], kplace, kr);

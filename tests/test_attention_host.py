@@ -178,12 +178,14 @@ def test_attn_paged_checks():
     assert f(n=0) == 0 and f(seqs=0) == 0 and f(new=0) == 0
     assert [f(desc=None), f(c=None), f(t=None), f(l=None), f(s=None), f(q=None), f(o=None)] == [ARG] * 7
     assert f(scale=float("nan")) == ARG and f(scale=float("inf")) == ARG
+    assert f(scale=3e38) == ARG                              # infinite times log2(e)
     assert f(ldt=3) == ARG                                   # the tables do not hold max_len tokens
     assert f(h=3) == SHAPE and f(h=0) == SHAPE and f(h=2 * 65, ldq=8320, ldo=8320) == SHAPE
     assert f(ldq=248) == ARG and f(ldq=260) == ALIGN and f(q=Q + 8) == ALIGN and f(c=C + 16) == ALIGN
     assert f(l=P + 1) == ALIGN and f(s=S + 2) == ALIGN and f(t=T + 2) == ALIGN
     assert f(o=Q) == ARG and f(o=C) == ARG and f(o=T) == ARG and f(o=P) == ARG and f(o=S) == ARG
-    assert size(h=3) == SHAPE
+    assert size(h=3) == SHAPE and size(n=(1 << 24) + 1) == SHAPE and size(most=(1 << 30) + 1) == SHAPE
+    assert size(h=128, n=1 << 24) == SHAPE                   # n * q_heads
     many = size(seqs=1, n=1, new=1, most=128)
     assert many >= 0 and need >= 0
     split = wal.wal_attn_paged_workspace_size(wal.make_kv_desc(8192, 16, 2, 64, 0), 4, 1, 1, 1, 131072)
