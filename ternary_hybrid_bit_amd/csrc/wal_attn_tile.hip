@@ -1,7 +1,7 @@
 // Attention of many query rows for gfx950: chunks of a prompt over the paged
 // cache, and whole prompts packed one after another.
 //
-// Bound by the matrix cores.  A workgroup takes 32 QT NW query rows of one key/value
+// Bound by the matrix cores.  A workgroup takes 128 or 256 query rows of one key/value
 // head (a row is one token of one of the query heads that share the head, token by
 // token, so that the rows of a workgroup see nearly the same keys) and runs over
 // tiles of 64 keys, staged in LDS by all its wavefronts: from memory to registers
@@ -23,6 +23,12 @@
 // The softmax is the running one with a maximum that follows only rises above 8
 // (a factor of 2^8); a lane adds up its own keys' weights and the two halves of a
 // row meet once, at the end.
+//
+// Measured: a prompt of 8192 (32 query, 8 key/value heads of 128) 532 us, 1.03 PFLOP/s;
+// 2048 tokens over 32768 of the int8 cache 1149 us, 0.93 PFLOP/s, its vector
+// instructions 3.0 times the prompt's for 1.9 times the products (k_attn_pair); 9 packed
+// prompts up to 777, heads of 256, 40 us; 13 chunks over up to 4100, heads of 64, 44 us and 8
+// to join (k_attn_tile).
 #include <hip/hip_runtime.h>
 
 #include "wal_attn.h"
