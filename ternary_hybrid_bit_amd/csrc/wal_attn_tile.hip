@@ -179,6 +179,10 @@ struct Stage {
     return kPaged ? 16 * lane : lane / kPieces * (2 * ld) + 16 * (lane % kPieces);
   }
   __device__ __forceinline__ uint32_t last_lane_offset(uint32_t ld, int32_t kb, int p) const {
+    if constexpr (kWaveRows == 2) {   // nor is a branch needed: the second row is a step of zero away
+      const uint32_t step = start(kb, p) + 1 < w.kend ? 2 * ld : 0;
+      return (lane < 32 ? 0 : step) + 16 * (lane % 32);
+    }
     return min(lane / kPieces, (uint32_t)(w.kend - 1 - start(kb, p))) * (2 * ld) + 16 * (lane % kPieces);
   }
   __device__ __forceinline__ bool is_last(int32_t kb) const { return !kPaged && kb + kKeys > w.kend; }
@@ -393,8 +397,11 @@ struct Rows32 {
       const float mn = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= f;
+      if (D <= 128 || kb != st.w.k0) {   // before the first tile they are 0, and wide ones costly to move to and fro
 #pragma unroll
-      for (int e = 0; e < kMT; ++e) o[e] *= f;
+        for (int e = 0; e < kMT; ++e) o[e] *= f;
+      }
+      keep_places();
     }
     float sum[4] = {};
 #pragma unroll
@@ -438,6 +445,7 @@ struct Rows32 {
           o[e][i] += j <= last && !(fabsf(y) < INFINITY) ? y : 0.f;
         }
     }
+    keep_places();
   }
   __device__ __forceinline__ void finish(const Attn& a, const Work& w) {
     l += __shfl_xor(l, 32);
@@ -512,7 +520,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(Attn a) {
       there[p] = !St::kPaged || st.on_page(next_page[p]);
       const uint64_t kat = st.offset(next_page[p], kb, p, (uint32_t)a.ldk);
       const uint64_t vat = St::kPaged ? kat : st.offset(next_page[p], kb, p, (uint32_t)a.ldv);
-      const bool cut = st.is_last(kb);
+      const bool cut = !St::kPaged && (St::kWaveRows == 2 || st.is_last(kb));
       kr[p] = st.fetch(kplane, kat, cut ? st.last_lane_offset((uint32_t)a.ldk, kb, p) : klane);
       vr[p] = st.fetch(vplane, vat, cut ? st.last_lane_offset((uint32_t)a.ldv, kb, p) : vlane);
     }
