@@ -50,7 +50,7 @@ struct Plan {
 //  * Many rows, several sequences: pieces that fill the places once if all contexts were
 //    the longest, from 128 to 1024 keys, unless there are workgroups enough for four rounds (13 sequences up to
 //    4100, at most 260 workgroups: 63 us whole, 55 in pieces of 2048 keys, 49 of 1024, 52 of 512; 6
-//    sequences up to 800, heads of 256: 42 us whole, 24 in pieces of 128 keys, 35 of 512).
+//    sequences up to 800, heads of 256: 42 us whole, 24 in pieces of 128 keys (23 with a later step), 35 of 512).
 uint32_t piece(bool stream, uint32_t dim, uint32_t n_seqs, uint64_t items, uint32_t tile_rows, uint32_t max_len) {
   const auto up128 = [](uint64_t keys) { return (keys + 127) / 128 * 128; };
   if (stream) {

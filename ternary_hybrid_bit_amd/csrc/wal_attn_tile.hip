@@ -27,7 +27,7 @@
 // Measured: a prompt of 8192 (32 query, 8 key/value heads of 128) 532 us, 1.03 PFLOP/s;
 // 2048 tokens over 32768 of the int8 cache 1149 us, 0.93 PFLOP/s, its vector
 // instructions 3.0 times the prompt's for 1.9 times the products (k_attn_pair); 9 packed
-// prompts up to 777, heads of 256, 40 us; 13 chunks over up to 4100, heads of 64, 44 us and 8
+// prompts up to 777, heads of 256, 37 us; 13 chunks over up to 4100, heads of 64, 44 us and 8
 // to join (k_attn_tile).
 #include <hip/hip_runtime.h>
 
