@@ -4,6 +4,7 @@
 
 #include "wal_args.h"
 #include "wal_device.h"
+#include "wal_seq.h"
 
 namespace wal {
 
@@ -73,20 +74,8 @@ __device__ __forceinline__ uint64_t part_row(const Attn& a, uint32_t split, uint
   return ((uint64_t)split * a.kv_heads + kvh) * ((uint64_t)a.n * a.group) + row;
 }
 
-// A sequence's part of a call, cut to the rows and tokens that there are
-// whatever starts and lens hold.
-struct Seq {
-  int32_t first, rows, len, old;   // first query row, rows, tokens, tokens before the first row's own
-};
-
 __device__ __forceinline__ Seq seq_of(const Attn& a, uint32_t s, bool paged) {
-  Seq q;
-  q.first = max(a.starts[s], 0);
-  const int32_t new_s = min(a.starts[s + 1], (int32_t)a.n) - q.first;
-  q.rows = max(min(new_s, (int32_t)a.max_new), 0);
-  q.len = max(min(paged ? a.lens[s] : new_s, (int32_t)a.max_len), 0);
-  q.old = paged ? q.len - new_s : 0;
-  return q;
+  return cut_seq(a.starts[s], a.starts[s + 1], paged ? a.lens[s] : 0, (int32_t)a.n, (int32_t)a.max_new, (int32_t)a.max_len, paged);
 }
 
 // The sequence of query row t: the last s with starts[s] <= t.
