@@ -250,13 +250,14 @@ __global__ __launch_bounds__(64 * NW, stream_waves(FMT, D, NT)) void k_attn_stre
     if (more) load_k<FMT, D>(kv, a, groups, g + 2 * NW, lane);
 
     uint32_t odd = 0;   // an infinity or NaN among the values of a tile that some row sees only in part
+    int32_t upto[NT];   // the last of the lane's eight keys that its row sees
+#pragma unroll
+    for (int t = 0; t < NT; ++t) upto[t] = full ? 7 : there ? last[t] - kb - 8 * (int32_t)c : -1;
     if (!full) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int32_t upto = there ? last[t] - kb - 8 * (int32_t)c : -1;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[t][i / 4][i % 4] = i <= upto ? x[t][i / 4][i % 4] : -INFINITY;
-      }
+        for (int i = 0; i < 8; ++i) x[t][i / 4][i % 4] = i <= upto[t] ? x[t][i / 4][i % 4] : -INFINITY;
       if constexpr (!kInt8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -288,10 +289,8 @@ __global__ __launch_bounds__(64 * NW, stream_waves(FMT, D, NT)) void k_attn_stre
       }
       if constexpr (kInt8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = y[i] * kv.vs[i];
-          y[i] = y[i] == 0.f ? 0.f : z;   // a key that is not seen, whatever its scale
-        }
+        for (int i = 0; i < 8; ++i)   // a key that is not seen: 0 whatever its scale; one that is, NaN if that is, at a weight of 0 too
+          y[i] = i <= upto[t] ? y[i] * kv.vs[i] : 0.f;
       }
 #pragma unroll
       for (int p = 0; p < 4; ++p) w[p] = pack_bf16(y[2 * p], y[2 * p + 1]);

@@ -28,3 +28,28 @@ def test_extreme_starts_stay_inside(wal, starts, max_new):  # noqa: F811
     torch.cuda.synchronize()
     assert (wide[:8] == 77.0).all() and (wide[16:] == 77.0).all()
     assert not ws[:wal.WAL_ATTN_WS_ZERO_BYTES].any()
+
+
+@pytest.mark.parametrize("fmt", [BF16, INT8])
+@pytest.mark.parametrize("n,new,dim", [(200, 1, 128), (200, 1, 64), (200, 4, 256), (200, 7, 128), (200, 50, 128),
+                                       (2900, 1, 128), (2900, 30, 64)])
+@pytest.mark.parametrize("where", ["seen by all", "seen by some"])
+def test_nan_of_a_weight_that_underflows(wal, fmt, n, new, dim, where):  # noqa: F811
+    """One key takes all the weight: a seen value row that is NaN makes its rows NaN though its weight is 0 in fp32, in
+    every kernel; rows that do not see it stay numbers."""
+    print(f"n={n} new={new} dim={dim} fmt={fmt} {where}", flush=True)
+    p = Paged(wal, [(n, new), (80, 1)], 4, 1, dim, 16, fmt, seed=31)
+    p.Q[:] = p.Q[:1, :dim].repeat(p.Q.shape[0], 4)                 # every row and head asks the same
+    # in one tile of the kernels for few rows, so that the same wavefront holds the maximum
+    bad = 20 if where == "seen by all" else n - new // 2 - 1
+    hot = min(bad - 2, n - new)
+    K = torch.cat([p.Q[:1, :dim].float() * 40, torch.zeros((1, dim), device=dev())])   # a score of 40 sqrt(dim): > 300
+    V = torch.ones((2, dim), device=dev())
+    V[1, 5] = float("nan")
+    wal.wal_kv_write(p.d, p.cache, p.slots[[hot, bad]].contiguous(), K, V)
+    got = host(p.call()).reshape(-1, 4, dim)
+    sees = np.append(n - new + np.arange(new) >= bad, False)
+    assert sees.any()
+    nan = np.isnan(got[sees]) if fmt == INT8 else np.isnan(got[sees][..., 5:6])   # int8: the whole row's scale
+    assert nan.all() and np.isfinite(got[~sees]).all()
+    assert (got[:new][~sees[:new]] == 1.0).all()                   # the hot key's value
