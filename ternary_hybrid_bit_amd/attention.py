@@ -10,7 +10,7 @@ Everything on the GPU is libwal's; this module keeps the page lists.
 """
 from __future__ import annotations
 
-from typing import List, Sequence, Tuple
+from typing import List, Sequence
 
 import numpy as np
 
@@ -53,17 +53,28 @@ class AttentionLayer:
             return wal_gemm_small(info, W, X, Y, ws=self._workspace("product", wal_workspace_size(info, X.shape[0])))
         return wal_gemm_prefill(info, W, X, Y, ws=self._workspace("prompt", wal_prefill_workspace_size(info, X.shape[0])))
 
-    def _append(self, seqs: Sequence[int], new: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
-        """Pages for the new tokens: their cache slots and positions."""
-        size, slots, pos = self.desc.page_size, [], []
+    def _place(self, seqs: Sequence[int], new: Sequence[int]):
+        """Where the new tokens go: their cache slots and positions, the sequences' pages with those that they
+        need besides, and their lengths.  Nothing is changed yet."""
+        size, slots, pos, pages, lens = self.desc.page_size, [], [], [], []
+        left = len(self.free)
         for s, n in zip(seqs, new):
             t = np.arange(self.lens[s], self.lens[s] + n)
-            while len(self.pages[s]) * size < self.lens[s] + n:
-                self.pages[s].append(self.free.pop())
-            slots.append(np.asarray(self.pages[s], np.int64)[t // size] * size + t % size if n else t)
+            more = max(-(-(self.lens[s] + n) // size) - len(self.pages[s]), 0)
+            if more > left:
+                raise RuntimeError(f"sequence {s} needs {more} more pages; the cache has {left} left")
+            pages.append(self.pages[s] + self.free[left - more:left])
+            left -= more
+            slots.append(np.asarray(pages[-1], np.int64)[t // size] * size + t % size if n else t)
             pos.append(t)
-            self.lens[s] += n
-        return np.concatenate(slots).astype(np.int32), np.concatenate(pos).astype(np.int32)
+            lens.append(self.lens[s] + n)
+        return np.concatenate(slots).astype(np.int32), np.concatenate(pos).astype(np.int32), pages, lens
+
+    def _keep(self, seqs: Sequence[int], pages: List[List[int]], lens: List[int]):
+        """Counts the tokens of a call as kept in the cache, and their pages as taken."""
+        del self.free[len(self.free) - sum(len(p) - len(self.pages[s]) for s, p in zip(seqs, pages)):]
+        for s, p, n in zip(seqs, pages, lens):
+            self.pages[s], self.lens[s] = p, n
 
     def release(self, s: int):
         self.free += self.pages[s]
@@ -71,13 +82,19 @@ class AttentionLayer:
 
     def attend(self, Q, K, V, seqs: Sequence[int], new: Sequence[int]):
         """The part between the products: Q, K, V (fp32 or bf16) of new[i] tokens of
-        sequence seqs[i] each, one after another -> bf16 [n][q_heads * head_dim]."""
+        sequence seqs[i] each, one after another -> bf16 [n][q_heads * head_dim].  A call that raises, for want of
+        pages (RuntimeError: release a sequence and call again) or otherwise, leaves the sequences as they were."""
+        out, pages, lens = self._attend(Q, K, V, seqs, new)
+        self._keep(seqs, pages, lens)
+        return out
+
+    def _attend(self, Q, K, V, seqs: Sequence[int], new: Sequence[int]):
+        """attend() up to its launches, and the sequences' pages and lengths after it."""
         torch = self.torch
-        slots, pos = self._append(seqs, new)
-        lens = [self.lens[s] for s in seqs]
-        tables = np.zeros((len(seqs), max(1, max(len(self.pages[s]) for s in seqs))), np.int32)
-        for i, s in enumerate(seqs):
-            tables[i, :len(self.pages[s])] = self.pages[s]
+        slots, pos, pages, lens = self._place(seqs, new)
+        tables = np.zeros((len(seqs), max(1, max(len(p) for p in pages))), np.int32)
+        for i, p in enumerate(pages):
+            tables[i, :len(p)] = p
         slots, pos, lens_dev, starts, tables = self._put(slots, pos, lens, np.cumsum([0] + list(new)), tables)
         q, out = (torch.empty(Q.shape, dtype=torch.bfloat16, device=self.dev) for _ in range(2))
         wal_kv_write(self.desc, self.cache, slots, K, V, pos=pos, turns=self.turns, layout=self.layout,
@@ -85,8 +102,8 @@ class AttentionLayer:
         max_new, max_len = max(new), max(lens)
         ws = self._workspace("attention", wal_attn_paged_workspace_size(self.desc, self.q_heads, len(seqs),
                                                                         Q.shape[0], max_new, max_len))
-        return wal_attn_paged(self.desc, self.cache, tables, lens_dev, starts, q, out, ws, max_new=max_new,
-                              max_len=max_len)
+        wal_attn_paged(self.desc, self.cache, tables, lens_dev, starts, q, out, ws, max_new=max_new, max_len=max_len)
+        return out, pages, lens
 
     def _put(self, *arrays):
         """int32 arrays to the GPU in one copy."""
@@ -96,9 +113,13 @@ class AttentionLayer:
         return [flat[i:j].view(x.shape) for x, i, j in zip(arrays, at[:-1], at[1:])]
 
     def forward(self, X, seqs: Sequence[int], new: Sequence[int]):
-        """X bf16 [n][hidden] -> fp32 [n][hidden], the new tokens of the sequences kept in the cache."""
+        """X bf16 [n][hidden] -> fp32 [n][hidden], the new tokens of the sequences kept in the cache (of none of them,
+        if the call raises)."""
         Q, K, V = (self._product(m, X) for m in self.mats[:3])
-        return self._product(self.mats[3], self.attend(Q, K, V, seqs, new))
+        out, pages, lens = self._attend(Q, K, V, seqs, new)
+        Y = self._product(self.mats[3], out)
+        self._keep(seqs, pages, lens)
+        return Y
 
     def prompt(self, X, lens: Sequence[int]):
         """The same for whole prompts that need no cache (scoring): X bf16, prompts one after another."""
