@@ -10,6 +10,7 @@ Everything on the GPU is libwal's; this module keeps the page lists.
 """
 from __future__ import annotations
 
+from operator import index
 from typing import List, Sequence
 
 import numpy as np
@@ -17,6 +18,17 @@ import numpy as np
 from . import (WAL_KV_BF16, WAL_MAX_BATCH, WAL_ROPE_HALF, make_kv_desc, make_rope_desc, wal_attn_paged,
                wal_attn_paged_workspace_size, wal_attn_prompt, wal_gemm_prefill, wal_gemm_small, wal_kv_size,
                wal_kv_write, wal_prefill_workspace_size, wal_rope, wal_rope_freqs, wal_workspace_size)
+
+
+def _counts(new: Sequence[int], *rows) -> List[int]:
+    """Counts of tokens, whose sum is every tensor's number of rows."""
+    new = [index(n) for n in new]
+    if not new or min(new) < 0:
+        raise ValueError(f"counts of tokens {new}: at least one, none below 0")
+    for t in rows:
+        if t.shape[0] != sum(new):
+            raise ValueError(f"{t.shape[0]} rows for {sum(new)} tokens")
+    return new
 
 
 class AttentionLayer:
@@ -53,6 +65,21 @@ class AttentionLayer:
             return wal_gemm_small(info, W, X, Y, ws=self._workspace("product", wal_workspace_size(info, X.shape[0])))
         return wal_gemm_prefill(info, W, X, Y, ws=self._workspace("prompt", wal_prefill_workspace_size(info, X.shape[0])))
 
+    def _checked(self, seqs: Sequence[int], new: Sequence[int], *rows):
+        """seqs and new as lists of int: distinct sequences of the layer with as many new tokens as each tensor has rows."""
+        seqs, new = [index(s) for s in seqs], _counts(new, *rows)
+        if len(seqs) != len(new):
+            raise ValueError(f"{len(seqs)} sequences with {len(new)} counts of new tokens")
+        if len(set(seqs)) != len(seqs):
+            raise ValueError(f"a sequence more than once in {seqs}")
+        for s in seqs:
+            self._known(s)
+        return seqs, new
+
+    def _known(self, s: int):
+        if not 0 <= s < len(self.lens):
+            raise ValueError(f"sequence {s} of a layer with {len(self.lens)}")
+
     def _place(self, seqs: Sequence[int], new: Sequence[int]):
         """Where the new tokens go: their cache slots and positions, the sequences' pages with those that they
         need besides, and their lengths.  Nothing is changed yet."""
@@ -63,7 +90,7 @@ class AttentionLayer:
             more = max(-(-(self.lens[s] + n) // size) - len(self.pages[s]), 0)
             if more > left:
                 raise RuntimeError(f"sequence {s} needs {more} more pages; the cache has {left} left")
-            pages.append(self.pages[s] + self.free[left - more:left])
+            pages.append(self.pages[s] + self.free[left - more:left] if more else self.pages[s])
             left -= more
             slots.append(np.asarray(pages[-1], np.int64)[t // size] * size + t % size if n else t)
             pos.append(t)
@@ -77,6 +104,7 @@ class AttentionLayer:
             self.pages[s], self.lens[s] = p, n
 
     def release(self, s: int):
+        self._known(s)
         self.free += self.pages[s]
         self.pages[s], self.lens[s] = [], 0
 
@@ -84,6 +112,7 @@ class AttentionLayer:
         """The part between the products: Q, K, V (fp32 or bf16) of new[i] tokens of
         sequence seqs[i] each, one after another -> bf16 [n][q_heads * head_dim].  A call that raises, for want of
         pages (RuntimeError: release a sequence and call again) or otherwise, leaves the sequences as they were."""
+        seqs, new = self._checked(seqs, new, Q, K, V)
         out, pages, lens = self._attend(Q, K, V, seqs, new)
         self._keep(seqs, pages, lens)
         return out
@@ -95,7 +124,7 @@ class AttentionLayer:
         tables = np.zeros((len(seqs), max(1, max(len(p) for p in pages))), np.int32)
         for i, p in enumerate(pages):
             tables[i, :len(p)] = p
-        slots, pos, lens_dev, starts, tables = self._put(slots, pos, lens, np.cumsum([0] + list(new)), tables)
+        slots, pos, lens_dev, starts, tables = self._put(slots, pos, lens, np.cumsum([0] + new), tables)
         q, out = (torch.empty(Q.shape, dtype=torch.bfloat16, device=self.dev) for _ in range(2))
         wal_kv_write(self.desc, self.cache, slots, K, V, pos=pos, turns=self.turns, layout=self.layout,
                      magnitude=self.magnitude, Q=Q, Q_out=q)
@@ -115,6 +144,7 @@ class AttentionLayer:
     def forward(self, X, seqs: Sequence[int], new: Sequence[int]):
         """X bf16 [n][hidden] -> fp32 [n][hidden], the new tokens of the sequences kept in the cache (of none of them,
         if the call raises)."""
+        seqs, new = self._checked(seqs, new, X)
         Q, K, V = (self._product(m, X) for m in self.mats[:3])
         out, pages, lens = self._attend(Q, K, V, seqs, new)
         Y = self._product(self.mats[3], out)
@@ -123,13 +153,13 @@ class AttentionLayer:
 
     def prompt(self, X, lens: Sequence[int]):
         """The same for whole prompts that need no cache (scoring): X bf16, prompts one after another."""
-        torch = self.torch
+        torch, lens = self.torch, _counts(lens, X)
         Q, K, V = (self._product(m, X) for m in self.mats[:3])
         pos = torch.from_numpy(np.concatenate([np.arange(n) for n in lens]).astype(np.int32)).to(self.dev)
         q, k = (torch.empty(t.shape, dtype=torch.bfloat16, device=self.dev) for t in (Q, K))
         for t, r in ((Q, q), (K, k)):
             wal_rope(t, r, pos, self.turns, self.head_dim, layout=self.layout, magnitude=self.magnitude)
-        starts = torch.tensor(np.cumsum([0] + list(lens)), dtype=torch.int32, device=self.dev)
+        starts = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device=self.dev)
         out = torch.empty_like(q)
         wal_attn_prompt(q, k, V.to(torch.bfloat16), starts, out, self.head_dim, max(lens))
         return self._product(self.mats[3], out)

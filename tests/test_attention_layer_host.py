@@ -99,6 +99,35 @@ def test_a_failing_launch_changes_nothing(monkeypatch):
     assert state(a) == before
 
 
+@pytest.mark.parametrize("seqs,new,n", [
+    ([0, 0], [2, 3], (5,)),                # a sequence twice: its first rows would see its last tokens
+    ([0, 1], [5], (5,)), ([0], [3, 2], (5,)),
+    ([0], [6], (5,)), ([0], [4], (5,)),    # counts and rows
+    ([0], [5], (5, 4)), ([0], [5], (5, 5, 6)), ([0], [5], (4, 5, 5)),
+    ([0, 1], [6, -1], (5,)), ([2], [5], (5,)), ([-1], [5], (5,)), ([], [], (0,)),
+])
+def test_refusals(calls, seqs, new, n):
+    a = layer(8, 2)
+    before = state(a)
+    with pytest.raises(ValueError):
+        a.attend(*rows(*n), seqs, new)
+    assert state(a) == before and not calls
+
+
+def test_refusals_of_other_calls(monkeypatch):
+    a = layer(8, 2)
+    with pytest.raises(TypeError):
+        a.attend(*rows(5), [0], [5.0])
+    for s in (-1, 2):
+        with pytest.raises(ValueError):
+            a.release(s)
+    monkeypatch.setattr(a, "_product", lambda m, X: torch.zeros((X.shape[0], m[0].d.out)))
+    for lens in ([], [4], [6], [6, -1]):
+        with pytest.raises(ValueError, match="tokens|prompt"):
+            a.prompt(torch.zeros((5, 256)), lens)
+    assert state(a) == ([*range(8)], [[], []], [0, 0])
+
+
 def test_counts_may_be_numpy_numbers(calls):
     a = layer(8, 2)
     a.attend(*rows(5), np.array([1, 0]), np.array([2, 3]))
