@@ -3,6 +3,8 @@ tolerance of test_gpu_attention_layer.py."""
 import numpy as np
 import pytest
 
+from oracle import attention as A
+
 from test_gpu_attention_layer import D, HIDDEN, host, mats, mod, reference  # noqa: F401
 
 torch = pytest.importorskip("torch")
@@ -33,3 +35,26 @@ def test_again_after_the_pages_ran_out(mod, mats):  # noqa: F811
     got[first] = layer.attend(Q[first], K[first], V[first], [0, 1, 2], [13, 39, 23]).float()
     got[last] = layer.attend(Q[last], K[last], V[last], [0, 1], [3, 1]).float()
     assert (np.abs(host(got) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("lens", [[50, 20], [1], [129, 3, 0, 64]])
+def test_prompt_per_element(mod, mats, lens, monkeypatch):  # noqa: F811
+    """What prompt() hands to the last product is, per element, the attention of the rotated q and k; the rest of prompt() is that product."""
+    X = inputs(sum(lens), 9)
+    layer = mod.AttentionLayer(*mats, head_dim=D, n_pages=1, max_seqs=1, page_size=16)
+    ref, bound = reference(layer, X, lens)
+    product, seen = layer._product, []
+
+    def keep(m, x):
+        if m is layer.mats[3]:
+            seen.append(x)
+        return product(m, x)
+    layer._product = keep
+    whole = layer.prompt(X, lens)
+    got = host(seen[0])
+    assert len(seen) == 1 and (np.abs(got - ref) <= bound).all()
+    assert torch.equal(whole, product(layer.mats[3], seen[0]))
+    if max(lens) > 1:                           # an oracle that does not rotate is told apart
+        monkeypatch.setattr(A, "rope_freqs", lambda rot, base: (np.zeros(rot // 2), 1.0))
+        still, bound = reference(layer, X, lens)
+        assert not (np.abs(got - still) <= bound).all()
