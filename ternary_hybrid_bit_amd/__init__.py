@@ -893,13 +893,15 @@ def wal_attn_paged_workspace_size(desc: wal_kv_desc, q_heads: int, n_seqs: int, 
 
 
 def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=None, scale: Optional[float] = None,
-                   max_new: int = 1, max_len: int = 0, stream=None):
+                   max_new: Optional[int] = None, max_len: int = 0, stream=None):
     """out = attention of Q's rows over the paged cache: tables int32
     [n_seqs][pages], lens int32 [n_seqs], starts int32 [n_seqs + 1], Q and out
     bf16 [n][q_heads * head_dim], ws of wal_attn_paged_workspace_size bytes, the
     first WAL_ATTN_WS_ZERO_BYTES of them zero before its first call (torch.zeros).
     scale: 1 / sqrt(head_dim) unless given; max_new and max_len bound the
-    sequences' new tokens and lengths (max_len 0: what the tables hold)."""
+    sequences' new tokens and lengths: rows and tokens past them are not computed.
+    max_new left out: 1 if there are no more rows than sequences (a token each),
+    else as many as Q has rows; max_len 0: what the tables hold."""
     T = _types()
     _kv_cache(T, desc, cache)
     dim = desc.head_dim
@@ -911,6 +913,8 @@ def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=No
     _, _, ldo = _mat(T, out, "out", T.only_bf16, cols, n)
     holds = pages * desc.page_size
     max_len = max_len or holds
+    if max_new is None:
+        max_new = 1 if n <= n_seqs else n
     if max_new < 0 or max_len < 0 or max_len > holds:
         raise ValueError(f"max_new {max_new}, max_len {max_len}: the tables hold {holds}")
     wsp, wsb = None, 0

@@ -53,3 +53,16 @@ def test_nan_of_a_weight_that_underflows(wal, fmt, n, new, dim, where):  # noqa:
     nan = np.isnan(got[sees]) if fmt == INT8 else np.isnan(got[sees][..., 5:6])   # int8: the whole row's scale
     assert nan.all() and np.isfinite(got[~sees]).all()
     assert (got[:new][~sees[:new]] == 1.0).all()                   # the hot key's value
+
+
+@pytest.mark.parametrize("seqs", [[(300, 40)], [(90, 5), (40, 1)], [(64, 64), (0, 0), (7, 7)], [(200, 1), (33, 1)]])
+def test_max_new_left_out(wal, seqs):  # noqa: F811
+    """Every row is computed when the call is not told how many new tokens the sequences have."""
+    p = Paged(wal, seqs, 4, 2, 128, 16, BF16, seed=41)
+    p.call()                                   # (makes the arguments)
+    n = p.Q.shape[0]
+    ws = torch.zeros(max(wal.WAL_ATTN_WS_ZERO_BYTES, wal.wal_attn_paged_workspace_size(
+        p.d, 8, len(seqs), n, n, p.tables.shape[1] * 16)), dtype=torch.uint8, device=dev())
+    out = torch.full((n, p.Q.shape[1]), 77.0, dtype=torch.bfloat16, device=dev())
+    wal.wal_attn_paged(p.d, p.cache, *p.args, p.Q, out, ws)
+    p.check(out)
