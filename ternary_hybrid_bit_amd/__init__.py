@@ -726,6 +726,9 @@ def _types() -> _Types:
     return _types_made
 
 
+_U32_MAX = 0xFFFFFFFF   # ctypes would pass the low 32 bits of anything larger
+
+
 def _mat(T, t, name: str, dtypes, cols: int, rows: int = 0):
     """A 2-D device matrix of one of the dtypes with at least so many columns
     and rows, unit stride along its rows, rows apart: (rows, columns, row pitch)."""
@@ -748,6 +751,8 @@ def _mat(T, t, name: str, dtypes, cols: int, rows: int = 0):
         ld = c if ld < c else ld   # the pitch of an only row means nothing
     elif ld < c:
         raise ValueError(f"{name} rows overlap (stride {ld} < {c})")
+    if (n | ld) > _U32_MAX:
+        raise ValueError(f"{name} has {n} rows, {ld} elements apart: more than 32 bits hold")
     return n, c, ld
 
 
@@ -764,6 +769,8 @@ def _vec(T, t, name: str, dtype, n: int) -> int:
         raise ValueError(f"{name} holds {shape[0]} elements; at least {n} are needed")
     if shape[0] > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
+    if shape[0] > _U32_MAX:
+        raise ValueError(f"{name} holds {shape[0]} elements: more than 32 bits hold")
     return shape[0]
 
 
@@ -886,6 +893,8 @@ def wal_kv_read(desc: wal_kv_desc, cache, slots, K=None, V=None, stream=None):
 
 def wal_attn_paged_workspace_size(desc: wal_kv_desc, q_heads: int, n_seqs: int, n: int, max_new: int,
                                   max_len: int) -> int:
+    if max(q_heads, n_seqs, n, max_new, max_len) > _U32_MAX:
+        raise ValueError(f"q_heads {q_heads}, n_seqs {n_seqs}, n {n}, max_new {max_new}, max_len {max_len}: more than 32 bits hold")
     b = _SZ()
     _check(_lib.wal_attn_paged_workspace_size(ctypes.byref(desc), q_heads, n_seqs, n, max_new, max_len,
                                               ctypes.byref(b)), "wal_attn_paged_workspace_size")
@@ -915,7 +924,7 @@ def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=No
     max_len = max_len or holds
     if max_new is None:
         max_new = 1 if n <= n_seqs else n
-    if max_new < 0 or max_len < 0 or max_len > holds:
+    if not 0 <= max_new <= _U32_MAX or not 0 <= max_len <= min(holds, _U32_MAX):
         raise ValueError(f"max_new {max_new}, max_len {max_len}: the tables hold {holds}")
     wsp, wsb = None, 0
     if ws is not None:
@@ -947,7 +956,7 @@ def wal_attn_prompt(Q, K, V, starts, out, head_dim: int, max_len: int, scale: Op
     _, _, ldv = _mat(T, V, "V", T.only_bf16, kv_cols, n)
     _, _, ldo = _mat(T, out, "out", T.only_bf16, cols, n)
     n_seqs = _vec(T, starts, "starts", T.i32, 1) - 1
-    if max_len < 0:
+    if not 0 <= max_len <= _U32_MAX:
         raise ValueError(f"max_len {max_len}")
     if not (Q.is_cuda and K.is_cuda and V.is_cuda and starts.is_cuda and out.is_cuda):
         _gpu(Q=Q, K=K, V=V, starts=starts, out=out)
