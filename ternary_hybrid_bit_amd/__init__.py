@@ -748,7 +748,7 @@ def _mat(T, t, name: str, dtypes, cols: int, rows: int = 0):
     if step != 1 and c > 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
     if n <= 1:
-        ld = c if ld < c else ld   # the pitch of an only row means nothing
+        ld = (c + 7) & ~7   # the pitch of an only row means nothing: one of whole 16 bytes
     elif ld < c:
         raise ValueError(f"{name} rows overlap (stride {ld} < {c})")
     if (n | ld) > _U32_MAX:
@@ -920,6 +920,8 @@ def wal_attn_paged(desc: wal_kv_desc, cache, tables, lens, starts, Q, out, ws=No
     n, cols, ldq = _mat(T, Q, "Q", T.only_bf16, dim)
     q_heads = _whole_heads(cols, "Q", dim)
     _, _, ldo = _mat(T, out, "out", T.only_bf16, cols, n)
+    if n_seqs == 1:
+        ldt = pages
     holds = pages * desc.page_size
     max_len = max_len or holds
     if max_new is None:

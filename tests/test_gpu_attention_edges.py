@@ -66,3 +66,34 @@ def test_max_new_left_out(wal, seqs):  # noqa: F811
     out = torch.full((n, p.Q.shape[1]), 77.0, dtype=torch.bfloat16, device=dev())
     wal.wal_attn_paged(p.d, p.cache, *p.args, p.Q, out, ws)
     p.check(out)
+
+
+def test_the_pitch_of_an_only_row_means_nothing(wal):  # noqa: F811
+    """One token in buffers whose rows are not 16 bytes apart: there is no second row."""
+    heads, dim, n = 2, 64, 1
+
+    def row(cols, dtype=torch.bfloat16):
+        t = torch.randn((3, cols + 3), device=dev()).to(dtype)[:1, :cols]
+        assert t.stride(0) == cols + 3 and t.data_ptr() % 16 == 0
+        return t
+    turns, _, m = table(wal, dim, "plain", 1.0)
+    pos, slots = i32([7]), i32([5])
+    d = wal.make_kv_desc(2, 16, heads, dim, BF16)
+    for dtype in (torch.bfloat16, torch.float32):
+        q, k, v = row(4 * dim, dtype), row(2 * dim, dtype), row(2 * dim, dtype)
+        results = []
+        for wrap in (lambda t: t, lambda t: t.contiguous()):
+            a, b, c = wrap(q), wrap(k), wrap(v)
+            turned, q_out, k2, v2, out, whole = (wrap(row(w, t)) for w, t in (
+                (4 * dim, dtype), (4 * dim, torch.bfloat16), (2 * dim, dtype), (2 * dim, dtype), (4 * dim, torch.bfloat16),
+                (4 * dim, torch.bfloat16)))
+            cache = torch.zeros(wal.wal_kv_size(d).total_bytes, dtype=torch.uint8, device=dev())
+            wal.wal_rope(a, turned, pos, turns, dim)
+            wal.wal_kv_write(d, cache, slots, b, c, pos=pos, turns=turns, Q=a, Q_out=q_out)
+            wal.wal_kv_read(d, cache, slots, k2, v2)
+            wal.wal_attn_paged(d, cache, torch.zeros((3, 5), dtype=torch.int32, device=dev())[:1, :2], i32([6]), i32([0, n]),
+                               q_out, out, max_len=32)
+            wal.wal_attn_prompt(q_out, k2.to(torch.bfloat16), v2.to(torch.bfloat16), i32([0, n]), whole, dim, 1)
+            results.append([turned, q_out, k2, v2, out, whole])
+            assert all(torch.isfinite(t).all() for t in results[-1])
+        assert all(torch.equal(x, y) for x, y in zip(*results))
