@@ -649,15 +649,17 @@ int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const int32_t* slot
  * lens[s] tokens in the cache and new_s = starts[s + 1] - starts[s] query rows,
  * rows starts[s] .. of q; row i of them is its token lens[s] - new_s + i, and
  *     out[row][h] = sum_j w_j v_j,  w = softmax_j(scale * q[row][h] . k_j)
- * over its tokens j <= lens[s] - new_s + i.  A row that sees no token is
- * zeros.  One token per sequence (decode), a few, and chunks of a prompt
+ * over its tokens j <= lens[s] - new_s + i.  A row that sees no token, or none
+ * with a score above -infinity, is zeros.  One token per sequence (decode), a few, and chunks of a prompt
  * may be mixed in one call.
  *   tables_dev  [n_seqs][ldt] int32: page of each page_size tokens of a
  *               sequence; tokens of a page outside the cache are left out
  *   lens_dev    [n_seqs] int32, starts_dev [n_seqs + 1] int32 rising from 0 to n
  *   max_new, max_len  bounds of new_s and lens[s] (known to the caller, who
- *               holds the pages; rows and tokens past them are not
- *               computed); ldt * page_size >= max_len
+ *               holds the pages): rows past max_new are not computed, a longer
+ *               sequence is taken to end at its token max_len;
+ *               ldt * page_size >= max_len.  Whatever starts and lens hold,
+ *               nothing outside the call's rows and pages is touched
  *   q_dev       [n][ldq] bf16, q_heads (a multiple of kv_heads, at most
  *               64 kv_heads) heads side by side; out_dev [n][ldo] bf16;
  *               16-byte aligned rows; out must not overlap the inputs

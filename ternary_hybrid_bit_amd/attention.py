@@ -6,7 +6,8 @@ wal_kv_write, wal_attn_paged and wal_attn_prompt: forward() takes the new
 tokens of any sequences, whole prompts, chunks of them and single tokens
 alike.  examples/attention_layer.py runs one.
 
-Everything on the GPU is libwal's; this module keeps the page lists.
+The products and the attention are libwal's (prompt() rounds v to bf16 with
+torch); this module keeps the page lists.
 """
 from __future__ import annotations
 

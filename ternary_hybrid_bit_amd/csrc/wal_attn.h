@@ -66,7 +66,6 @@ using namespace wal;
 
 constexpr float kNoMax = -3.0e38f;   // a running maximum before the first key: finite, so that nothing subtracts infinities
 
-typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // Place of a row's partial result: row (first row of the sequence + token) * group + query head of the group.

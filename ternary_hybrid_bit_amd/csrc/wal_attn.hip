@@ -42,11 +42,13 @@ struct Plan {
 //    8192, int8: 102 us at 768 keys a piece, 108 at 2048 and at 512; 8 sequences up to 2048:
 //    13.7 us at 256, 17.6 at 512; 4 sequences up to 16000, heads of 256: 34 us at 768, 46 at
 //    512).  A piece of attn_stream is never above what a workgroup's page list holds.  Few
-//    short contexts are not split at all (517 tokens: 9.1 us with eight wavefronts a workgroup,
-//    6.5 + 3.0 us and a launch in pieces of 256 keys).
+//    short contexts are not split at all (517 tokens: 9.3 us with eight wavefronts a workgroup,
+//    6.5 + 3.0 us and a launch in pieces of 256 keys joined by k_attn_join; pieces joined by the
+//    last workgroup were not timed at these lengths).
 //  * Many rows, one sequence: into as many pieces as give the fewest rounds of
 //    workgroups over the places for them, not below 512 keys, the joining counted as 1.5 % of
-//    the products (2048 tokens over 32768, 256 workgroups: 1140 us whole, 1161 in two pieces).
+//    the products (2048 tokens over 32768, 256 workgroups: 1140 us whole, 1161 in two pieces).  At most
+//    64 pieces: more were not timed, and few workgroups, as of one key/value head, leave places empty.
 //  * Many rows, several sequences: pieces that fill the places once if all contexts were
 //    the longest, from 128 to 1024 keys, unless there are workgroups enough for four rounds (13 sequences up to
 //    4100, at most 260 workgroups: 63 us whole, 55 in pieces of 2048 keys, 49 of 1024, 52 of 512; 6

@@ -19,7 +19,10 @@
 // The softmax is the running one, with weights 2^(x - m): m follows the true
 // maximum only when a score exceeds it by more than 8 (weights up to 2^8 lose
 // nothing in fp32 or bf16), so most tiles exchange nothing between lanes and
-// rescale nothing.
+// rescale nothing.  Weights become bf16, the operand type of the second product, once, for int8 times
+// their value rows' scales; their sum is of the unrounded ones, in fp32.  Against 64 bits the outputs are
+// off by 2.1e-3 to 2.4e-3 (relative 2-norm) where their own rounding to bf16 alone gives 1.7e-3; weights in
+// two bf16 parts would keep to that at twice the products with V.
 //
 // Wavefronts join through LDS.  When the context is split over workgroups, each
 // writes its sums in fp32; up to kJoinHere pieces are added up, in their order, by the
@@ -27,7 +30,7 @@
 //
 // Measured (32 query, 8 key/value heads of 128): 131001 bf16 tokens 98 us with the join of
 // 512 pieces, over three caches in turn (5.5 TB/s); 64 sequences up to 8192, int8,
-// 105 us (4.6 TB/s); 517 tokens 9.4 us, a chain of dependent loads.
+// 104.5 us (4.7 TB/s); 517 tokens 9.3 us, a chain of dependent loads.
 #include <hip/hip_runtime.h>
 
 #include "wal_attn.h"

@@ -22,12 +22,15 @@
 //
 // The softmax is the running one with a maximum that follows only rises above 8
 // (a factor of 2^8); a lane adds up its own keys' weights and the two halves of a
-// row meet once, at the end.
+// row meet once, at the end.  Weights become bf16, the operand type of the second product, once,
+// for int8 times their value rows' scales (outputs 2.0e-3 to 2.4e-3 from 64 bits, relative
+// 2-norm, where their own rounding to bf16 alone gives 1.5e-3 to 1.7e-3): a second part of them would
+// add half of all products to kernels that the matrix cores bound.
 //
-// Measured: a prompt of 8192 (32 query, 8 key/value heads of 128) 532 us, 1.03 PFLOP/s;
-// 2048 tokens over 32768 of the int8 cache 1149 us, 0.93 PFLOP/s, its vector
+// Measured: a prompt of 8192 (32 query, 8 key/value heads of 128) 532-540 us, 1.02 PFLOP/s;
+// 2048 tokens over 32768 of the int8 cache 1149-1176 us, 0.92 PFLOP/s, its vector
 // instructions 3.0 times the prompt's for 1.9 times the products (k_attn_pair); 9 packed
-// prompts up to 777, heads of 256, 37 us; 13 chunks over up to 4100, heads of 64, 44 us and 8
+// prompts up to 777, heads of 256, 37 us; 13 chunks over up to 4100, heads of 64, 43 us and 8
 // to join (k_attn_tile).
 #include <hip/hip_runtime.h>
 

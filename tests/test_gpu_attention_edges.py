@@ -97,3 +97,14 @@ def test_the_pitch_of_an_only_row_means_nothing(wal):  # noqa: F811
             results.append([turned, q_out, k2, v2, out, whole])
             assert all(torch.isfinite(t).all() for t in results[-1])
         assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+@pytest.mark.parametrize("n,new,dim", [(120, 1, 128), (120, 7, 128), (120, 60, 64), (5000, 1, 64), (5000, 40, 128)])
+def test_rows_whose_scores_are_all_minus_infinity(wal, n, new, dim):  # noqa: F811
+    p = Paged(wal, [(n, new), (40, 1)], 4, 2, dim, 16, BF16, seed=51)
+    p.Q[:, 5::dim] = 1.0
+    K, V = (torch.from_numpy(x[:n].reshape(n, -1).astype(np.float32)).to(dev()) for x in (p.k, p.v))
+    K[:, 5] = float("-inf")                    # the first key/value head of the first sequence
+    wal.wal_kv_write(p.d, p.cache, p.slots[:n].contiguous(), K, V)
+    got = host(p.call()).reshape(-1, 2, 4, dim)
+    assert (got[:new, 0] == 0).all() and np.isfinite(got).all() and (got[new:] != 0).any() and (got[:new, 1] != 0).any()
