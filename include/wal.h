@@ -591,6 +591,22 @@ typedef struct {
 int wal_rope(const void* x_dev, int x_dtype, uint32_t n, uint32_t heads, uint32_t head_dim, uint32_t ldx,
              const wal_rotary* r, void* out_dev, int out_dtype, uint32_t ldo, void* stream);
 
+/* wal_head_norm: every head of every row over the root of its mean square,
+ *     y_j = w_j x_j / sqrt(mean_i x_i^2 + eps),
+ * then, with r, rotated at its row's position (r NULL: not), or, with a gate, times
+ * gate_j / (1 + exp(-gate_j)) (NULL: not; r and a gate do not go together).
+ *   x_dev, out_dev  as for wal_rope (head_dim a multiple of 16, at most 512)
+ *   weight_dev  [head_dim] fp32 or bf16, the same for all heads
+ *   eps         normal and finite, above 0
+ *   gate_dev    [n][ldg] fp32 or bf16 beside x, 16-byte aligned rows; must not
+ *               overlap out
+ * All fp32; squares past its range are taken of scaled values, so any finite x
+ * gives finite results.  bf16 output rounds to nearest even.  n = 0 does nothing.
+ * Errors: ARG, SHAPE, ALIGN, DEVICE. */
+int wal_head_norm(const void* x_dev, int x_dtype, uint32_t n, uint32_t heads, uint32_t head_dim, uint32_t ldx,
+                  const void* weight_dev, int w_dtype, float eps, const wal_rotary* r, const void* gate_dev,
+                  int gate_dtype, uint32_t ldg, void* out_dev, int out_dtype, uint32_t ldo, void* stream);
+
 /* The paged cache of one layer: n_pages pages of page_size tokens, one device
  * buffer of total_bytes (256-byte aligned) with the planes
  *   K, V    [n_pages][kv_heads][page_size][head_dim] bf16 or int8 codes
@@ -636,6 +652,22 @@ int wal_kv_size(const wal_kv_desc* d, wal_kv_info* info);
 int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n, const void* k_dev,
                  uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype, const wal_rotary* r,
                  const void* q_dev, uint32_t q_heads, uint32_t ldq, void* q_out_dev, uint32_t ldqo, void* stream);
+
+/* wal_kv_write_normed: the same with the heads of k and q normed first, as
+ * wal_head_norm norms them (where rotated: before the rotation).  A NULL weight
+ * leaves its side as it is; q's weight goes with q.
+ * Errors: those of wal_kv_write; ARG for norms that are NULL or an eps outside
+ * wal_head_norm's. */
+typedef struct {
+  const void* q_weight_dev;     /* [head_dim] or NULL                                    */
+  const void* k_weight_dev;     /* [head_dim] or NULL                                    */
+  int dtype;                    /* of both: WAL_X_F32 or WAL_X_BF16                      */
+  float eps;
+} wal_norms;
+int wal_kv_write_normed(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n, const void* k_dev,
+                        uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype, const wal_norms* norms,
+                        const wal_rotary* r, const void* q_dev, uint32_t q_heads, uint32_t ldq, void* q_out_dev,
+                        uint32_t ldqo, void* stream);
 
 /* wal_kv_read: the rows of slots[0..n) as numbers, k_out [n][ldk] and v_out
  * [n][ldv] in fp32 or bf16 (out_dtype; nearest even), 16-byte aligned rows;
@@ -693,6 +725,70 @@ int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t
                     uint32_t ldv, const int32_t* starts_dev, uint32_t n_seqs, uint32_t n, uint32_t max_len,
                     uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim, float scale, int causal,
                     void* out_dev, uint32_t ldo, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Blocks of the gated delta rule (the WAL2-Ternary-27B card, "Архитектура", counts
+ * 48 of them among 64 blocks; nothing more is printed, the formulas below
+ * are the usual ones): between the products, a causal convolution of q | k | v, the
+ * delta rule, and wal_head_norm with a gate.
+ *
+ * Both calls take rows packed by sequence: sequence s is rows starts[s] .. starts[s + 1]
+ * (starts_dev [n_seqs + 1] int32 rising from 0 to n; whatever it holds, nothing outside
+ * the call's rows is touched; rows outside every sequence are left as they are).  What
+ * a sequence carries from call to call is kept in place slots[s] of a state (slots_dev
+ * [n_seqs] int32, distinct).  A new sequence's place holds zeros.  A slot outside the state: the
+ * sequence begins with zeros and nothing is kept; state and slots NULL: so does every
+ * sequence.  A sequence without rows leaves its state as it is.
+ * n, n_seqs and n_slots are at most 2^24.
+ *
+ * wal_conv: out[t][c] = f(bias[c] + sum_{j < taps} weight[c][j] x[t - taps + 1 + j][c])
+ * for rows t of a sequence, f(y) = y / (1 + exp(-y)) with silu, else y.  Rows before the
+ * call's first are the state's: state_dev [n_slots][taps - 1][channels] of x's type holds the
+ * sequence's last taps - 1 rows, the oldest first.
+ *   x_dev    [n][ldx] fp32 or bf16, out_dev [n][ldo] fp32 or bf16; 16-byte aligned rows
+ *   weight_dev [channels][taps], bias_dev [channels] or NULL: fp32 or bf16 (w_dtype),
+ *            16-byte aligned, as is state_dev
+ *   channels a multiple of 8, taps 2 to 4
+ * Sums are fp32, bf16 output rounds to nearest even.  out must not overlap the inputs.
+ * Errors: ARG, SHAPE, ALIGN, DEVICE. */
+int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint32_t ldx, const void* weight_dev,
+             int w_dtype, uint32_t taps, const void* bias_dev, int silu, const int32_t* starts_dev, uint32_t n_seqs,
+             void* state_dev, const int32_t* slots_dev, uint32_t n_slots, void* out_dev, int out_dtype, uint32_t ldo,
+             void* stream);
+
+/* wal_delta: the gated delta rule (Yang et al. 2024, "Gated Delta Networks: Improving
+ * Mamba2 with Delta Rule").  Each value head h has a state S [key_dim][value_dim] and uses key
+ * head h / (value_heads / key_heads); for each token of a sequence in turn
+ *     S <- alpha S + beta k (v - alpha S^T k)^T,     out[t][h] = scale S^T q.
+ *   k, q     k[t], q[t] divided by sqrt(sum_j x_j^2 + norm_eps) when that is above 0
+ *            (normal), as they are when it is 0
+ *   alpha    exp(-decay[h] softplus(a[t][h] + shift[h])), beta = 1 / (1 + exp(-b[t][h]));
+ *            decay and shift NULL: alpha = exp(a[t][h]), beta = b[t][h].  The
+ *            logarithm of alpha is taken as 0 where it is above
+ *   q_dev, k_dev  [n][ldq], [n][ldk] bf16, key_heads heads side by side; v_dev, out_dev
+ *            [n][ldv], [n][ldo] bf16, value_heads heads; 16-byte aligned rows (views of
+ *            one fused buffer are fine); out must not overlap the inputs
+ *   a_dev, b_dev  [n][lda], [n][ldb] fp32; decay_dev, shift_dev [value_heads] fp32
+ *   state_dev [n_slots][value_heads][key_dim][value_dim] fp32, 16-byte aligned
+ *   max_new  bounds the sequences' rows: rows past it are neither computed nor kept
+ *   ws       wal_delta_workspace_size bytes, 256-byte aligned (NULL when that is 0),
+ *            contents arbitrary.  Calls that may overlap in time need their own
+ * States, norms, gates and sums are fp32.  From a token with an infinity or NaN among its
+ * q, k, v or gates on, what depends on it is an infinity or NaN.  The result does not
+ * depend on timing.
+ * Errors: ARG, SHAPE, ALIGN, BUFFER, DEVICE. */
+typedef struct {
+  uint32_t key_heads, value_heads;  /* value_heads a multiple of key_heads, at most 1024    */
+  uint32_t key_dim;                 /* 64 or 128                                            */
+  uint32_t value_dim;               /* a multiple of 32, at most 256                        */
+  float norm_eps, scale;
+} wal_delta_desc;
+int wal_delta_workspace_size(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new, size_t* bytes);
+int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk,
+              const void* v_dev, uint32_t ldv, const float* a_dev, uint32_t lda, const float* b_dev, uint32_t ldb,
+              const float* decay_dev, const float* shift_dev, const int32_t* starts_dev, uint32_t n_seqs, uint32_t n,
+              uint32_t max_new, float* state_dev, const int32_t* slots_dev, uint32_t n_slots, void* out_dev,
+              uint32_t ldo, void* ws_dev, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

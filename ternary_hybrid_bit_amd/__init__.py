@@ -86,9 +86,19 @@ class wal_rotary(ctypes.Structure):
                 ("layout", ctypes.c_uint32), ("magnitude", ctypes.c_float)]
 
 
+class wal_norms(ctypes.Structure):
+    _fields_ = [("q_weight_dev", ctypes.c_void_p), ("k_weight_dev", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 class wal_kv_desc(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_uint32), ("page_size", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
                 ("head_dim", ctypes.c_uint32), ("fmt", ctypes.c_uint32)]
+
+
+class wal_delta_desc(ctypes.Structure):
+    _fields_ = [("key_heads", ctypes.c_uint32), ("value_heads", ctypes.c_uint32), ("key_dim", ctypes.c_uint32),
+                ("value_dim", ctypes.c_uint32), ("norm_eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
 class wal_kv_info(ctypes.Structure):
@@ -147,11 +157,19 @@ _sig = {
     "wal_kv_size": (_I, [ctypes.POINTER(wal_kv_desc), ctypes.POINTER(wal_kv_info)]),
     "wal_kv_write": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _U32, _P, _U32, _I,
                           ctypes.POINTER(wal_rotary), _P, _U32, _U32, _P, _U32, _P]),
+    "wal_kv_write_normed": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _U32, _P, _U32, _I,
+                                 ctypes.POINTER(wal_norms), ctypes.POINTER(wal_rotary), _P, _U32, _U32, _P, _U32, _P]),
+    "wal_head_norm": (_I, [_P, _I, _U32, _U32, _U32, _U32, _P, _I, _F, ctypes.POINTER(wal_rotary), _P, _I, _U32, _P,
+                           _I, _U32, _P]),
     "wal_kv_read": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _U32, _P, _U32, _I, _P]),
     "wal_attn_paged_workspace_size": (_I, [ctypes.POINTER(wal_kv_desc), _U32, _U32, _U32, _U32, _U32,
                                            ctypes.POINTER(_SZ)]),
     "wal_attn_paged": (_I, [ctypes.POINTER(wal_kv_desc), _P, _P, _U32, _P, _P, _U32, _U32, _U32, _U32, _P, _U32, _U32,
                             _F, _P, _U32, _P, _SZ, _P]),
+    "wal_conv": (_I, [_P, _I, _U32, _U32, _U32, _P, _I, _U32, _P, _I, _P, _U32, _P, _P, _U32, _P, _I, _U32, _P]),
+    "wal_delta_workspace_size": (_I, [ctypes.POINTER(wal_delta_desc), _U32, _U32, _U32, ctypes.POINTER(_SZ)]),
+    "wal_delta": (_I, [ctypes.POINTER(wal_delta_desc), _P, _U32, _P, _U32, _P, _U32, _P, _U32, _P, _U32, _P, _P, _P,
+                       _U32, _U32, _U32, _P, _P, _U32, _P, _U32, _P, _SZ, _P]),
     "wal_attn_prompt": (_I, [_P, _U32, _P, _U32, _P, _U32, _P, _U32, _U32, _U32, _U32, _U32, _U32, _F, _I, _P, _U32,
                              _P]),
 }
@@ -712,6 +730,7 @@ class _Types:
     def __init__(self):
         import torch
         self.tensor, self.bf16, self.i32, self.i64 = torch.Tensor, torch.bfloat16, torch.int32, torch.int64
+        self.f32, self.only_f32 = torch.float32, (torch.float32,)
         self.acts, self.only_bf16 = (torch.bfloat16, torch.float32), (torch.bfloat16,)
         self.only_i32 = (torch.int32,)
 
@@ -745,7 +764,7 @@ def _mat(T, t, name: str, dtypes, cols: int, rows: int = 0):
     if n < rows:
         raise ValueError(f"{name} has {n} rows; at least {rows} are needed")
     ld, step = t.stride()
-    if step != 1 and c > 1:
+    if step != 1 and c > 1 and n:
         raise ValueError(f"{name} must have unit stride along its last axis")
     if n <= 1:
         ld = (c + 7) & ~7   # the pitch of an only row means nothing: one of whole 16 bytes
@@ -805,6 +824,47 @@ def wal_rope(X, out, pos, turns, head_dim: int, layout=WAL_ROPE_HALF, magnitude:
     return out
 
 
+def _norm_weight(T, t, name: str, head_dim: int):
+    """A norm's weight: as many fp32 or bf16 values as a head has, one after another."""
+    if not isinstance(t, T.tensor):
+        raise TypeError(f"{name} must be a torch tensor on the GPU, not {type(t).__name__}")
+    if t.dtype not in T.acts:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected one of {[str(d) for d in T.acts]}")
+    if t.shape != (head_dim,) or (head_dim > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be 1-D, {head_dim} elements with unit stride (shape {tuple(t.shape)})")
+
+
+def wal_head_norm(X, out, weight, head_dim: int, eps: float = 1e-6, pos=None, turns=None, layout=WAL_ROPE_HALF,
+                  magnitude: float = 1.0, gate=None, stream=None):
+    """out = X [n][heads * head_dim] with every head over the root of its mean square, times weight [head_dim];
+    then rotated as by wal_rope when pos and turns are given, or times silu(gate), gate [n][heads * head_dim].
+    bf16 or fp32 device tensors, out may be X itself."""
+    T = _types()
+    n, cols, ldx = _mat(T, X, "X", T.acts, head_dim)
+    heads = _whole_heads(cols, "X", head_dim)
+    _, _, ldo = _mat(T, out, "out", T.acts, cols, n)
+    _norm_weight(T, weight, "weight", head_dim)
+    if (pos is None) != (turns is None):
+        raise ValueError("pos and turns go together")
+    if pos is not None and gate is not None:
+        raise ValueError("a rotation and a gate do not go together")
+    r = None if pos is None else _rotary(T, pos, turns, n, layout, magnitude)
+    g, gdt, ldg = None, 0, 0
+    if gate is not None:
+        _, _, ldg = _mat(T, gate, "gate", T.acts, cols, n)
+        g, gdt = gate.data_ptr(), gate.dtype is T.bf16
+    if not (X.is_cuda and out.is_cuda and weight.is_cuda and (r is None or (pos.is_cuda and turns.is_cuda))
+            and (gate is None or gate.is_cuda)):
+        _gpu(X=X, out=out, weight=weight, pos=pos, turns=turns, gate=gate)
+    if n:
+        st = _lib.wal_head_norm(X.data_ptr(), X.dtype is T.bf16, n, heads, head_dim, ldx, weight.data_ptr(),
+                                weight.dtype is T.bf16, eps, r, g, gdt, ldg, out.data_ptr(), out.dtype is T.bf16, ldo,
+                                _stream(stream))
+        if st:
+            _check(st, "wal_head_norm")
+    return out
+
+
 def make_kv_desc(n_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int = WAL_KV_BF16) -> wal_kv_desc:
     return wal_kv_desc(n_pages, page_size, kv_heads, head_dim, fmt)
 
@@ -835,10 +895,12 @@ def _kv_cache(T, desc: wal_kv_desc, cache):
 
 
 def wal_kv_write(desc: wal_kv_desc, cache, slots, K, V, pos=None, turns=None, layout=WAL_ROPE_HALF,
-                 magnitude: float = 1.0, Q=None, Q_out=None, stream=None):
+                 magnitude: float = 1.0, Q=None, Q_out=None, stream=None, q_norm=None, k_norm=None,
+                 eps: float = 1e-6):
     """Writes K, V [n][kv_heads * head_dim] (bf16 or fp32) to the cache's slots
     [n] (int32).  With pos and turns the keys are rotated first, and Q, when
-    given, is rotated into Q_out (bf16)."""
+    given, is rotated into Q_out (bf16).  k_norm, q_norm [head_dim] (one type, fp32 or bf16): the heads of K and of
+    Q are normed before that, as by wal_head_norm with such a weight and eps."""
     T = _types()
     width = _kv_cache(T, desc, cache)
     n, _, ldk = _mat(T, K, "K", T.acts, width)
@@ -857,10 +919,29 @@ def wal_kv_write(desc: wal_kv_desc, cache, slots, K, V, pos=None, turns=None, la
         q_heads = _whole_heads(cols, "Q", desc.head_dim)
         _, _, ldqo = _mat(T, Q_out, "Q_out", T.only_bf16, cols, n)
         q, q_out = Q.data_ptr(), Q_out.data_ptr()
+    norms = None
+    if k_norm is not None or q_norm is not None:
+        for t, name in ((k_norm, "k_norm"), (q_norm, "q_norm")):
+            if t is not None:
+                _norm_weight(T, t, name, desc.head_dim)
+        if q_norm is not None and Q is None:
+            raise ValueError("q_norm needs Q")
+        if k_norm is not None and q_norm is not None and k_norm.dtype is not q_norm.dtype:
+            raise TypeError(f"k_norm has dtype {k_norm.dtype}, q_norm {q_norm.dtype}: they must be the same")
+        first = k_norm if k_norm is not None else q_norm
+        norms = wal_norms(None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                          first.dtype is T.bf16, eps)
+        if not (first.is_cuda and (q_norm is None or q_norm.is_cuda)):
+            _gpu(k_norm=k_norm, q_norm=q_norm)
     if not (cache.is_cuda and slots.is_cuda and K.is_cuda and V.is_cuda and (r is None or (pos.is_cuda and turns.is_cuda))
             and (Q is None or (Q.is_cuda and Q_out.is_cuda))):
         _gpu(cache=cache, slots=slots, K=K, V=V, pos=pos, turns=turns, Q=Q, Q_out=Q_out)
-    if n:
+    if n and norms is not None:
+        st = _lib.wal_kv_write_normed(desc, cache.data_ptr(), slots.data_ptr(), n, K.data_ptr(), ldk, V.data_ptr(), ldv,
+                                      K.dtype is T.bf16, norms, r, q, q_heads, ldq, q_out, ldqo, _stream(stream))
+        if st:
+            _check(st, "wal_kv_write_normed")
+    elif n:
         st = _lib.wal_kv_write(desc, cache.data_ptr(), slots.data_ptr(), n, K.data_ptr(), ldk, V.data_ptr(), ldv,
                                K.dtype is T.bf16, r, q, q_heads, ldq, q_out, ldqo, _stream(stream))
         if st:
@@ -969,4 +1050,133 @@ def wal_attn_prompt(Q, K, V, starts, out, head_dim: int, max_len: int, scale: Op
                                   ldo, _stream(stream))
         if st:
             _check(st, "wal_attn_prompt")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Blocks of the gated delta rule.
+
+def _state(T, t, name: str, dtype, shape) -> int:
+    """A contiguous device tensor [places][*shape] of what sequences carry between calls: its places."""
+    if not isinstance(t, T.tensor):
+        raise TypeError(f"{name} must be a torch tensor on the GPU, not {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    if t.dim() != 1 + len(shape) or tuple(t.shape[1:]) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected [places, {', '.join(map(str, shape))}]")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape[0] > _U32_MAX:
+        raise ValueError(f"{name} has {t.shape[0]} places: more than 32 bits hold")
+    return t.shape[0]
+
+
+def _gate_mat(T, t, name: str, cols: int, rows: int) -> int:
+    """fp32 rows of any pitch: their pitch."""
+    return max(_mat(T, t, name, T.only_f32, cols, rows)[2], cols)
+
+
+def wal_conv(X, weight, starts, out, state=None, slots=None, bias=None, silu: bool = True, stream=None):
+    """Causal convolution of each channel over rows packed by sequence: X [n][channels] (bf16 or fp32), weight
+    [channels][taps] and bias [channels] (bf16 or fp32), starts int32 [n_seqs + 1], out [n][channels] (bf16 or fp32),
+    through silu unless that is False.  state [places][taps - 1][channels] of X's type holds, in place slots[s]
+    (int32 [n_seqs]), sequence s's rows before the call, and its last ones after it; None: no rows before."""
+    T = _types()
+    n, channels, ldx = _mat(T, X, "X", T.acts, 8)
+    w_rows, taps, pitch = _mat(T, weight, "weight", T.acts, 1)
+    if w_rows != channels:
+        raise ValueError(f"weight has {w_rows} rows for {channels} channels")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    _, _, ldo = _mat(T, out, "out", T.acts, channels, n)
+    n_seqs = _vec(T, starts, "starts", T.i32, 1) - 1
+    if (state is None) != (slots is None):
+        raise ValueError("state and slots go together")
+    st_p = sl_p = bias_p = None
+    n_slots = 0
+    if state is not None:
+        n_slots = _state(T, state, "state", X.dtype, (taps - 1, channels))
+        _vec(T, slots, "slots", T.i32, n_seqs)
+        if n_slots:
+            st_p, sl_p = state.data_ptr(), slots.data_ptr()
+    if bias is not None:
+        _norm_weight(T, bias, "bias", channels)
+        if bias.dtype is not weight.dtype:
+            raise TypeError(f"bias has dtype {bias.dtype}, weight {weight.dtype}: they must be the same")
+        bias_p = bias.data_ptr()
+    if not (X.is_cuda and weight.is_cuda and starts.is_cuda and out.is_cuda and (state is None or (state.is_cuda and slots.is_cuda))
+            and (bias is None or bias.is_cuda)):
+        _gpu(X=X, weight=weight, starts=starts, out=out, state=state, slots=slots, bias=bias)
+    if n and n_seqs:
+        st = _lib.wal_conv(X.data_ptr(), X.dtype is T.bf16, n, channels, ldx, weight.data_ptr(), weight.dtype is T.bf16,
+                           taps, bias_p, 1 if silu else 0, starts.data_ptr(), n_seqs, st_p, sl_p, n_slots,
+                           out.data_ptr(), out.dtype is T.bf16, ldo, _stream(stream))
+        if st:
+            _check(st, "wal_conv")
+    return out
+
+
+def make_delta_desc(key_heads: int, value_heads: int, key_dim: int, value_dim: int, norm_eps: float = 1e-6,
+                    scale: Optional[float] = None) -> wal_delta_desc:
+    """scale: 1 / sqrt(key_dim) unless given; norm_eps 0: q and k are taken as they are."""
+    return wal_delta_desc(key_heads, value_heads, key_dim, value_dim, norm_eps,
+                          (key_dim ** -0.5 if key_dim > 0 else 0.0) if scale is None else scale)
+
+
+def wal_delta_workspace_size(desc: wal_delta_desc, n_seqs: int, n: int, max_new: int) -> int:
+    if not all(0 <= x <= _U32_MAX for x in (n_seqs, n, max_new)):
+        raise ValueError(f"n_seqs {n_seqs}, n {n}, max_new {max_new}: more than 32 bits hold")
+    b = _SZ()
+    _check(_lib.wal_delta_workspace_size(ctypes.byref(desc), n_seqs, n, max_new, ctypes.byref(b)),
+           "wal_delta_workspace_size")
+    return b.value
+
+
+def wal_delta(desc: wal_delta_desc, Q, K, V, A, B, starts, out, state=None, slots=None, ws=None, decay=None,
+              shift=None, max_new: Optional[int] = None, stream=None):
+    """The gated delta rule over rows packed by sequence: Q, K bf16 [n][key_heads * key_dim], V, out bf16
+    [n][value_heads * value_dim], A, B fp32 [n][value_heads], starts int32 [n_seqs + 1].  With decay and shift (fp32
+    [value_heads]) A and B are what the gates are made of, else the logarithm of the decay and the step themselves.
+    state fp32 [places][value_heads][key_dim][value_dim] holds sequence s's state in place slots[s] (int32 [n_seqs]);
+    None: every sequence begins with zeros and none is kept.  ws of wal_delta_workspace_size bytes.
+    max_new bounds the sequences' rows (rows past it are not computed); left out: as many as Q has."""
+    T = _types()
+    kw, h, vw = desc.key_heads * desc.key_dim, desc.value_heads, desc.value_heads * desc.value_dim
+    n, _, ldq = _mat(T, Q, "Q", T.only_bf16, kw)
+    _, _, ldk = _mat(T, K, "K", T.only_bf16, kw, n)
+    _, _, ldv = _mat(T, V, "V", T.only_bf16, vw, n)
+    lda, ldb = _gate_mat(T, A, "A", h, n), _gate_mat(T, B, "B", h, n)
+    _, _, ldo = _mat(T, out, "out", T.only_bf16, vw, n)
+    n_seqs = _vec(T, starts, "starts", T.i32, 1) - 1
+    if (state is None) != (slots is None):
+        raise ValueError("state and slots go together")
+    if (decay is None) != (shift is None):
+        raise ValueError("decay and shift go together")
+    st_p = sl_p = de_p = sh_p = wsp = None
+    n_slots = wsb = 0
+    if state is not None:
+        n_slots = _state(T, state, "state", T.f32, (h, desc.key_dim, desc.value_dim))
+        _vec(T, slots, "slots", T.i32, n_seqs)
+        if n_slots:
+            st_p, sl_p = state.data_ptr(), slots.data_ptr()
+    if decay is not None:
+        _vec(T, decay, "decay", T.f32, h)
+        _vec(T, shift, "shift", T.f32, h)
+        de_p, sh_p = decay.data_ptr(), shift.data_ptr()
+    if max_new is None:
+        max_new = n
+    if not 0 <= max_new <= _U32_MAX:
+        raise ValueError(f"max_new {max_new}")
+    if ws is not None:
+        wsb, wsp = _ws_bytes(ws), ws.data_ptr()
+    if not (Q.is_cuda and K.is_cuda and V.is_cuda and A.is_cuda and B.is_cuda and starts.is_cuda and out.is_cuda
+            and (state is None or (state.is_cuda and slots.is_cuda)) and (decay is None or (decay.is_cuda and shift.is_cuda))
+            and (ws is None or ws.is_cuda)):
+        _gpu(Q=Q, K=K, V=V, A=A, B=B, starts=starts, out=out, state=state, slots=slots, decay=decay, shift=shift, ws=ws)
+    if n and n_seqs:
+        st = _lib.wal_delta(desc, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, A.data_ptr(), lda,
+                            B.data_ptr(), ldb, de_p, sh_p, starts.data_ptr(), n_seqs, n, max_new, st_p, sl_p, n_slots,
+                            out.data_ptr(), ldo, wsp, wsb, _stream(stream))
+        if st:
+            _check(st, "wal_delta")
     return out

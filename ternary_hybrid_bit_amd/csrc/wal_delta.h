@@ -1,0 +1,66 @@
+// What the gated delta rule's kernels share (gfx950): their arguments and gates.
+#pragma once
+
+#include "wal_args.h"
+#include "wal_device.h"
+#include "wal_seq.h"
+
+namespace wal {
+
+constexpr uint32_t kSlice = 32;   // columns of a state that a workgroup takes
+
+struct Delta {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const float* a;
+  const float* b;
+  const float* decay;            // of each value head, NULL: a and b are the gates themselves
+  const float* shift;
+  const int32_t* starts;
+  const int32_t* slots;
+  float* state;                  // [n_slots][value head][key_dim][value_dim]
+  uint16_t* out;
+  uint64_t ldq, ldk, ldv, lda, ldb, ldo;
+  uint32_t n_seqs, n, max_new, n_slots;
+  uint32_t heads, group, value_dim, slices;   // value heads, those that share a key head
+  float eps, scale;              // eps 0: q and k as they are
+};
+
+// Launches (wal_status).
+int delta_step(const Delta& a, uint32_t key_dim, void* stream);
+
+}  // namespace wal
+
+namespace {
+
+using namespace wal;
+
+__device__ __forceinline__ Seq delta_seq(const Delta& a, uint32_t s) {
+  return cut_seq(a.starts[s], a.starts[s + 1], 0, (int32_t)a.n, (int32_t)a.max_new, (int32_t)a.n, false);
+}
+
+// Where a sequence's state is kept; below 0: nowhere, it begins with zeros.
+__device__ __forceinline__ int64_t kept_at(const Delta& a, uint32_t s) {
+  const uint32_t slot = a.slots ? (uint32_t)a.slots[s] : 0xFFFFFFFFu;
+  return a.state && slot < a.n_slots ? (int64_t)slot : -1;
+}
+
+struct Gates {
+  float log_alpha, beta;   // the decay's logarithm, at most 0, and the step
+};
+
+__device__ __forceinline__ Gates gates_of(const Delta& a, uint64_t row, uint32_t head) {
+  const float x = a.a[row * a.lda + head], y = a.b[row * a.ldb + head];
+  if (!a.decay) return Gates{x > 0.f ? 0.f : x, y};
+  const float z = x + a.shift[head], soft = fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
+  const float g = -a.decay[head] * soft;
+  return Gates{z != z ? z : g > 0.f ? 0.f : g, 1.f / (1.f + expf(-y))};
+}
+
+__device__ __forceinline__ float bf16_value(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
+
+// 1 / sqrt(sum of squares + eps): what a row of q or k is multiplied by.
+__device__ __forceinline__ float unit(const Delta& a, float squares) { return a.eps > 0.f ? 1.f / sqrtf(squares + a.eps) : 1.f; }
+
+}  // namespace

@@ -1,0 +1,91 @@
+// Entry points of the gated delta rule: checks of the arguments and the choice
+// of kernel.
+#include <hip/hip_runtime.h>
+
+#include "wal_delta.h"
+
+namespace {
+
+constexpr uint32_t kMaxRows = 1u << 24;   // rows and sequences of a call
+
+int check_desc(const wal_delta_desc* d) {
+  if (!d || !(fabsf(d->scale) < INFINITY) || !(d->norm_eps == 0.f || (d->norm_eps >= 0x1p-126f && d->norm_eps < INFINITY)))
+    return WAL_ERR_ARG;
+  if (!d->key_heads || !d->value_heads || d->value_heads > 1024 || d->value_heads % d->key_heads) return WAL_ERR_SHAPE;
+  if ((d->key_dim != 64 && d->key_dim != 128) || !d->value_dim || d->value_dim % kSlice || d->value_dim > 256)
+    return WAL_ERR_SHAPE;
+  return WAL_OK;
+}
+
+}  // namespace
+
+extern "C" int wal_delta_workspace_size(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new,
+                                        size_t* bytes) {
+  const int st = check_desc(d);
+  if (st) return st;
+  if (!bytes) return WAL_ERR_ARG;
+  if (n_seqs > kMaxRows || n > kMaxRows || max_new > kMaxRows) return WAL_ERR_SHAPE;
+  *bytes = 0;
+  return WAL_OK;
+}
+
+extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk,
+                         const void* v_dev, uint32_t ldv, const float* a_dev, uint32_t lda, const float* b_dev,
+                         uint32_t ldb, const float* decay_dev, const float* shift_dev, const int32_t* starts_dev,
+                         uint32_t n_seqs, uint32_t n, uint32_t max_new, float* state_dev, const int32_t* slots_dev,
+                         uint32_t n_slots, void* out_dev, uint32_t ldo, void* ws_dev, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  int st = wal_delta_workspace_size(d, n_seqs, n, max_new, &need);
+  if (st) return st;
+  if (!a_dev || !b_dev || !starts_dev || !state_dev != !slots_dev || !decay_dev != !shift_dev || (need && !ws_dev))
+    return WAL_ERR_ARG;
+  if (n_slots > kMaxRows) return WAL_ERR_SHAPE;
+  const uint64_t kw = (uint64_t)d->key_heads * d->key_dim, vw = (uint64_t)d->value_heads * d->value_dim, h = d->value_heads;
+  if ((st = check_rows(q_dev, ldq, kw, WAL_X_BF16)) || (st = check_rows(k_dev, ldk, kw, WAL_X_BF16)) ||
+      (st = check_rows(v_dev, ldv, vw, WAL_X_BF16)) || (st = check_rows(out_dev, ldo, vw, WAL_X_BF16)))
+    return st;
+  if (lda < h || ldb < h) return WAL_ERR_ARG;
+  if (!aligned(a_dev, 4) || !aligned(b_dev, 4) || !aligned(decay_dev, 4) || !aligned(shift_dev, 4) ||
+      !aligned(starts_dev, 4) || !aligned(slots_dev, 4) || !aligned(state_dev, 16) || (need && !aligned(ws_dev, 256)))
+    return WAL_ERR_ALIGN;
+  if (ws_bytes < need) return WAL_ERR_BUFFER;
+  const Rows out = rows(out_dev, n, ldo, vw, 2), ws = flat(ws_dev, need);
+  const Rows state = state_dev ? flat(state_dev, 4ull * n_slots * h * d->key_dim * d->value_dim) : Rows{};
+  const Rows in[9] = {rows(q_dev, n, ldq, kw, 2), rows(k_dev, n, ldk, kw, 2), rows(v_dev, n, ldv, vw, 2),
+                      rows(a_dev, n, lda, h, 4), rows(b_dev, n, ldb, h, 4), flat(starts_dev, 4ull * (n_seqs + 1ull)),
+                      slots_dev ? flat(slots_dev, 4ull * n_seqs) : Rows{},
+                      decay_dev ? flat(decay_dev, 4 * h) : Rows{}, shift_dev ? flat(shift_dev, 4 * h) : Rows{}};
+  for (const Rows& r : in)
+    if (meet(r, out) || meet(r, state) || meet(r, ws)) return WAL_ERR_ARG;
+  if (meet(out, state) || meet(out, ws) || meet(state, ws)) return WAL_ERR_ARG;
+  if (!n || !n_seqs || !max_new) return WAL_OK;
+  Delta a{};
+  a.q = static_cast<const uint16_t*>(q_dev);
+  a.k = static_cast<const uint16_t*>(k_dev);
+  a.v = static_cast<const uint16_t*>(v_dev);
+  a.a = a_dev;
+  a.b = b_dev;
+  a.decay = decay_dev;
+  a.shift = shift_dev;
+  a.starts = starts_dev;
+  a.slots = slots_dev;
+  a.state = state_dev;
+  a.out = static_cast<uint16_t*>(out_dev);
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldo = ldo;
+  a.n_seqs = n_seqs;
+  a.n = n;
+  a.max_new = max_new;
+  a.n_slots = n_slots;
+  a.heads = d->value_heads;
+  a.group = d->value_heads / d->key_heads;
+  a.value_dim = d->value_dim;
+  a.slices = d->value_dim / kSlice;
+  a.eps = d->norm_eps;
+  a.scale = d->scale;
+  return delta_step(a, d->key_dim, stream);
+}

@@ -1,9 +1,11 @@
-// Rotary positions and the rows of the paged key/value cache for gfx950:
+// Norms of single heads, rotary positions and the rows of the paged key/value
+// cache for gfx950:
+//     x_j -> w_j x_j / sqrt(mean x^2 + eps)   (where a call norms)
 //     (a, b) -> m (a cos p f - b sin p f, b cos p f + a sin p f)
 // for every pair of a head at position p, and the row formats of
 // include/wal.h (bf16, or int8 codes with one fp32 scale per token and head).
 //
-// All three calls are one pass over memory, bound by its bandwidth for many
+// All calls are one pass over memory, bound by its bandwidth for many
 // tokens and by one round trip for few.  The work is cut into units of 16
 // elements of one head: eight pairs (two pieces of eight elements in the half
 // layout, 16 neighbours in the interleaved one) or 16 unrotated elements, so
@@ -48,9 +50,19 @@ struct RopeKv {
   uint32_t slice;                 // units of a token that a workgroup takes
   uint32_t units, q_units, k_units;   // units of a token, of its q and its k heads
   uint32_t per_head, rot_units;   // units of a head, rotated ones among them
+  uint32_t lanes;                 // lanes of a head: its units, and with norms idle ones up to a power of two
   uint32_t rot, n_slots, page_shift, kv_heads, dim;
   uint32_t interleaved, out_bf16, int8;
+  // norms
+  const void* weight[2];          // of q and k, NULL: not normed
+  const void* gate;               // rows of ldg elements beside the q rows
+  uint64_t ldg;
+  float eps, inv_dim;
+  uint32_t w_bf16;
 };
+
+// What happens to a head before it is rotated and written.
+enum { kAsIs = 0, kNormed = 1, kGatedF32 = 2, kGatedBf16 = 3 };
 
 __device__ __forceinline__ float2 turn(int32_t pos, uint64_t t, float m) {
   const uint32_t f = (uint32_t)(((uint64_t)(int64_t)pos * t) >> 32);
@@ -136,8 +148,8 @@ __device__ __forceinline__ Unit unit_of(const RopeKv& a, uint32_t t, uint32_t u)
   x.t = t;
   x.kind = u < a.q_units ? 0u : u < a.q_units + a.k_units ? 1u : 2u;
   const uint32_t w = x.kind == 0 ? u : x.kind == 1 ? u - a.q_units : u - a.q_units - a.k_units;
-  x.head = w / a.per_head;
-  x.j = w - x.head * a.per_head;
+  x.head = w / a.lanes;
+  x.j = w - x.head * a.lanes;
   x.rotated = x.kind < 2 && x.j < a.rot_units;
   const bool split = x.rotated && !a.interleaved;
   x.lo = split ? 8 * x.j : 16 * x.j;
@@ -154,29 +166,82 @@ __device__ __forceinline__ void load_unit(const RopeKv& a, const Unit& x, float*
   load8<BF16>(p, at + x.hi, v + 8);
 }
 
-template <bool BF16>
+// The lane's 16 elements of a head over the root of the head's mean square, times the weights w.  The lanes of a
+// head sit side by side, a power of two of them.
+__device__ __forceinline__ void norm_unit(const RopeKv& a, const Unit& x, const float* w, float* v) {
+  const auto squares = [&](float f) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s = fmaf(v[e] * f, v[e] * f, s);
+    for (uint32_t m = 1; m < a.lanes; m <<= 1) s += __shfl_xor(s, (int)m);
+    return s;
+  };
+  float s = squares(1.f), f = 1.f;
+  if (!(s < INFINITY)) {   // squares past the range of fp32: of 2^-80 times the values (an infinity or NaN stays one)
+    f = 0x1p-80f;
+    s = squares(f);
+  }
+  const float r = f / sqrtf(fmaf(s, a.inv_dim, a.eps * (f * f)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[8 * i + e] *= r * w[(i ? x.hi : x.lo) + e];
+}
+
+template <bool BF16, int MODE>
 __global__ __launch_bounds__(kRopeThreads) void k_rope_kv(RopeKv a) {
+  constexpr bool kGate = MODE >= kGatedF32;
   __shared__ float2 cs[kRopeLdsPairs];
+  __shared__ __attribute__((aligned(16))) float wsh[MODE ? 2 : 1][MODE ? kMaxRopeDim : 1];
   const uint32_t t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
   const uint32_t u0 = blockIdx.y * a.slice, nu = min(a.slice, a.units - u0), total = nt * nu;
   uint32_t i = threadIdx.x;
   Unit x{};
-  float v[16];
-  if (i < total) {
+  float v[16], g[kGate ? 16 : 1];
+  const auto take = [&] {
     const uint32_t t = i / nu;
     x = unit_of(a, t0 + t, u0 + i - t * nu);
+    if (MODE && x.j >= a.per_head) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      if constexpr (kGate) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) g[e] = 0.f;
+      }
+      return;
+    }
     load_unit<BF16>(a, x, v);
-  }
+    if constexpr (kGate) {
+      const uint64_t at = x.t * a.ldg + x.head * a.dim;
+      load8<MODE == kGatedBf16>(a.gate, at + x.lo, g);
+      load8<MODE == kGatedBf16>(a.gate, at + x.hi, g + 8);
+    }
+  };
+  if (i < total) take();
   const uint32_t pairs = a.rot / 2;
   if (pairs) {
     for (uint32_t p = threadIdx.x; p < nt * pairs; p += kRopeThreads) {
       const uint32_t t = p / pairs;
       cs[p] = turn(a.pos[t0 + t], a.turns[p - t * pairs], a.magnitude);
     }
-    __syncthreads();
   }
+  if constexpr (MODE != kAsIs) {
+    for (uint32_t e = threadIdx.x; e < 2 * a.dim; e += kRopeThreads) {
+      const uint32_t k = e >= a.dim, d = e - k * a.dim;
+      const void* w = k ? a.weight[1] : a.weight[0];
+      if (w)
+        wsh[k][d] = a.w_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(w)[d] << 16)
+                             : static_cast<const float*>(w)[d];
+    }
+  }
+  if (MODE || pairs) __syncthreads();
   while (i < total) {
-    if (x.rotated) {
+    const bool idle = MODE && x.j >= a.per_head;
+    if constexpr (MODE != kAsIs) {
+      // every lane of the head takes part, idle ones with zeros
+      if (x.kind == 0 ? a.weight[0] != nullptr : x.kind == 1 && a.weight[1] != nullptr) norm_unit(a, x, wsh[x.kind], v);
+    }
+    if (!kGate && x.rotated) {
       const float2* c = cs + (x.t - t0) * pairs + 8 * x.j;
       if (a.interleaved) {
 #pragma unroll
@@ -186,7 +251,12 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_kv(RopeKv a) {
         for (int e = 0; e < 8; ++e) turn_pair(v[e], v[8 + e], c[e]);
       }
     }
-    if (x.kind == 0) {
+    if constexpr (kGate) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] *= g[e] / (1.f + expf(-g[e]));
+    }
+    if (idle) {
+    } else if (kGate || x.kind == 0) {   // a gate goes with neither a rotation nor the cache
       const uint64_t at = x.t * a.ldqo + x.head * a.dim;
       store8(a.q_out, at + x.lo, v, a.out_bf16);
       store8(a.q_out, at + x.hi, v + 8, a.out_bf16);
@@ -225,11 +295,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_kv(RopeKv a) {
       }
     }
     i += kRopeThreads;
-    if (i < total) {
-      const uint32_t t = i / nu;
-      x = unit_of(a, t0 + t, u0 + i - t * nu);
-      load_unit<BF16>(a, x, v);
-    }
+    if (i < total) take();
   }
 }
 
@@ -283,23 +349,49 @@ int check_rotary(const wal_rotary* r, uint32_t head_dim) {
   return WAL_OK;
 }
 
+bool eps_ok(float eps) { return eps >= 0x1p-126f && eps < INFINITY; }
+
+// Lanes of a normed head: a power of two, so that they add up by exchange.
+uint32_t lanes_of(uint32_t per_head) {
+  uint32_t n = 1;
+  while (n < per_head) n *= 2;
+  return n;
+}
+
+void set_rotary(RopeKv& a, const wal_rotary* r) {
+  a.turns = r->turns_dev;
+  a.pos = r->pos_dev;
+  a.rot = r->rot_dim;
+  a.rot_units = r->rot_dim / 16;
+  a.interleaved = r->layout == WAL_ROPE_INTERLEAVED;
+  a.magnitude = r->magnitude;
+}
+
 // Tokens of a workgroup and the slice of their units: whole tokens, about four units a thread
 // when there are many, a unit a thread over more workgroups when there are few.
-int launch(RopeKv& a, bool bf16_in, hipStream_t s) {
+template <int MODE>
+void launch(const RopeKv& a, bool bf16_in, dim3 grid, hipStream_t s) {
+  if (bf16_in)
+    hipLaunchKernelGGL((k_rope_kv<true, MODE>), grid, dim3(kRopeThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_rope_kv<false, MODE>), grid, dim3(kRopeThreads), 0, s, a);
+}
+
+int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
   const uint32_t by_lds = a.rot ? kRopeLdsPairs / (a.rot / 2) : 64;
   a.tokens = 1;
   a.slice = a.units;
   if ((uint64_t)a.n * a.units <= 512 * kRopeThreads) {
-    a.slice = kRopeThreads / a.per_head * a.per_head;
+    a.slice = kRopeThreads / a.lanes * a.lanes;
     if (a.slice > a.units) a.slice = a.units;
   } else {
     while (a.tokens < by_lds && a.tokens * a.units < 4 * kRopeThreads) ++a.tokens;
   }
   const dim3 grid((a.n + a.tokens - 1) / a.tokens, (a.units + a.slice - 1) / a.slice);
-  if (bf16_in)
-    hipLaunchKernelGGL(k_rope_kv<true>, grid, dim3(kRopeThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL(k_rope_kv<false>, grid, dim3(kRopeThreads), 0, s, a);
+  if (mode == kAsIs) launch<kAsIs>(a, bf16_in, grid, s);
+  if (mode == kNormed) launch<kNormed>(a, bf16_in, grid, s);
+  if (mode == kGatedF32) launch<kGatedF32>(a, bf16_in, grid, s);
+  if (mode == kGatedBf16) launch<kGatedBf16>(a, bf16_in, grid, s);
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
 
@@ -329,24 +421,70 @@ extern "C" int wal_rope(const void* x_dev, int x_dtype, uint32_t n, uint32_t hea
   a.magnitude = r->magnitude;
   a.n = n;
   a.per_head = head_dim / 16;
+  a.lanes = a.per_head;
   a.units = a.q_units = heads * a.per_head;
   a.rot = r->rot_dim;
   a.rot_units = r->rot_dim / 16;
   a.dim = head_dim;
   a.interleaved = r->layout == WAL_ROPE_INTERLEAVED;
   a.out_bf16 = out_dtype == WAL_X_BF16;
-  return launch(a, x_dtype == WAL_X_BF16, static_cast<hipStream_t>(stream));
+  return launch(a, x_dtype == WAL_X_BF16, kAsIs, static_cast<hipStream_t>(stream));
 }
 
-extern "C" int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n,
-                            const void* k_dev, uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype,
-                            const wal_rotary* r, const void* q_dev, uint32_t q_heads, uint32_t ldq, void* q_out_dev,
-                            uint32_t ldqo, void* stream) {
+extern "C" int wal_head_norm(const void* x_dev, int x_dtype, uint32_t n, uint32_t heads, uint32_t head_dim,
+                             uint32_t ldx, const void* weight_dev, int w_dtype, float eps, const wal_rotary* r,
+                             const void* gate_dev, int gate_dtype, uint32_t ldg, void* out_dev, int out_dtype,
+                             uint32_t ldo, void* stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || !dtype_ok(w_dtype) || (gate_dev && !dtype_ok(gate_dtype)))
+    return WAL_ERR_ARG;
+  if (!weight_dev || !eps_ok(eps) || (r && gate_dev)) return WAL_ERR_ARG;
+  if (!heads || heads > 65535 || !head_dim || head_dim % 16 || head_dim > kMaxRopeDim || n > (1u << 30))
+    return WAL_ERR_SHAPE;
+  int st;
+  if (r && (st = check_rotary(r, head_dim))) return st;
+  const uint64_t width = (uint64_t)heads * head_dim;
+  if ((st = check_rows(x_dev, ldx, width, x_dtype)) || (st = check_rows(out_dev, ldo, width, out_dtype))) return st;
+  if (gate_dev && (st = check_rows(gate_dev, ldg, width, gate_dtype))) return st;
+  if (!aligned(weight_dev, elem_bytes(w_dtype))) return WAL_ERR_ALIGN;
+  const Rows xs = rows(x_dev, n, ldx, width, elem_bytes(x_dtype)), os = rows(out_dev, n, ldo, width, elem_bytes(out_dtype));
+  const bool same = x_dev == out_dev && x_dtype == out_dtype && ldx == ldo;
+  if (!same && meet(xs, os)) return WAL_ERR_ARG;
+  if (meet(os, flat(weight_dev, (uint64_t)head_dim * elem_bytes(w_dtype)))) return WAL_ERR_ARG;
+  if (gate_dev && meet(os, rows(gate_dev, n, ldg, width, elem_bytes(gate_dtype)))) return WAL_ERR_ARG;
+  if (r && (meet(os, flat(r->pos_dev, 4ull * n)) || meet(os, flat(r->turns_dev, 4ull * r->rot_dim)))) return WAL_ERR_ARG;
+  if (!n) return WAL_OK;
+  RopeKv a{};
+  a.q = static_cast<const char*>(x_dev);
+  a.q_out = out_dev;
+  a.ldq = ldx;
+  a.ldqo = ldo;
+  a.n = n;
+  a.per_head = head_dim / 16;
+  a.lanes = lanes_of(a.per_head);
+  a.units = a.q_units = heads * a.lanes;
+  if (r) set_rotary(a, r);
+  a.dim = head_dim;
+  a.out_bf16 = out_dtype == WAL_X_BF16;
+  a.weight[0] = weight_dev;
+  a.w_bf16 = w_dtype == WAL_X_BF16;
+  a.eps = eps;
+  a.inv_dim = 1.f / (float)head_dim;
+  a.gate = gate_dev;
+  a.ldg = ldg;
+  const int mode = !gate_dev ? kNormed : gate_dtype == WAL_X_BF16 ? kGatedBf16 : kGatedF32;
+  return launch(a, x_dtype == WAL_X_BF16, mode, static_cast<hipStream_t>(stream));
+}
+
+static int kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n,
+                    const void* k_dev, uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype,
+                    const wal_norms* norms, const wal_rotary* r, const void* q_dev, uint32_t q_heads, uint32_t ldq,
+                    void* q_out_dev, uint32_t ldqo, void* stream) {
   wal_kv_info f;
   int st = wal_kv_size(d, &f);
   if (st) return st;
   if (!cache_dev || !slots_dev || !dtype_ok(kv_dtype)) return WAL_ERR_ARG;
   if (!q_dev != !q_out_dev || (q_dev && !r)) return WAL_ERR_ARG;
+  if (norms && (!dtype_ok(norms->dtype) || !eps_ok(norms->eps) || (norms->q_weight_dev && !q_dev))) return WAL_ERR_ARG;
   if (n > (1u << 30) || (q_dev && (!q_heads || q_heads > 16384))) return WAL_ERR_SHAPE;
   if (r && (st = check_rotary(r, d->head_dim))) return st;
   const uint64_t width = (uint64_t)d->kv_heads * d->head_dim, qw = (uint64_t)q_heads * d->head_dim;
@@ -354,12 +492,16 @@ extern "C" int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t
   if (q_dev && ((st = check_rows(q_dev, ldq, qw, kv_dtype)) || (st = check_rows(q_out_dev, ldqo, qw, WAL_X_BF16))))
     return st;
   if (!aligned(cache_dev, 256) || !aligned(slots_dev, 4)) return WAL_ERR_ALIGN;
+  const uint32_t wb = norms ? elem_bytes(norms->dtype) : 1;
+  if (norms && (!aligned(norms->q_weight_dev, wb) || !aligned(norms->k_weight_dev, wb))) return WAL_ERR_ALIGN;
   const uint32_t eb = elem_bytes(kv_dtype);
   const Rows cache = flat(cache_dev, f.total_bytes);
   const Rows qo = q_dev ? rows(q_out_dev, n, ldqo, qw, 2) : Rows{};
-  const Rows in[5] = {rows(k_dev, n, ldk, width, eb), rows(v_dev, n, ldv, width, eb), flat(slots_dev, 4ull * n),
+  const Rows in[7] = {rows(k_dev, n, ldk, width, eb), rows(v_dev, n, ldv, width, eb), flat(slots_dev, 4ull * n),
                       r ? flat(r->pos_dev, 4ull * n) : Rows{},
-                      r ? flat(r->turns_dev, 4ull * r->rot_dim) : Rows{}};
+                      r ? flat(r->turns_dev, 4ull * r->rot_dim) : Rows{},
+                      norms && norms->q_weight_dev ? flat(norms->q_weight_dev, (uint64_t)wb * d->head_dim) : Rows{},
+                      norms && norms->k_weight_dev ? flat(norms->k_weight_dev, (uint64_t)wb * d->head_dim) : Rows{}};
   for (const Rows& s : in)
     if (meet(s, cache) || meet(s, qo)) return WAL_ERR_ARG;
   if (q_dev) {
@@ -375,13 +517,13 @@ extern "C" int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t
   a.q_out = q_out_dev;
   a.cache = static_cast<uint8_t*>(cache_dev);
   a.slots = slots_dev;
-  if (r) {
-    a.turns = r->turns_dev;
-    a.pos = r->pos_dev;
-    a.rot = r->rot_dim;
-    a.rot_units = r->rot_dim / 16;
-    a.interleaved = r->layout == WAL_ROPE_INTERLEAVED;
-    a.magnitude = r->magnitude;
+  if (r) set_rotary(a, r);
+  if (norms) {
+    a.weight[0] = norms->q_weight_dev;
+    a.weight[1] = norms->k_weight_dev;
+    a.w_bf16 = norms->dtype == WAL_X_BF16;
+    a.eps = norms->eps;
+    a.inv_dim = 1.f / (float)d->head_dim;
   }
   a.ldq = ldq;
   a.ld_to_k = (int64_t)ldk - ldq;
@@ -392,7 +534,7 @@ extern "C" int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t
   a.off_ks = f.off_ks;
   a.ks_to_vs = f.off_vs - f.off_ks;
   a.n = n;
-  a.per_head = d->head_dim / 16;
+  a.per_head = a.lanes = d->head_dim / 16;
   a.q_units = q_dev ? q_heads * a.per_head : 0;
   a.k_units = d->kv_heads * a.per_head;
   a.units = a.q_units + 2 * a.k_units;
@@ -402,7 +544,24 @@ extern "C" int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t
   a.dim = d->head_dim;
   a.out_bf16 = 1;
   a.int8 = d->fmt == WAL_KV_INT8;
-  return launch(a, kv_dtype == WAL_X_BF16, static_cast<hipStream_t>(stream));
+  return launch(a, kv_dtype == WAL_X_BF16, a.weight[0] || a.weight[1] ? kNormed : kAsIs, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int wal_kv_write(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n,
+                            const void* k_dev, uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype,
+                            const wal_rotary* r, const void* q_dev, uint32_t q_heads, uint32_t ldq, void* q_out_dev,
+                            uint32_t ldqo, void* stream) {
+  return kv_write(d, cache_dev, slots_dev, n, k_dev, ldk, v_dev, ldv, kv_dtype, nullptr, r, q_dev, q_heads, ldq,
+                  q_out_dev, ldqo, stream);
+}
+
+extern "C" int wal_kv_write_normed(const wal_kv_desc* d, void* cache_dev, const int32_t* slots_dev, uint32_t n,
+                                   const void* k_dev, uint32_t ldk, const void* v_dev, uint32_t ldv, int kv_dtype,
+                                   const wal_norms* norms, const wal_rotary* r, const void* q_dev, uint32_t q_heads,
+                                   uint32_t ldq, void* q_out_dev, uint32_t ldqo, void* stream) {
+  if (!norms) return WAL_ERR_ARG;
+  return kv_write(d, cache_dev, slots_dev, n, k_dev, ldk, v_dev, ldv, kv_dtype, norms, r, q_dev, q_heads, ldq,
+                  q_out_dev, ldqo, stream);
 }
 
 extern "C" int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const int32_t* slots_dev, uint32_t n,
