@@ -8,6 +8,10 @@
 namespace wal {
 
 constexpr uint32_t kSlice = 32;   // columns of a state that a workgroup takes
+constexpr int kChunk = 64;        // tokens that meet in products
+// What the scan over chunks reads of a chunk and head: T and P in parts, as operands, and the factors of its rows.
+constexpr int kTParts = 3, kPParts = 2;
+constexpr uint32_t kPAt = kTParts * 6 * 1024, kVecAt = kPAt + kPParts * 6 * 1024, kItemBytes = kVecAt + 5 * 256;
 
 struct Delta {
   const uint16_t* q;
@@ -25,10 +29,17 @@ struct Delta {
   uint32_t n_seqs, n, max_new, n_slots;
   uint32_t heads, group, value_dim, slices;   // value heads, those that share a key head
   float eps, scale;              // eps 0: q and k as they are
+  // calls on chunks: sequence s has the places from starts[s] / 64 + s on, one for each chunk; a launch takes `places`
+  // of them from place0, and a sequence that goes on leaves its state in carry[1] and finds it in carry[0]
+  uint8_t* ws;
+  float* carry[2];
+  uint32_t place0, places;
 };
 
 // Launches (wal_status).
 int delta_step(const Delta& a, uint32_t key_dim, void* stream);
+// In as many launches as a.places take of the call's `all` places.
+int delta_chunks(Delta& a, uint32_t key_dim, uint32_t all, void* stream);
 
 }  // namespace wal
 

@@ -7,6 +7,27 @@
 namespace {
 
 constexpr uint32_t kMaxRows = 1u << 24;   // rows and sequences of a call
+constexpr uint32_t kFewRows = 16;         // of a sequence: token by token
+constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: what the last cache holds
+
+// How a call is cut.
+struct Plan {
+  bool step;                 // token by token, else on chunks
+  uint32_t all, places;      // places of chunks, and those of one launch
+  uint64_t carry, bytes;     // bytes of a carried state; of the workspace
+};
+
+Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new) {
+  Plan p{};
+  p.step = max_new <= kFewRows;
+  if (p.step || !n || !n_seqs) return p;
+  const uint64_t place = (uint64_t)d->value_heads * kItemBytes, most = kMaxItems / place;
+  p.all = n / kChunk + n_seqs;
+  p.places = p.all <= most ? p.all : most ? (uint32_t)most : 1;
+  p.carry = p.places < p.all ? 4ull * d->value_heads * d->key_dim * d->value_dim : 0;
+  p.bytes = p.places * place + 2 * p.carry;
+  return p;
+}
 
 int check_desc(const wal_delta_desc* d) {
   if (!d || !(fabsf(d->scale) < INFINITY) || !(d->norm_eps == 0.f || (d->norm_eps >= 0x1p-126f && d->norm_eps < INFINITY)))
@@ -25,7 +46,7 @@ extern "C" int wal_delta_workspace_size(const wal_delta_desc* d, uint32_t n_seqs
   if (st) return st;
   if (!bytes) return WAL_ERR_ARG;
   if (n_seqs > kMaxRows || n > kMaxRows || max_new > kMaxRows) return WAL_ERR_SHAPE;
-  *bytes = 0;
+  *bytes = plan_of(d, n_seqs, n, max_new).bytes;
   return WAL_OK;
 }
 
@@ -87,5 +108,11 @@ extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ld
   a.slices = d->value_dim / kSlice;
   a.eps = d->norm_eps;
   a.scale = d->scale;
-  return delta_step(a, d->key_dim, stream);
+  const Plan p = plan_of(d, n_seqs, n, max_new);
+  if (p.step) return delta_step(a, d->key_dim, stream);
+  a.ws = static_cast<uint8_t*>(ws_dev);
+  a.places = p.places;
+  a.carry[0] = reinterpret_cast<float*>(a.ws + (uint64_t)p.places * d->value_heads * kItemBytes);
+  a.carry[1] = a.carry[0] + p.carry / 4;
+  return delta_chunks(a, d->key_dim, p.all, stream);
 }
