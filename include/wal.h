@@ -767,7 +767,7 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  *            logarithm of alpha is taken as 0 where it is above
  *   q_dev, k_dev  [n][ldq], [n][ldk] bf16, key_heads heads side by side; v_dev, out_dev
  *            [n][ldv], [n][ldo] bf16, value_heads heads; 16-byte aligned rows (views of
- *            one fused buffer are fine); out must not overlap the inputs
+ *            one fused buffer are fine), pitches at most 2^24; out must not overlap the inputs
  *   a_dev, b_dev  [n][lda], [n][ldb] fp32; decay_dev, shift_dev [value_heads] fp32
  *   state_dev [n_slots][value_heads][key_dim][value_dim] fp32, 16-byte aligned
  *   max_new  bounds the sequences' rows: rows past it are neither computed nor kept

@@ -485,16 +485,6 @@ struct Rows32 {
   }
 };
 
-// Barrier of a workgroup that hands over LDS contents only: loads from memory stay in flight over it (a full
-// __syncthreads() would wait for those just issued, a memory latency in every tile).
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_sched_barrier(0);   // nor does arithmetic move over it: a step keeps to its kind of work
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // Few workgroups, or heads too wide for two wavefronts a SIMD: four wavefronts that go through a tile
 // together; two workgroups on a compute unit overlap each other's products and exponentials.
 template <int KIND, int D>

@@ -7,6 +7,7 @@
 namespace {
 
 constexpr uint32_t kMaxRows = 1u << 24;   // rows and sequences of a call
+constexpr uint32_t kMaxPitch = 1u << 24;  // elements from a row to the next: 64 rows in 32 bits of bytes
 constexpr uint32_t kFewRows = 16;         // of a sequence: token by token
 constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: what the last cache holds
 
@@ -66,6 +67,7 @@ extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ld
       (st = check_rows(v_dev, ldv, vw, WAL_X_BF16)) || (st = check_rows(out_dev, ldo, vw, WAL_X_BF16)))
     return st;
   if (lda < h || ldb < h) return WAL_ERR_ARG;
+  if (ldq > kMaxPitch || ldk > kMaxPitch || ldv > kMaxPitch || ldo > kMaxPitch) return WAL_ERR_SHAPE;
   if (!aligned(a_dev, 4) || !aligned(b_dev, 4) || !aligned(decay_dev, 4) || !aligned(shift_dev, 4) ||
       !aligned(starts_dev, 4) || !aligned(slots_dev, 4) || !aligned(state_dev, 16) || (need && !aligned(ws_dev, 256)))
     return WAL_ERR_ALIGN;

@@ -49,12 +49,24 @@ __device__ __forceinline__ void split(const float (&x)[8], bf16x8_t (&p)[N]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) r[i] = x[i];
 #pragma unroll
-  for (int k = 0; k < N; ++k)
+  for (int k = 0; k < N; ++k) {
+    u32x4_t w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[k][i] = (__bf16)r[i];
-      if (k + 1 < N) r[i] -= (float)p[k][i];
+    for (int i = 0; i < 4; ++i) {
+      const bf16x2_t b = {(__bf16)r[2 * i], (__bf16)r[2 * i + 1]};   // to nearest even
+      w[i] = __builtin_bit_cast(uint32_t, b);
+      if (k + 1 < N) {
+        r[2 * i] -= __uint_as_float(w[i] << 16);
+        r[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+      }
     }
+    p[k] = as_operand(w);
+  }
+}
+template <int N>
+__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, bf16x8_t (&p)[N]) {
+  const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  split(z, p);
 }
 
 // The sequence of a chunk's place: sequence s has those from starts[s] / 64 + s on.
@@ -309,6 +321,11 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
 
 constexpr int kScanWaves = 2;
 
+// Rows of a chunk in memory: what lies behind the last one reads as zeros and is not written.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, uint64_t ld, int32_t count, uint32_t width) {
+  return rsrc(p, (uint32_t)(2 * ((uint64_t)(count - 1) * ld + width)));
+}
+
 template <int DK>
 __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
   constexpr int U = DK / 32;                       // 32-row blocks of the state
@@ -321,7 +338,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
   // chiplets in turn.
   const uint32_t x = blockIdx.x % 8, g = blockIdx.x / 8, pair = g / a.slices * 8 + x;
   if (pair >= a.n_seqs * a.heads) return;
-  const uint32_t s = pair / a.heads, h = pair % a.heads, kh = h / a.group;
+  const uint32_t s = pair / a.heads, h = pair % a.heads, kh = h / a.group, dv = a.value_dim;
   const uint32_t col = kSlice * (g % a.slices) + 16 * wave + n;
   const Seq q = delta_seq(a, s);
   const uint32_t base = (uint32_t)q.first / kC + s;
@@ -329,8 +346,8 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
   const int32_t j0 = max(0, (int32_t)a.place0 - (int32_t)base), j1 = min(chunks, (int32_t)(a.place0 + a.places) - (int32_t)base);
   if (j0 >= j1) return;
   const int64_t slot = kept_at(a, s);
-  const uint64_t head_at = ((uint64_t)h * DK + 8 * c) * a.value_dim + col;
-  float* kept = slot < 0 ? nullptr : a.state + (uint64_t)slot * a.heads * DK * a.value_dim + head_at;
+  const uint64_t head_at = ((uint64_t)h * DK + 8 * c) * dv + col;
+  float* kept = slot < 0 ? nullptr : a.state + (uint64_t)slot * a.heads * DK * dv + head_at;
   const float* before = j0 ? a.carry[0] + head_at : kept;
   float* after = j1 < chunks ? a.carry[1] + head_at : kept;
 
@@ -340,19 +357,24 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(32 * u + 4 * hf + i) * a.value_dim] : 0.f;
+      for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(32 * u + 4 * hf + i) * dv] : 0.f;
 
-  const auto item_of = [&](int32_t j) { return a.ws + ((uint64_t)(base + (uint32_t)j - a.place0) * a.heads + h) * kItemBytes; };
-  u32x4_t kr[kPasses];
+  // What a chunk needs is loaded a chunk ahead, each part when the one before is used: K into LDS by way of registers,
+  // the rest as operands.  Lanes' offsets in a chunk's rows are the same for all chunks.
+  const uint32_t ldq = (uint32_t)a.ldq, ldk = (uint32_t)a.ldk, ldv = (uint32_t)a.ldv, ldo = (uint32_t)a.ldo;
+  const uint32_t klane = 2 * (tid / kPieces * ldk + 8 * (tid % kPieces)), vlane = 2 * (8 * c * ldv + col), olane = 2 * (8 * c * ldo + col),
+                 qlane = 2 * (dealt(0, 0, n) * ldq + 8 * c);
+  u32x4_t kr[kPasses], tw[kTParts][kBlocks], pw[kPParts][kBlocks], qw[2][2][U];
   f32x4_t vr;
+  uint16_t v[2][2][4];
+  const auto item_of = [&](int32_t j) { return a.ws + ((uint64_t)(base + (uint32_t)j - a.place0) * a.heads + h) * kItemBytes; };
+  const auto rows_of = [&](const uint16_t* p, uint64_t ld, int32_t j, uint32_t at, uint32_t width) {
+    return chunk_rows(p + (uint64_t)(q.first + j * kC) * ld + at, ld, min(q.rows - j * kC, kC), width);
+  };
   const auto load_k = [&](int32_t j) {
-    const int32_t count = min(q.rows - j * kC, kC);
+    const __amdgpu_buffer_rsrc_t r = rows_of(a.k, a.ldk, j, kh * DK, DK);
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int32_t r = (int32_t)(tid / kPieces + i * kRows);
-      kr[i] = *reinterpret_cast<const u32x4_t*>(a.k + (uint64_t)(q.first + j * kC + min(r, count - 1)) * a.ldk + kh * DK + 8 * (tid % kPieces));
-      if (r >= count) kr[i] = u32x4_t{0, 0, 0, 0};
-    }
+    for (int i = 0; i < kPasses; ++i) kr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, klane + i * kRows * 2 * ldk, 0, 0);
     if (wave == 0) vr = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 16 * lane);
   };
   const auto store_k = [&](int b) {
@@ -361,96 +383,107 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
       *reinterpret_cast<u32x4_t*>(ksh[b] + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
     if (wave == 0) *reinterpret_cast<f32x4_t*>(&vsh[b][4 * lane]) = vr;
   };
+  const auto load_t = [&](int32_t j) {
+#pragma unroll
+    for (int e = 0; e < kTParts; ++e)
+#pragma unroll
+      for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + (e * kBlocks + i) * kBlockBytes + 16 * lane);
+  };
+  const auto load_p = [&](int32_t j) {
+#pragma unroll
+    for (int e = 0; e < kPParts; ++e)
+#pragma unroll
+      for (int i = 0; i < (int)kBlocks; ++i)
+        pw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + kPAt + (e * kBlocks + i) * kBlockBytes + 16 * lane);
+  };
+  const auto load_q = [&](int32_t j) {
+    const __amdgpu_buffer_rsrc_t r = rows_of(a.q, a.ldq, j, kh * DK, DK);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int u = 0; u < U; ++u) qw[w][hf][u] = __builtin_amdgcn_raw_buffer_load_b128(r, qlane + (32 * w + 4 * hf) * 2 * ldq + 64 * u, 0, 0);
+  };
+  const auto load_v = [&](int32_t j) {
+    const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[w][hf][i] = __builtin_amdgcn_raw_buffer_load_b16(r, vlane + (32 * w + 4 * hf + i) * 2 * ldv, 0, 0);
+  };
   load_k(j0);
+  load_v(j0);
+  load_t(j0);
+  load_q(j0);
+  load_p(j0);
   store_k(j0 & 1);
-  __syncthreads();
+  lds_barrier();
 
   for (int32_t j = j0; j < j1; ++j) {
-    const uint8_t* item = item_of(j);
+    const float decay = *reinterpret_cast<const float*>(item_of(j) + kVecAt + 16 * kC);
     const uint8_t* k = ksh[j & 1];
     const float* vec = vsh[j & 1];
-    const int32_t count = min(q.rows - j * kC, kC);
-    const uint64_t from = (uint64_t)(q.first + j * kC);
-    // what this chunk needs later on
-    u32x4_t tw[kTParts][kBlocks], pw[kPParts][kBlocks], qw[2][2][U];
-#pragma unroll
-    for (int i = 0; i < (int)kBlocks; ++i) {
-#pragma unroll
-      for (int e = 0; e < kTParts; ++e) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item + (e * kBlocks + i) * kBlockBytes + 16 * lane);
-#pragma unroll
-      for (int e = 0; e < kPParts; ++e) pw[e][i] = *reinterpret_cast<const u32x4_t*>(item + kPAt + (e * kBlocks + i) * kBlockBytes + 16 * lane);
-    }
-    uint16_t v[2][2][4];
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t r = 32 * w + 8 * (int32_t)c + 4 * hf + i;
-          v[w][hf][i] = a.v[(from + min(r, count - 1)) * a.ldv + h * a.value_dim + col];
-        }
-        const uint64_t at = from + min((int32_t)dealt(w, hf, n), count - 1);
-#pragma unroll
-        for (int u = 0; u < U; ++u) qw[w][hf][u] = *reinterpret_cast<const u32x4_t*>(a.q + at * a.ldq + kh * DK + 32 * u + 8 * c);
-      }
-    if (j + 1 < j1) load_k(j + 1);
+    const int32_t next = min(j + 1, j1 - 1);
+    load_k(next);
 
-    // the state in parts, K S and Q S
+    // The state in parts, K S and Q S.  Runs of products go over their four tiles first, so that none waits for
+    // the one before.
     f32x4_t ks[2][2], o[2][2];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) ks[w][hf] = o[w][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) ks[t / 2][t % 2] = o[t / 2][t % 2] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    bf16x8_t parts[U][3];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float y[8] = {st[u][0][0], st[u][0][1], st[u][0][2], st[u][0][3], st[u][1][0], st[u][1][1], st[u][1][2], st[u][1][3]};
-      bf16x8_t part[3];
-      split(y, part);
+      split(st[u][0], st[u][1], parts[u]);
+      bf16x8_t kw[4];
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int t = 0; t < 4; ++t)
+        kw[t] = as_operand(*reinterpret_cast<const u32x4_t*>(k + dealt_piece<DK>(dealt(t / 2, t % 2, n), 4 * u + c)));
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const bf16x8_t kw = as_operand(*reinterpret_cast<const u32x4_t*>(k + dealt_piece<DK>(dealt(w, hf, n), 4 * u + c)));
+      for (int e = 2; e >= 0; --e)
 #pragma unroll
-          for (int e = 2; e >= 0; --e) ks[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kw, part[e], ks[w][hf], 0, 0, 0);
-#pragma unroll
-          for (int e = 1; e >= 0; --e)
-            o[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[w][hf][u]), part[e], o[w][hf], 0, 0, 0);
-        }
+        for (int t = 0; t < 4; ++t)
+          ks[t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kw[t], parts[u][e], ks[t / 2][t % 2], 0, 0, 0);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 1; e >= 0; --e)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          o[t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[t / 2][t % 2][u]), parts[u][e], o[t / 2][t % 2], 0, 0, 0);
     // the rows b V - b e^G K S0
     f32x4_t rows[2][2];
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int32_t r = 32 * w + 8 * (int32_t)c + 4 * hf;
+        const uint32_t r = 32 * w + 8 * c + 4 * hf;
         const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows[w][hf][i] = c1[i] * (r + i < count ? bf16_value(v[w][hf][i]) : 0.f) - c2[i] * ks[w][hf][i];
+        for (int i = 0; i < 4; ++i) rows[w][hf][i] = fmaf(-c2[i], ks[w][hf][i], c1[i] * bf16_value(v[w][hf][i]));
       }
+    load_q(next);
+    load_v(next);
     f32x4_t u[2][2];
     const auto solve = [&] {
       bf16x8_t part[2][3];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const float y[8] = {rows[w][0][0], rows[w][0][1], rows[w][0][2], rows[w][0][3], rows[w][1][0], rows[w][1][1], rows[w][1][2], rows[w][1][3]};
-        split(y, part[w]);
-      }
+      for (int w = 0; w < 2; ++w) split(rows[w][0], rows[w][1], part[w]);
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int t = 0; t < 4; ++t) u[t / 2][t % 2] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          u[w][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int e = 2; e >= 0; --e)   // parts whose product is 2^-16, 2^-8 and 1 of the whole
 #pragma unroll
-          for (int e = 2; e >= 0; --e)   // parts whose product is 2^-16, 2^-8 and 1 of the whole
+        for (int f = 0; f <= e; ++f)
 #pragma unroll
-            for (int f = 0; f <= e; ++f)
-#pragma unroll
-              for (int sb = 0; sb <= w; ++sb)
-                u[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(tw[f][2 * w + 2 * sb + hf]), part[sb][e - f], u[w][hf], 0, 0, 0);
-        }
+          for (int b = 0; b < (int)kBlocks; ++b) {
+            const int w = b > 1, sb = b > 3, hf = b & 1;
+            u[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(tw[f][b]), part[sb][e - f], u[w][hf], 0, 0, 0);
+          }
     };
     solve();
     int32_t bad = kC;   // the first of the column's rows that is not finite
@@ -476,36 +509,36 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
           for (int i = 0; i < 4; ++i)
             if (32 * w + 8 * (int32_t)c + 4 * hf + i >= bad) u[w][hf][i] = 0.f;
     }
+    load_t(next);
     // S = decay S + K^T diag(e^(G_end - G)) u
-    const float decay = *reinterpret_cast<const float*>(item + kVecAt + 16 * kC);
     bf16x8_t up[2][3];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      float y[8];
+      f32x4_t y[2];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const f32x4_t c3 = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * hf + i] = c3[i] * u[w][hf][i];
-      }
-      split(y, up[w]);
+      for (int hf = 0; hf < 2; ++hf) y[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf) * u[w][hf];
+      split(y[0], y[1], up[w]);
     }
 #pragma unroll
     for (int ub = 0; ub < U; ++ub)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < 2; ++hf) st[ub][hf] *= decay;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st[ub][hf][i] *= decay;
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          union { s16x4_t half[2]; bf16x8_t all; } kt;   // four tokens of the lane's row of K^T each
+      for (int ub = 0; ub < U; ub += 2) {
+        union { s16x4_t half[2]; bf16x8_t all; } kt[4];   // four tokens of the lane's row of K^T each
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int z = 0; z < 2; ++z)
-            kt.half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t*)(k + dealt_piece<DK>(32 * w + 8 * c + 4 * z + (n >> 2), 4 * ub + (n & 3)) + 8 * hf));
+            kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4_t*)(k + dealt_piece<DK>(32 * w + 8 * c + 4 * z + (n >> 2), 4 * (ub + t / 2) + (n & 3)) + 8 * (t % 2)));
 #pragma unroll
-          for (int e = 2; e >= 0; --e) st[ub][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kt.all, up[w][e], st[ub][hf], 0, 0, 0);
-        }
+        for (int e = 2; e >= 0; --e)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            st[ub + t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kt[t].all, up[w][e], st[ub + t / 2][t % 2], 0, 0, 0);
       }
     if (bad < kC)
 #pragma unroll
@@ -513,36 +546,35 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) st[ub][hf] = f32x4_t{NAN, NAN, NAN, NAN};
     // O = diag(e^G) Q S0 + P u
+    bf16x8_t uq[2][2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const float y[8] = {u[w][0][0], u[w][0][1], u[w][0][2], u[w][0][3], u[w][1][0], u[w][1][1], u[w][1][2], u[w][1][3]};
-      bf16x8_t part[2];
-      split(y, part);
-      up[w][0] = part[0];
-      up[w][1] = part[1];
+      split(u[w][0], u[w][1], uq[w]);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) o[w][hf] *= *reinterpret_cast<const f32x4_t*>(vec + 3 * kC + 32 * w + 8 * c + 4 * hf);
     }
+#pragma unroll
+    for (int e = 1; e >= 0; --e)
+#pragma unroll
+      for (int f = 0; f <= e; ++f)
+#pragma unroll
+        for (int b = 0; b < (int)kBlocks; ++b) {
+          const int w = b > 1, sb = b > 3, hf = b & 1;
+          o[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][b]), uq[sb][e - f], o[w][hf], 0, 0, 0);
+        }
+    load_p(next);
+    const __amdgpu_buffer_rsrc_t ro = rows_of(a.out, a.ldo, j, h * dv, dv);
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int32_t r = 32 * w + 8 * (int32_t)c + 4 * hf;
-        const f32x4_t c4 = *reinterpret_cast<const f32x4_t*>(vec + 3 * kC + r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[w][hf][i] *= c4[i];
-#pragma unroll
-        for (int e = 1; e >= 0; --e)
-#pragma unroll
-          for (int f = 0; f <= e; ++f)
-#pragma unroll
-            for (int sb = 0; sb <= w; ++sb)
-              o[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][2 * w + 2 * sb + hf]), up[sb][e - f], o[w][hf], 0, 0, 0);
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (r + i < count)
-            a.out[(from + r + i) * a.ldo + h * a.value_dim + col] = __builtin_bit_cast(uint16_t, (__bf16)(r + i >= bad ? NAN : o[w][hf][i]));
-      }
-    if (j + 1 < j1) store_k((j + 1) & 1);
-    __syncthreads();
+          __builtin_amdgcn_raw_buffer_store_b16(
+              __builtin_bit_cast(uint16_t, (__bf16)(32 * w + 8 * (int32_t)c + 4 * hf + i >= bad ? NAN : o[w][hf][i])), ro,
+              olane + (32 * w + 4 * hf + i) * 2 * ldo, 0, 0);
+    store_k((j + 1) & 1);
+    lds_barrier();
   }
   if (after)
 #pragma unroll
@@ -550,7 +582,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) after[(uint64_t)(32 * u + 4 * hf + i) * a.value_dim] = st[u][hf][i];
+        for (int i = 0; i < 4; ++i) after[(uint64_t)(32 * u + 4 * hf + i) * dv] = st[u][hf][i];
 }
 
 template <int DK>

@@ -194,7 +194,8 @@ def test_delta_refusals():
     for kw in (dict(desc=(0, 4, 64, 32, 0, 1)), dict(desc=(3, 4, 64, 32, 0, 1)), dict(desc=(2, 0, 64, 32, 0, 1)),
                dict(desc=(2, 4, 96, 32, 0, 1)), dict(desc=(2, 4, 64, 40, 0, 1)), dict(desc=(2, 4, 64, 288, 0, 1)),
                dict(desc=(1, 1025, 64, 32, 0, 1)), dict(n=(1 << 24) + 1), dict(seqs=(1 << 24) + 1),
-               dict(new=(1 << 24) + 1), dict(n_slots=(1 << 24) + 1)):
+               dict(new=(1 << 24) + 1), dict(n_slots=(1 << 24) + 1), dict(ldq=(1 << 24) + 8), dict(ldk=(1 << 24) + 8),
+               dict(ldv=(1 << 24) + 8), dict(ldo=(1 << 24) + 8)):
         assert call(**kw) == SHAPE, kw
     for name in ("q", "k", "v", "out", "state"):
         assert call(**{name: p[name] + 8}) == ALIGN, name
