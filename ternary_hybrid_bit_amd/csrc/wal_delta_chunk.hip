@@ -319,270 +319,311 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
   }
 }
 
-constexpr int kScanWaves = 2;
+constexpr int kScanGroups = 2;   // groups of 16 columns of a workgroup
 
 // Rows of a chunk in memory: what lies behind the last one reads as zeros and is not written.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, uint64_t ld, int32_t count, uint32_t width) {
   return rsrc(p, (uint32_t)(2 * ((uint64_t)(count - 1) * ld + width)));
 }
 
+// Two wavefronts share 16 columns, each on a SIMD of its own: the first takes the states from chunk to chunk, which is
+// what a sequence waits for, the second, a chunk behind, makes the outputs from the states and rows that the first leaves in
+// LDS as operands, and brings the next K.  (One wavefront for both: 559 us instead of @@ us for a prompt of 8192 tokens.)
 template <int DK>
-__global__ __launch_bounds__(64 * kScanWaves, 1) void k_delta_scan(Delta a) {
-  constexpr int U = DK / 32;                       // 32-row blocks of the state
-  constexpr uint32_t kPieces = DK / 8, kRows = 64 * kScanWaves / kPieces;
-  constexpr int kPasses = kC / (int)kRows;
-  __shared__ __attribute__((aligned(256))) uint8_t ksh[2][kC * DK * 2];
-  __shared__ __attribute__((aligned(16))) float vsh[2][4 * kC];
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, c = lane >> 4;
+struct Scan {
+  static constexpr int U = DK / 32;                       // 32-row blocks of the state
+  static constexpr uint32_t kPieces = DK / 8, kRows = 64 * kScanGroups / kPieces;
+  static constexpr int kPasses = kC / (int)kRows;
+  struct Shared {
+    __attribute__((aligned(256))) uint8_t k[2][kC * DK * 2];
+    u32x4_t parts[2][kScanGroups][U][2][64];              // of the states before a chunk
+    f32x4_t u[2][kScanGroups][2][2][64];
+    __attribute__((aligned(16))) float vec[2][4 * kC];
+    int32_t bad[2][kScanGroups][16];                      // the first of a column's rows that is not finite
+  };
+  const Delta& a;
+  Shared& sh;
+  const Seq q;
+  const uint32_t base, h, kh, col, lane, n, c, group;
+  const int32_t j0, j1;
+
+  __device__ __forceinline__ const uint8_t* item_of(int32_t j) const {
+    return a.ws + ((uint64_t)(base + (uint32_t)j - a.place0) * a.heads + h) * kItemBytes;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint16_t* p, uint64_t ld, int32_t j, uint32_t at, uint32_t width) const {
+    return chunk_rows(p + (uint64_t)(q.first + j * kC) * ld + at, ld, min(q.rows - j * kC, kC), width);
+  }
+
+  // The first wavefront: u and the state after each chunk.  What a chunk needs is loaded a chunk ahead, each part when
+  // the one before is used.  Runs of products go over their tiles first, so that none waits for the one before.
+  __device__ __forceinline__ void states(const float* before, float* after) {
+    const uint32_t dv = a.value_dim, ldv = (uint32_t)a.ldv, vlane = 2 * (8 * c * ldv + col);
+    f32x4_t st[U][2];   // element i: row 32 u + 8 c + 4 h + i
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(32 * u + 4 * hf + i) * dv] : 0.f;
+    u32x4_t tw[kTParts][kBlocks];
+    uint16_t v[2][2][4];
+    const auto load_t = [&](int32_t j) {
+#pragma unroll
+      for (int e = 0; e < kTParts; ++e)
+#pragma unroll
+        for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + (e * kBlocks + i) * kBlockBytes + 16 * lane);
+    };
+    const auto load_v = [&](int32_t j) {
+      const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[w][hf][i] = __builtin_amdgcn_raw_buffer_load_b16(r, vlane + (32 * w + 4 * hf + i) * 2 * ldv, 0, 0);
+    };
+    load_v(j0);
+    load_t(j0);
+    lds_barrier();
+    for (int32_t j = j0; j < j1; ++j) {
+      const float decay = *reinterpret_cast<const float*>(item_of(j) + kVecAt + 16 * kC);
+      const uint8_t* k = sh.k[j & 1];
+      const float* vec = sh.vec[j & 1];
+      const int32_t next = min(j + 1, j1 - 1);
+      // the state in parts, and K S
+      f32x4_t ks[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ks[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        bf16x8_t part[3], kw[4];
+        split(st[u][0], st[u][1], part);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sh.parts[j & 1][group][u][e][lane] = __builtin_bit_cast(u32x4_t, part[e]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          kw[t] = as_operand(*reinterpret_cast<const u32x4_t*>(k + dealt_piece<DK>(dealt(t / 2, t % 2, n), 4 * u + c)));
+#pragma unroll
+        for (int e = 2; e >= 0; --e)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) ks[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kw[t], part[e], ks[t], 0, 0, 0);
+      }
+      // the rows b V - b e^G K S0
+      f32x4_t rows[2][2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t r = 32 * w + 8 * c + 4 * hf;
+          const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rows[w][hf][i] = fmaf(-c2[i], ks[2 * w + hf][i], c1[i] * bf16_value(v[w][hf][i]));
+        }
+      load_v(next);
+      f32x4_t u[2][2];
+      const auto solve = [&] {
+        bf16x8_t part[2][3];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) split(rows[w][0], rows[w][1], part[w]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t / 2][t % 2] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 2; e >= 0; --e)   // parts whose product is 2^-16, 2^-8 and 1 of the whole
+#pragma unroll
+          for (int f = 0; f <= e; ++f)
+#pragma unroll
+            for (int b = 0; b < (int)kBlocks; ++b) {
+              const int w = b > 1, sb = b > 3, hf = b & 1;
+              u[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(tw[f][b]), part[sb][e - f], u[w][hf], 0, 0, 0);
+            }
+      };
+      solve();
+      int32_t bad = kC;
+      if (__any(!(fabsf(u[0][0][0]) < INFINITY) || !(fabsf(u[1][0][0]) < INFINITY))) {
+#pragma unroll
+        for (int w = 1; w >= 0; --w)
+#pragma unroll
+          for (int hf = 1; hf >= 0; --hf)
+#pragma unroll
+            for (int i = 3; i >= 0; --i)
+              if (!(fabsf(rows[w][hf][i]) < INFINITY)) {
+                bad = 32 * w + 8 * (int32_t)c + 4 * hf + i;
+                rows[w][hf][i] = 0.f;
+              }
+        bad = min(bad, __shfl_xor(bad, 16));
+        bad = min(bad, __shfl_xor(bad, 32));
+        solve();
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (32 * w + 8 * (int32_t)c + 4 * hf + i >= bad) u[w][hf][i] = 0.f;
+      }
+      load_t(next);
+      if (c == 0) sh.bad[j & 1][group][n] = bad;
+      // S = decay S + K^T diag(e^(G_end - G)) u
+      bf16x8_t up[2][3];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        f32x4_t y[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          sh.u[j & 1][group][w][hf][lane] = u[w][hf];
+          y[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf) * u[w][hf];
+        }
+        split(y[0], y[1], up[w]);
+      }
+#pragma unroll
+      for (int ub = 0; ub < U; ++ub)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) st[ub][hf] *= decay;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int ub = 0; ub < U; ub += 2) {
+          union { s16x4_t half[2]; bf16x8_t all; } kt[4];   // four tokens of the lane's row of K^T each
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (lds_s16x4_t*)(k + dealt_piece<DK>(32 * w + 8 * c + 4 * z + (n >> 2), 4 * (ub + t / 2) + (n & 3)) + 8 * (t % 2)));
+#pragma unroll
+          for (int e = 2; e >= 0; --e)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              st[ub + t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kt[t].all, up[w][e], st[ub + t / 2][t % 2], 0, 0, 0);
+        }
+      if (__any(bad < kC)) {
+#pragma unroll
+        for (int ub = 0; ub < U; ++ub)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[ub][hf][i] = bad < kC ? NAN : st[ub][hf][i];
+      }
+      lds_barrier();
+    }
+    if (after)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) after[(uint64_t)(32 * u + 4 * hf + i) * dv] = st[u][hf][i];
+  }
+
+  // The second wavefront: K of the chunk after, and the outputs of the chunk before, O = diag(e^G) Q S0 + P u.
+  __device__ __forceinline__ void outputs() {
+    const uint32_t dv = a.value_dim, ldq = (uint32_t)a.ldq, ldk = (uint32_t)a.ldk, ldo = (uint32_t)a.ldo, tid = 64 * group + lane;
+    const uint32_t klane = 2 * (tid / kPieces * ldk + 8 * (tid % kPieces)), olane = 2 * (8 * c * ldo + col), qlane = 2 * (dealt(0, 0, n) * ldq + 8 * c);
+    u32x4_t kr[kPasses], pw[kPParts][kBlocks], qw[4][U];
+    f32x4_t vr, c4[4];
+    const auto load_k = [&](int32_t j) {
+      const __amdgpu_buffer_rsrc_t r = rows_of(a.k, a.ldk, j, kh * DK, DK);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) kr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, klane + i * kRows * 2 * ldk, 0, 0);
+      if (group == 0) vr = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 16 * lane);
+    };
+    const auto store_k = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        *reinterpret_cast<u32x4_t*>(sh.k[b] + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
+      if (group == 0) *reinterpret_cast<f32x4_t*>(&sh.vec[b][4 * lane]) = vr;
+    };
+    const auto load_pq = [&](int32_t j) {
+      const __amdgpu_buffer_rsrc_t r = rows_of(a.q, a.ldq, j, kh * DK, DK);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) qw[t][u] = __builtin_amdgcn_raw_buffer_load_b128(r, qlane + (16 * (t & 2) + 4 * (t & 1)) * 2 * ldq + 64 * u, 0, 0);
+        c4[t] = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 4 * (3 * kC + 16 * (t & 2) + 8 * c + 4 * (t & 1)));
+      }
+#pragma unroll
+      for (int e = 0; e < kPParts; ++e)
+#pragma unroll
+        for (int i = 0; i < (int)kBlocks; ++i)
+          pw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + kPAt + (e * kBlocks + i) * kBlockBytes + 16 * lane);
+    };
+    load_k(j0);
+    load_pq(j0);
+    store_k(j0 & 1);
+    lds_barrier();
+    for (int32_t j = j0; j <= j1; ++j) {
+      if (j < j1 - 1) load_k(j + 1);
+      if (j > j0) {
+        const int b = (j - 1) & 1;
+        f32x4_t o[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 1; e >= 0; --e) {
+            const bf16x8_t part = as_operand(sh.parts[b][group][u][e][lane]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[t][u]), part, o[t], 0, 0, 0);
+          }
+        bf16x8_t part[2][2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) split(sh.u[b][group][w][0][lane], sh.u[b][group][w][1][lane], part[w]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t] *= c4[t];
+#pragma unroll
+        for (int e = 1; e >= 0; --e)
+#pragma unroll
+          for (int f = 0; f <= e; ++f)
+#pragma unroll
+            for (int i = 0; i < (int)kBlocks; ++i) {
+              const int t = 2 * (i > 1) + (i & 1);
+              o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][i]), part[i > 3][e - f], o[t], 0, 0, 0);
+            }
+        load_pq(min(j, j1 - 1));
+        const int32_t bad = sh.bad[b][group][n];
+        if (__any(bad < kC)) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i >= bad) o[t][i] = NAN;
+        }
+        const __amdgpu_buffer_rsrc_t r = rows_of(a.out, a.ldo, j - 1, h * dv, dv);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)o[t][i]), r,
+                                                  olane + (16 * (t & 2) + 4 * (t & 1) + i) * 2 * ldo, 0, 0);
+      }
+      if (j < j1 - 1) store_k((j + 1) & 1);
+      if (j < j1) lds_barrier();
+    }
+  }
+};
+
+template <int DK>
+__global__ __launch_bounds__(128 * kScanGroups, 1) void k_delta_scan(Delta a) {
+  __shared__ typename Scan<DK>::Shared sh;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, c = lane >> 4;
+  const uint32_t group = wave % kScanGroups;
   // The workgroups of a head sit on one chiplet, so that its cache serves what they share: blocks go to the eight
   // chiplets in turn.
   const uint32_t x = blockIdx.x % 8, g = blockIdx.x / 8, pair = g / a.slices * 8 + x;
   if (pair >= a.n_seqs * a.heads) return;
-  const uint32_t s = pair / a.heads, h = pair % a.heads, kh = h / a.group, dv = a.value_dim;
-  const uint32_t col = kSlice * (g % a.slices) + 16 * wave + n;
+  const uint32_t s = pair / a.heads, h = pair % a.heads, col = kSlice * (g % a.slices) + 16 * group + n;
   const Seq q = delta_seq(a, s);
   const uint32_t base = (uint32_t)q.first / kC + s;
   const int32_t chunks = (q.rows + kC - 1) / kC;
   const int32_t j0 = max(0, (int32_t)a.place0 - (int32_t)base), j1 = min(chunks, (int32_t)(a.place0 + a.places) - (int32_t)base);
   if (j0 >= j1) return;
   const int64_t slot = kept_at(a, s);
-  const uint64_t head_at = ((uint64_t)h * DK + 8 * c) * dv + col;
-  float* kept = slot < 0 ? nullptr : a.state + (uint64_t)slot * a.heads * DK * dv + head_at;
-  const float* before = j0 ? a.carry[0] + head_at : kept;
-  float* after = j1 < chunks ? a.carry[1] + head_at : kept;
-
-  f32x4_t st[U][2];   // element i: row 32 u + 8 c + 4 h + i
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(32 * u + 4 * hf + i) * dv] : 0.f;
-
-  // What a chunk needs is loaded a chunk ahead, each part when the one before is used: K into LDS by way of registers,
-  // the rest as operands.  Lanes' offsets in a chunk's rows are the same for all chunks.
-  const uint32_t ldq = (uint32_t)a.ldq, ldk = (uint32_t)a.ldk, ldv = (uint32_t)a.ldv, ldo = (uint32_t)a.ldo;
-  const uint32_t klane = 2 * (tid / kPieces * ldk + 8 * (tid % kPieces)), vlane = 2 * (8 * c * ldv + col), olane = 2 * (8 * c * ldo + col),
-                 qlane = 2 * (dealt(0, 0, n) * ldq + 8 * c);
-  u32x4_t kr[kPasses], tw[kTParts][kBlocks], pw[kPParts][kBlocks], qw[2][2][U];
-  f32x4_t vr;
-  uint16_t v[2][2][4];
-  const auto item_of = [&](int32_t j) { return a.ws + ((uint64_t)(base + (uint32_t)j - a.place0) * a.heads + h) * kItemBytes; };
-  const auto rows_of = [&](const uint16_t* p, uint64_t ld, int32_t j, uint32_t at, uint32_t width) {
-    return chunk_rows(p + (uint64_t)(q.first + j * kC) * ld + at, ld, min(q.rows - j * kC, kC), width);
-  };
-  const auto load_k = [&](int32_t j) {
-    const __amdgpu_buffer_rsrc_t r = rows_of(a.k, a.ldk, j, kh * DK, DK);
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) kr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, klane + i * kRows * 2 * ldk, 0, 0);
-    if (wave == 0) vr = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 16 * lane);
-  };
-  const auto store_k = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<u32x4_t*>(ksh[b] + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
-    if (wave == 0) *reinterpret_cast<f32x4_t*>(&vsh[b][4 * lane]) = vr;
-  };
-  const auto load_t = [&](int32_t j) {
-#pragma unroll
-    for (int e = 0; e < kTParts; ++e)
-#pragma unroll
-      for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + (e * kBlocks + i) * kBlockBytes + 16 * lane);
-  };
-  const auto load_p = [&](int32_t j) {
-#pragma unroll
-    for (int e = 0; e < kPParts; ++e)
-#pragma unroll
-      for (int i = 0; i < (int)kBlocks; ++i)
-        pw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + kPAt + (e * kBlocks + i) * kBlockBytes + 16 * lane);
-  };
-  const auto load_q = [&](int32_t j) {
-    const __amdgpu_buffer_rsrc_t r = rows_of(a.q, a.ldq, j, kh * DK, DK);
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int u = 0; u < U; ++u) qw[w][hf][u] = __builtin_amdgcn_raw_buffer_load_b128(r, qlane + (32 * w + 4 * hf) * 2 * ldq + 64 * u, 0, 0);
-  };
-  const auto load_v = [&](int32_t j) {
-    const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[w][hf][i] = __builtin_amdgcn_raw_buffer_load_b16(r, vlane + (32 * w + 4 * hf + i) * 2 * ldv, 0, 0);
-  };
-  load_k(j0);
-  load_v(j0);
-  load_t(j0);
-  load_q(j0);
-  load_p(j0);
-  store_k(j0 & 1);
-  lds_barrier();
-
-  for (int32_t j = j0; j < j1; ++j) {
-    const float decay = *reinterpret_cast<const float*>(item_of(j) + kVecAt + 16 * kC);
-    const uint8_t* k = ksh[j & 1];
-    const float* vec = vsh[j & 1];
-    const int32_t next = min(j + 1, j1 - 1);
-    load_k(next);
-
-    // The state in parts, K S and Q S.  Runs of products go over their four tiles first, so that none waits for
-    // the one before.
-    f32x4_t ks[2][2], o[2][2];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) ks[t / 2][t % 2] = o[t / 2][t % 2] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    bf16x8_t parts[U][3];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      split(st[u][0], st[u][1], parts[u]);
-      bf16x8_t kw[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        kw[t] = as_operand(*reinterpret_cast<const u32x4_t*>(k + dealt_piece<DK>(dealt(t / 2, t % 2, n), 4 * u + c)));
-#pragma unroll
-      for (int e = 2; e >= 0; --e)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          ks[t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kw[t], parts[u][e], ks[t / 2][t % 2], 0, 0, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 1; e >= 0; --e)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          o[t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[t / 2][t % 2][u]), parts[u][e], o[t / 2][t % 2], 0, 0, 0);
-    // the rows b V - b e^G K S0
-    f32x4_t rows[2][2];
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t r = 32 * w + 8 * c + 4 * hf;
-        const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rows[w][hf][i] = fmaf(-c2[i], ks[w][hf][i], c1[i] * bf16_value(v[w][hf][i]));
-      }
-    load_q(next);
-    load_v(next);
-    f32x4_t u[2][2];
-    const auto solve = [&] {
-      bf16x8_t part[2][3];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) split(rows[w][0], rows[w][1], part[w]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) u[t / 2][t % 2] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int e = 2; e >= 0; --e)   // parts whose product is 2^-16, 2^-8 and 1 of the whole
-#pragma unroll
-        for (int f = 0; f <= e; ++f)
-#pragma unroll
-          for (int b = 0; b < (int)kBlocks; ++b) {
-            const int w = b > 1, sb = b > 3, hf = b & 1;
-            u[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(tw[f][b]), part[sb][e - f], u[w][hf], 0, 0, 0);
-          }
-    };
-    solve();
-    int32_t bad = kC;   // the first of the column's rows that is not finite
-    if (__any(!(fabsf(u[0][0][0]) < INFINITY) || !(fabsf(u[1][0][0]) < INFINITY))) {
-#pragma unroll
-      for (int w = 1; w >= 0; --w)
-#pragma unroll
-        for (int hf = 1; hf >= 0; --hf)
-#pragma unroll
-          for (int i = 3; i >= 0; --i)
-            if (!(fabsf(rows[w][hf][i]) < INFINITY)) {
-              bad = 32 * w + 8 * (int32_t)c + 4 * hf + i;
-              rows[w][hf][i] = 0.f;
-            }
-      bad = min(bad, __shfl_xor(bad, 16));
-      bad = min(bad, __shfl_xor(bad, 32));
-      solve();
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (32 * w + 8 * (int32_t)c + 4 * hf + i >= bad) u[w][hf][i] = 0.f;
-    }
-    load_t(next);
-    // S = decay S + K^T diag(e^(G_end - G)) u
-    bf16x8_t up[2][3];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      f32x4_t y[2];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) y[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf) * u[w][hf];
-      split(y[0], y[1], up[w]);
-    }
-#pragma unroll
-    for (int ub = 0; ub < U; ++ub)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) st[ub][hf] *= decay;
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int ub = 0; ub < U; ub += 2) {
-        union { s16x4_t half[2]; bf16x8_t all; } kt[4];   // four tokens of the lane's row of K^T each
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int z = 0; z < 2; ++z)
-            kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t*)(k + dealt_piece<DK>(32 * w + 8 * c + 4 * z + (n >> 2), 4 * (ub + t / 2) + (n & 3)) + 8 * (t % 2)));
-#pragma unroll
-        for (int e = 2; e >= 0; --e)
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            st[ub + t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kt[t].all, up[w][e], st[ub + t / 2][t % 2], 0, 0, 0);
-      }
-    if (bad < kC)
-#pragma unroll
-      for (int ub = 0; ub < U; ++ub)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) st[ub][hf] = f32x4_t{NAN, NAN, NAN, NAN};
-    // O = diag(e^G) Q S0 + P u
-    bf16x8_t uq[2][2];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      split(u[w][0], u[w][1], uq[w]);
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) o[w][hf] *= *reinterpret_cast<const f32x4_t*>(vec + 3 * kC + 32 * w + 8 * c + 4 * hf);
-    }
-#pragma unroll
-    for (int e = 1; e >= 0; --e)
-#pragma unroll
-      for (int f = 0; f <= e; ++f)
-#pragma unroll
-        for (int b = 0; b < (int)kBlocks; ++b) {
-          const int w = b > 1, sb = b > 3, hf = b & 1;
-          o[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][b]), uq[sb][e - f], o[w][hf], 0, 0, 0);
-        }
-    load_p(next);
-    const __amdgpu_buffer_rsrc_t ro = rows_of(a.out, a.ldo, j, h * dv, dv);
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_buffer_store_b16(
-              __builtin_bit_cast(uint16_t, (__bf16)(32 * w + 8 * (int32_t)c + 4 * hf + i >= bad ? NAN : o[w][hf][i])), ro,
-              olane + (32 * w + 4 * hf + i) * 2 * ldo, 0, 0);
-    store_k((j + 1) & 1);
-    lds_barrier();
-  }
-  if (after)
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) after[(uint64_t)(32 * u + 4 * hf + i) * dv] = st[u][hf][i];
+  const uint64_t head_at = ((uint64_t)h * DK + 8 * c) * a.value_dim + col;
+  float* kept = slot < 0 ? nullptr : a.state + (uint64_t)slot * a.heads * DK * a.value_dim + head_at;
+  Scan<DK> scan{a, sh, q, base, h, h / a.group, col, lane, n, c, group, j0, j1};
+  if (wave < kScanGroups) scan.states(j0 ? a.carry[0] + head_at : kept, j1 < chunks ? a.carry[1] + head_at : kept);
+  else scan.outputs();
 }
 
 template <int DK>
@@ -596,7 +637,7 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
     const uint64_t blocks = ((uint64_t)a.n_seqs * a.heads + 7) / 8 * 8 * a.slices;
     if (items > 0x7FFFFFFFull || blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
     hipLaunchKernelGGL((k_delta_chunk<DK>), dim3((uint32_t)items), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(64 * kScanWaves), 0, s, a);
+    hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(128 * kScanGroups), 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
@@ -606,7 +647,7 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
 namespace wal {
 
 int delta_chunks(Delta& a, uint32_t key_dim, uint32_t all, void* stream) {
-  static_assert(kScanWaves * 16 == kSlice, "a workgroup takes a slice");
+  static_assert(kScanGroups * 16 == kSlice, "a workgroup takes a slice");
   hipStream_t s = static_cast<hipStream_t>(stream);
   return key_dim == 64 ? launch<64>(a, all, s) : launch<128>(a, all, s);
 }
