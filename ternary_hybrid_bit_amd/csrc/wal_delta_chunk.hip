@@ -365,6 +365,9 @@ struct Scan {
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(32 * u + 4 * hf + i) * dv] : 0.f;
+    // Lanes' places in K: of rows dealt(0, 0, n), and for the transposing reads; a 32-column block further is an exclusive
+    // or with 64 bytes, and rows 4 hf and 32 w further change no bits that the pieces' exchange looks at.
+    const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c), tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3);
     u32x4_t tw[kTParts][kBlocks];
     uint16_t v[2][2][4];
     const auto load_t = [&](int32_t j) {
@@ -386,7 +389,8 @@ struct Scan {
     load_t(j0);
     lds_barrier();
     for (int32_t j = j0; j < j1; ++j) {
-      const float decay = *reinterpret_cast<const float*>(item_of(j) + kVecAt + 16 * kC);
+      const float decay = *reinterpret_cast<const __attribute__((address_space(4))) float*>(
+          reinterpret_cast<uintptr_t>(item_of(j) + kVecAt + 16 * kC));
       const uint8_t* k = sh.k[j & 1];
       const float* vec = sh.vec[j & 1];
       const int32_t next = min(j + 1, j1 - 1);
@@ -402,7 +406,7 @@ struct Scan {
         for (int e = 0; e < 2; ++e) sh.parts[j & 1][group][u][e][lane] = __builtin_bit_cast(u32x4_t, part[e]);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          kw[t] = as_operand(*reinterpret_cast<const u32x4_t*>(k + dealt_piece<DK>(dealt(t / 2, t % 2, n), 4 * u + c)));
+          kw[t] = as_operand(*reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK));
 #pragma unroll
         for (int e = 2; e >= 0; --e)
 #pragma unroll
@@ -489,7 +493,7 @@ struct Scan {
 #pragma unroll
             for (int z = 0; z < 2; ++z)
               kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (lds_s16x4_t*)(k + dealt_piece<DK>(32 * w + 8 * c + 4 * z + (n >> 2), 4 * (ub + t / 2) + (n & 3)) + 8 * (t % 2)));
+                  (lds_s16x4_t*)(k + (tat ^ 64 * (ub + t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
 #pragma unroll
           for (int e = 2; e >= 0; --e)
 #pragma unroll
@@ -520,20 +524,21 @@ struct Scan {
     const uint32_t dv = a.value_dim, ldq = (uint32_t)a.ldq, ldk = (uint32_t)a.ldk, ldo = (uint32_t)a.ldo, tid = 64 * group + lane;
     const uint32_t klane = 2 * (tid / kPieces * ldk + 8 * (tid % kPieces)), olane = 2 * (8 * c * ldo + col), qlane = 2 * (dealt(0, 0, n) * ldq + 8 * c);
     u32x4_t kr[kPasses], pw[kPParts][kBlocks], qw[4][U];
-    f32x4_t vr, c4[4];
+    f32x4_t c4[4];
+    float2 vr;
     const auto load_k = [&](int32_t j) {
       const __amdgpu_buffer_rsrc_t r = rows_of(a.k, a.ldk, j, kh * DK, DK);
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) kr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, klane + i * kRows * 2 * ldk, 0, 0);
-      if (group == 0) vr = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 16 * lane);
+      vr = *reinterpret_cast<const float2*>(item_of(j) + kVecAt + 8 * tid);
     };
     const auto store_k = [&](int b) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
         *reinterpret_cast<u32x4_t*>(sh.k[b] + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
-      if (group == 0) *reinterpret_cast<f32x4_t*>(&sh.vec[b][4 * lane]) = vr;
+      *reinterpret_cast<float2*>(&sh.vec[b][2 * tid]) = vr;
     };
-    const auto load_pq = [&](int32_t j) {
+    const auto load_q = [&](int32_t j) {
       const __amdgpu_buffer_rsrc_t r = rows_of(a.q, a.ldq, j, kh * DK, DK);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -541,6 +546,8 @@ struct Scan {
         for (int u = 0; u < U; ++u) qw[t][u] = __builtin_amdgcn_raw_buffer_load_b128(r, qlane + (16 * (t & 2) + 4 * (t & 1)) * 2 * ldq + 64 * u, 0, 0);
         c4[t] = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 4 * (3 * kC + 16 * (t & 2) + 8 * c + 4 * (t & 1)));
       }
+    };
+    const auto load_p = [&](int32_t j) {
 #pragma unroll
       for (int e = 0; e < kPParts; ++e)
 #pragma unroll
@@ -548,57 +555,56 @@ struct Scan {
           pw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + kPAt + (e * kBlocks + i) * kBlockBytes + 16 * lane);
     };
     load_k(j0);
-    load_pq(j0);
     store_k(j0 & 1);
     lds_barrier();
-    for (int32_t j = j0; j <= j1; ++j) {
-      if (j < j1 - 1) load_k(j + 1);
-      if (j > j0) {
-        const int b = (j - 1) & 1;
-        f32x4_t o[4];
+    load_k(min(j0 + 1, j1 - 1));
+    load_p(j0);
+    load_q(j0);
+    store_k((j0 + 1) & 1);
+    load_k(min(j0 + 2, j1 - 1));
+    lds_barrier();
+    for (int32_t j = j0; j < j1; ++j) {
+      // the states' wavefront is at chunk j + 1, whose K is there
+      f32x4_t o[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < 4; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      store_k(j & 1);   // of chunk j + 2: all are done with chunk j's
+      load_k(min(j + 3, j1 - 1));
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 1; e >= 0; --e) {
-            const bf16x8_t part = as_operand(sh.parts[b][group][u][e][lane]);
+        for (int e = 1; e >= 0; --e) {
+          const bf16x8_t part = as_operand(sh.parts[j & 1][group][u][e][lane]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[t][u]), part, o[t], 0, 0, 0);
-          }
-        bf16x8_t part[2][2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) split(sh.u[b][group][w][0][lane], sh.u[b][group][w][1][lane], part[w]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) o[t] *= c4[t];
-#pragma unroll
-        for (int e = 1; e >= 0; --e)
-#pragma unroll
-          for (int f = 0; f <= e; ++f)
-#pragma unroll
-            for (int i = 0; i < (int)kBlocks; ++i) {
-              const int t = 2 * (i > 1) + (i & 1);
-              o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][i]), part[i > 3][e - f], o[t], 0, 0, 0);
-            }
-        load_pq(min(j, j1 - 1));
-        const int32_t bad = sh.bad[b][group][n];
-        if (__any(bad < kC)) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i >= bad) o[t][i] = NAN;
+          for (int t = 0; t < 4; ++t) o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[t][u]), part, o[t], 0, 0, 0);
         }
-        const __amdgpu_buffer_rsrc_t r = rows_of(a.out, a.ldo, j - 1, h * dv, dv);
+      bf16x8_t part[2][2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+      for (int w = 0; w < 2; ++w) split(sh.u[j & 1][group][w][0][lane], sh.u[j & 1][group][w][1][lane], part[w]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)o[t][i]), r,
-                                                  olane + (16 * (t & 2) + 4 * (t & 1) + i) * 2 * ldo, 0, 0);
-      }
-      if (j < j1 - 1) store_k((j + 1) & 1);
-      if (j < j1) lds_barrier();
+      for (int t = 0; t < 4; ++t) o[t] *= c4[t];
+      load_q(min(j + 1, j1 - 1));
+#pragma unroll
+      for (int e = 1; e >= 0; --e)
+#pragma unroll
+        for (int f = 0; f <= e; ++f)
+#pragma unroll
+          for (int i = 0; i < (int)kBlocks; ++i) {
+            const int t = 2 * (i > 1) + (i & 1);
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][i]), part[i > 3][e - f], o[t], 0, 0, 0);
+          }
+      load_p(min(j + 1, j1 - 1));
+      const int32_t bad = sh.bad[j & 1][group][n];
+      const __amdgpu_buffer_rsrc_t r = rows_of(a.out, a.ldo, j, h * dv, dv);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t row = 16 * (t & 2) + 4 * (t & 1) + i;
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)((int32_t)(row + 8 * c) >= bad ? NAN : o[t][i])), r,
+                                                olane + row * 2 * ldo, 0, 0);
+        }
+      if (j + 1 < j1) lds_barrier();   // (the other wavefronts have met here once less)
     }
   }
 };
