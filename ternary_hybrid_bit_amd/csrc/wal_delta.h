@@ -9,9 +9,14 @@ namespace wal {
 
 constexpr uint32_t kSlice = 32;   // columns of a state that a workgroup takes
 constexpr int kChunk = 64;        // tokens that meet in products
-// What the scan over chunks reads of a chunk and head: T and P in parts, as operands, and the factors of its rows.
-constexpr int kTParts = 3, kPParts = 2;
-constexpr uint32_t kPAt = kTParts * 6 * 1024, kVecAt = kPAt + kPParts * 6 * 1024, kItemBytes = kVecAt + 5 * 256;
+// What the scan over chunks reads, by the place of a chunk: of a key head K by rows and Q as operands, of a value head
+// T in two parts and P as operands and the factors of the rows (all but the factors in half precision).
+constexpr uint32_t kOperand = 1024, kTriangle = 6 * kOperand;   // 16 bytes a lane; a 64 x 64 lower triangle
+constexpr uint32_t kPAt = 2 * kTriangle, kVecAt = kPAt + kTriangle, kItemBytes = kVecAt + 6 * 256;
+constexpr uint32_t key_item_bytes(uint32_t key_dim) { return 2 * kChunk * 2 * key_dim; }
+constexpr uint64_t place_bytes(uint32_t key_heads, uint32_t heads, uint32_t key_dim) {
+  return (uint64_t)key_heads * key_item_bytes(key_dim) + (uint64_t)heads * kItemBytes;
+}
 
 struct Delta {
   const uint16_t* q;
@@ -31,9 +36,10 @@ struct Delta {
   float eps, scale;              // eps 0: q and k as they are
   // calls on chunks: sequence s has the places from starts[s] / 64 + s on, one for each chunk; a launch takes `places`
   // of them from place0, and a sequence that goes on leaves its state in carry[1] and finds it in carry[0]
-  uint8_t* ws;
+  uint8_t* ws;                   // of value heads
+  uint8_t* key_ws;               // of key heads
   float* carry[2];
-  uint32_t place0, places;
+  uint32_t place0, places, key_item;
 };
 
 // Launches (wal_status).

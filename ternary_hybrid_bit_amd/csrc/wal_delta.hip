@@ -22,7 +22,7 @@ Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_
   Plan p{};
   p.step = max_new <= kFewRows;
   if (p.step || !n || !n_seqs) return p;
-  const uint64_t place = (uint64_t)d->value_heads * kItemBytes, most = kMaxItems / place;
+  const uint64_t place = place_bytes(d->key_heads, d->value_heads, d->key_dim), most = kMaxItems / place;
   p.all = n / kChunk + n_seqs;
   p.places = p.all <= most ? p.all : most ? (uint32_t)most : 1;
   p.carry = p.places < p.all ? 4ull * d->value_heads * d->key_dim * d->value_dim : 0;
@@ -113,8 +113,10 @@ extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ld
   const Plan p = plan_of(d, n_seqs, n, max_new);
   if (p.step) return delta_step(a, d->key_dim, stream);
   a.ws = static_cast<uint8_t*>(ws_dev);
+  a.key_ws = a.ws + (uint64_t)p.places * d->value_heads * kItemBytes;
+  a.key_item = key_item_bytes(d->key_dim);
   a.places = p.places;
-  a.carry[0] = reinterpret_cast<float*>(a.ws + (uint64_t)p.places * d->value_heads * kItemBytes);
+  a.carry[0] = reinterpret_cast<float*>(a.ws + p.places * place_bytes(d->key_heads, d->value_heads, d->key_dim));
   a.carry[1] = a.carry[0] + p.carry / 4;
   return delta_chunks(a, d->key_dim, p.all, stream);
 }

@@ -11,11 +11,14 @@
 // keeping 16 columns of the state in registers: everything that a column of the
 // values meets belongs to that column alone.
 //
-// Numbers.  q, k and v are bf16 and go into the products as they are, the norms of q and k into
-// the rows' factors.  What is fp32 (states, T, the rows b V - .., u) enters a product in
-// parts of 8 bits, x = hi + mid + lo: three make a state's update as exact as fp32, two do for
-// what only outputs in bf16 see.  G is added up in 64 bits, because e^(G_i - G_j) has to
-// be exact also after a token that forgets everything.  Exponents are never above 0.
+// Numbers.  What an update of a state sees is as exact as fp32: values enter its products as two parts in half
+// precision, x = hi + lo, 22 bits; one part does for what only outputs in bf16 see.  Half precision has those bits but
+// little range, so every operand is scaled by a power of two that some factor in fp32 undoes: rows of K and Q (bf16, so
+// one part holds them) to lengths of 2^12, columns of the state and of b V - .. by their largest values, T and P, whose
+// values are at most 2 as long as b |k|^2 is, by 2^12.  (Three parts in bf16, which needs no scales, took twice the
+// products and twice the time.)  Keys and queries are taken as unit vectors and lengths, the lengths into the
+// factors of the rows.  G is added up in 64 bits, because e^(G_i - G_j) has to be exact also after a token that
+// forgets everything.  Exponents are never above 0.
 //
 // Not finite.  A product with T would carry a NaN of row j into rows above j, as 0 * NaN.  From
 // a chunk's first token on whose key or gates are not finite, rows are taken out of A and their
@@ -29,10 +32,12 @@ namespace {
 
 constexpr int kC = kChunk;
 constexpr uint32_t kLd = kC + 4;       // of T in LDS: four 16 x 16 blocks of the diagonal on different banks
-constexpr uint32_t kBlockBytes = 1024; // an operand of a matrix instruction: 16 bytes a lane
-constexpr uint32_t kBlocks = 6;        // of a 64 x 64 lower triangle, as (32-row block, half, 32-column block)
+constexpr uint32_t kBlocks = kTriangle / kOperand;   // (32-row block, half, 32-column block) of a lower triangle
+constexpr int kPair = 2;               // value heads of a workgroup of k_delta_chunk
 constexpr float kForget = -1000.f;     // logarithms of decays below this one are it: e^-1000 is 0
 
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
@@ -40,33 +45,41 @@ typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 // halves make the eight rows 8 c .. of a B operand.
 __device__ __forceinline__ uint32_t dealt(uint32_t u, uint32_t h, uint32_t m) { return 32 * u + 8 * (m >> 2) + 4 * h + (m & 3); }
 
-__device__ __forceinline__ bf16x8_t as_operand(u32x4_t w) { return __builtin_bit_cast(bf16x8_t, w); }
+__device__ __forceinline__ f16x8_t as_operand(u32x4_t w) { return __builtin_bit_cast(f16x8_t, w); }
 
-// Eight values as N parts of 8 bits: x = p[0] + p[1] + ..
+__device__ __forceinline__ f32x4_t product(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// Eight values, times s, as N parts in half precision: s x = p[0] + p[1]
 template <int N>
-__device__ __forceinline__ void split(const float (&x)[8], bf16x8_t (&p)[N]) {
-  float r[8];
+__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, float s, u32x4_t (&p)[N]) {
+  static_assert(N == 1 || N == 2, "two parts hold 22 bits");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = x[i];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    u32x4_t w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bf16x2_t b = {(__bf16)r[2 * i], (__bf16)r[2 * i + 1]};   // to nearest even
-      w[i] = __builtin_bit_cast(uint32_t, b);
-      if (k + 1 < N) {
-        r[2 * i] -= __uint_as_float(w[i] << 16);
-        r[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
-      }
+  for (int i = 0; i < 4; ++i) {
+    const float r0 = (i < 2 ? x[2 * i] : y[2 * i - 4]) * s, r1 = (i < 2 ? x[2 * i + 1] : y[2 * i - 3]) * s;
+    const f16x2_t hi = {(_Float16)r0, (_Float16)r1};
+    p[0][i] = __builtin_bit_cast(uint32_t, hi);
+    if constexpr (N > 1) {
+      const f16x2_t lo = {(_Float16)fmaf((float)hi[0], -1.f, r0), (_Float16)fmaf((float)hi[1], -1.f, r1)};
+      p[1][i] = __builtin_bit_cast(uint32_t, lo);
     }
-    p[k] = as_operand(w);
   }
 }
-template <int N>
-__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, bf16x8_t (&p)[N]) {
-  const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-  split(z, p);
+
+// 2^(to - e) for values below 2^(e + 1), and 2^(e - to); e is at least -107.
+struct Scale {
+  float up, down;
+};
+__device__ __forceinline__ Scale scale_to(float most, int to) {
+  const uint32_t e = max(__float_as_uint(most) >> 23 & 0xFFu, 20u);
+  return Scale{__uint_as_float((254u + to - e) << 23), __uint_as_float((e - to) << 23)};
+}
+
+// The largest of the four lanes that hold a column.
+__device__ __forceinline__ float column_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 // The sequence of a chunk's place: sequence s has those from starts[s] / 64 + s on.
@@ -82,28 +95,23 @@ __device__ __forceinline__ uint32_t seq_of_place(const Delta& a, uint32_t place,
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)lo);
 }
 
-// Place of a row's 16-byte piece in LDS, in k_delta_chunk (16 rows side by side are read together) ..
+// What a launch's place holds of a value head and of a key head.
+__device__ __forceinline__ uint8_t* item_of(const Delta& a, uint32_t local, uint32_t head) {
+  return a.ws + ((uint64_t)local * a.heads + head) * kItemBytes;
+}
+__device__ __forceinline__ uint8_t* key_item_of(const Delta& a, uint32_t local, uint32_t kh) {
+  return a.key_ws + ((uint64_t)local * (a.heads / a.group) + kh) * a.key_item;
+}
+
+// Place of a row's 16-byte piece in LDS: 16 neighbours that are read together, the rows of dealt(), and in the transposing
+// reads four neighbours fall on different banks.
 template <int DK>
 __device__ __forceinline__ uint32_t row_piece(uint32_t r, uint32_t p) {
   return r * (2 * DK) + 16 * (DK == 128 ? p ^ (r & 15) : p ^ ((r >> 1) & 7));
 }
-// .. and in k_delta_scan, where it is the rows of dealt(), and by the transposing reads four neighbours.
 template <int DK>
 __device__ __forceinline__ uint32_t dealt_piece(uint32_t r, uint32_t p) {
   return r * (2 * DK) + 16 * (DK == 128 ? p ^ ((r & 3) << 2 | ((r >> 3) & 3)) : p ^ (((r >> 1) & 1) << 2 | ((r >> 3) & 3)));
-}
-
-// Four elements of a 16 x 16 tile (row 4 c + i, column n) of the product of 16 rows each.
-template <int DK>
-__device__ __forceinline__ f32x4_t tile_product(const uint8_t* x, const uint8_t* y, uint32_t it, uint32_t jt, uint32_t n, uint32_t c) {
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int s = 0; s < DK / 32; ++s) {
-    const u32x4_t xa = *reinterpret_cast<const u32x4_t*>(x + row_piece<DK>(16 * it + n, 4 * s + c));
-    const u32x4_t yb = *reinterpret_cast<const u32x4_t*>(y + row_piece<DK>(16 * jt + n, 4 * s + c));
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(xa), as_operand(yb), acc, 0, 0, 0);
-  }
-  return acc;
 }
 
 // acc += X Y of 16 x 16 blocks of LDS in fp32.
@@ -122,37 +130,39 @@ __device__ __forceinline__ f32x4_t block_product(const float (*t)[kLd], uint32_t
   return acc;
 }
 
-// Eight values of a lower triangle in the order of operand block b.
-__device__ __forceinline__ void operand_values(const float (*t)[kLd], uint32_t b, uint32_t l, float (&x)[8]) {
-  const uint32_t u = b >> 1 > 0, s = b >> 1 > 1, row = dealt(u, b & 1, l & 15), col = 32 * s + 8 * (l >> 4);
+// Rows I .. 15 of the inverse of 1 + a, a 16 x 16 block whose rows the 16 lanes of a group hold: x is the lane's column.
+template <int I>
+__device__ __forceinline__ void invert_rows(const float (&a)[16], float (&x)[16], uint32_t n) {
+  if constexpr (I < 16) {
+    float y[2] = {I == n ? 1.f : 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(&t[row][col + 4 * i]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[4 * i + j] = w[j];
+    for (int j = 0; j < I; ++j) y[j & 1] = fmaf(-dpp<0x150 + I>(a[j]), x[j], y[j & 1]);   // lane I's, in every lane
+    x[I] = y[0] + y[1];
+    invert_rows<I + 1>(a, x, n);
   }
 }
 
+// T, P and the rows' factors of a chunk of up to two value heads that share a key head, and (the first of them) K and Q.
 template <int DK>
 __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
-  constexpr uint32_t kPieces = DK / 8, kRows = 256 / kPieces;
-  constexpr uint32_t kRaw = 2 * kC * DK * 2, kMat = kC * kLd * 4;
+  constexpr uint32_t kPieces = DK / 8, kRows = 256 / kPieces, U = DK / 32;
+  constexpr uint32_t kRaw = 2 * kC * DK * 2, kMat = kPair * kC * kLd * 4;
   __shared__ __attribute__((aligned(256))) uint8_t raw[kRaw > kMat ? kRaw : kMat];
-  __shared__ __attribute__((aligned(16))) float t[kC][kLd];
-  __shared__ double far[kC];
-  __shared__ float kk[kC], qq[kC], beta_sh[kC], rk_sh[kC], rq_sh[kC];
-  __shared__ uint32_t first_bad;
+  __shared__ double far[kPair][kC];
+  __shared__ float kk[kC], qq[kC], left[kPair][kC], unit_k[kC], unit_q[kC];
+  __shared__ uint32_t first_bad[kPair];
   uint8_t *ks = raw, *qs = raw + kRaw / 2;
-  float(*p)[kLd] = reinterpret_cast<float(*)[kLd]>(raw);
+  float(*t)[kC][kLd] = reinterpret_cast<float(*)[kC][kLd]>(raw);
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, c = lane >> 4;
-  const uint32_t h = blockIdx.x % a.heads, local = blockIdx.x / a.heads, place = a.place0 + local;
-  const uint32_t s = seq_of_place(a, place, lane);
+  const uint32_t pairs = (a.group + kPair - 1) / kPair, key_heads = a.heads / a.group;
+  const uint32_t pair = blockIdx.x % pairs, kh = blockIdx.x / pairs % key_heads, local = blockIdx.x / pairs / key_heads;
+  const uint32_t h0 = kh * a.group + kPair * pair, heads = min(a.group - kPair * pair, (uint32_t)kPair);
+  const uint32_t s = seq_of_place(a, a.place0 + local, lane);
   const Seq q = delta_seq(a, s);
-  const int32_t row0 = kC * (int32_t)(place - ((uint32_t)q.first / kC + s));   // of the sequence
+  const int32_t row0 = kC * (int32_t)(a.place0 + local - ((uint32_t)q.first / kC + s));   // of the sequence
   if (row0 < 0 || row0 >= q.rows) return;
   const int32_t count = min(q.rows - row0, kC);
   const uint64_t from = (uint64_t)(q.first + row0);
-  const uint32_t kh = h / a.group;
 
   u32x4_t kr[kC / kRows], qr[kC / kRows];
 #pragma unroll
@@ -163,9 +173,9 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     qr[i] = *reinterpret_cast<const u32x4_t*>(a.q + at * a.ldq + kh * DK + 8 * (tid % kPieces));
   }
   float beta = 0.f;
-  if (wave == 0) {
+  if (wave < heads) {
     const bool there = (int32_t)lane < count;
-    const Gates g = gates_of(a, from + min((int32_t)lane, count - 1), h);
+    const Gates g = gates_of(a, from + min((int32_t)lane, count - 1), h0 + wave);
     beta = there ? g.beta : 0.f;
     double x = !there ? 0.0 : g.log_alpha < kForget ? (double)kForget : (double)g.log_alpha;
 #pragma unroll
@@ -173,19 +183,26 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       const double y = __shfl_up(x, d);
       if (lane >= (uint32_t)d) x += y;
     }
-    far[lane] = x;
+    far[wave][lane] = x;
   }
+  uint8_t* key_item = key_item_of(a, local, kh);
 #pragma unroll
   for (int i = 0; i < (int)(kC / kRows); ++i) {
     const uint32_t r = tid / kPieces + i * kRows, piece = tid % kPieces;
     if ((int32_t)r >= count) kr[i] = qr[i] = u32x4_t{0, 0, 0, 0};
+    f32x4_t k4[2], q4[2];
     float x = 0.f, y = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float k0 = __uint_as_float(kr[i][j] << 16), k1 = __uint_as_float(kr[i][j] & 0xFFFF0000u);
-      const float q0 = __uint_as_float(qr[i][j] << 16), q1 = __uint_as_float(qr[i][j] & 0xFFFF0000u);
-      x = fmaf(k1, k1, fmaf(k0, k0, x));
-      y = fmaf(q1, q1, fmaf(q0, q0, y));
+      k4[j / 2][2 * (j % 2)] = __uint_as_float(kr[i][j] << 16);
+      k4[j / 2][2 * (j % 2) + 1] = __uint_as_float(kr[i][j] & 0xFFFF0000u);
+      q4[j / 2][2 * (j % 2)] = __uint_as_float(qr[i][j] << 16);
+      q4[j / 2][2 * (j % 2) + 1] = __uint_as_float(qr[i][j] & 0xFFFF0000u);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x = fmaf(k4[j / 4][j % 4], k4[j / 4][j % 4], x);
+      y = fmaf(q4[j / 4][j % 4], q4[j / 4][j % 4], y);
     }
 #pragma unroll
     for (int d = 1; d < (int)kPieces; d *= 2) {
@@ -196,126 +213,166 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       kk[r] = x;
       qq[r] = y;
     }
-    *reinterpret_cast<u32x4_t*>(ks + row_piece<DK>(r, piece)) = kr[i];
-    *reinterpret_cast<u32x4_t*>(qs + row_piece<DK>(r, piece)) = qr[i];
+    u32x4_t kw[1], qw[1];
+    split(k4[0], k4[1], scale_to(sqrtf(x), 12).up, kw);
+    split(q4[0], q4[1], scale_to(sqrtf(y), 12).up, qw);
+    *reinterpret_cast<u32x4_t*>(ks + row_piece<DK>(r, piece)) = kw[0];
+    *reinterpret_cast<u32x4_t*>(qs + row_piece<DK>(r, piece)) = qw[0];
+    if (pair == 0) {
+      *reinterpret_cast<u32x4_t*>(key_item + r * (2 * DK) + 16 * piece) = kw[0];
+      // operand (tile of dealt rows, 32 columns), lane (row, eight columns)
+      const uint32_t tile = 2 * (r >> 5) + ((r >> 2) & 1), m = (r >> 3 & 3) * 4 + (r & 3);
+      *reinterpret_cast<u32x4_t*>(key_item + kC * 2 * DK + (tile * U + piece / 4) * kOperand + 16 * (16 * (piece % 4) + m)) = qw[0];
+    }
   }
   __syncthreads();
 
-  // the ten tiles of the lower triangle, of A and of P
-  uint8_t* item = a.ws + (uint64_t)(local * a.heads + h) * kItemBytes;
-  f32x4_t ak[3], pk[3];
+  // The ten 16 x 16 tiles of A's lower triangle by rows; P's six operands: transposed tiles of K Q^T with dealt rows, whose
+  // results are what a lane of the operand holds.  Wavefronts 0 and 1 take two tiles and two operands, the others three and one.
+  const uint32_t tiles = wave < 2 ? 2 : 3, ops = wave < 2 ? 2 : 1;
+  const uint32_t tile0 = wave < 2 ? 2 * wave : 3 * wave - 2, op0 = wave < 2 ? 2 * wave : wave + 2;
+  f32x4_t ak[3], pk[2][2];
 #pragma unroll
   for (int x = 0; x < 3; ++x) {
-    const uint32_t tile = wave + 4 * x, it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
-    if (tile >= 10) continue;
-    ak[x] = tile_product<DK>(ks, ks, it, jt, n, c);
-    pk[x] = tile_product<DK>(qs, ks, it, jt, n, c);
+    const uint32_t tile = min(tile0 + x, 9u), it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
+    ak[x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (x < (int)tiles)
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u)
+        ak[x] = product(as_operand(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(16 * it + n, 4 * u + c))),
+                        as_operand(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(16 * jt + n, 4 * u + c))), ak[x]);
   }
-  if (wave == 0) {
-    const double g = far[lane], end = far[kC - 1];
-    const bool there = (int32_t)lane < count;
-    const float kn = kk[lane], rk = there ? unit(a, kn) : 0.f, rq = there ? unit(a, qq[lane]) * a.scale : 0.f;
-    const bool bad = !(fabsf(kn) < INFINITY) || !(fabsf(beta) < INFINITY) || g != g;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t b = min(op0 + x, 5u), w = b > 1, sb = b > 3, hf = b & 1;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      pk[x][z] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (x < (int)ops)
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u)
+          pk[x][z] = product(as_operand(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(dealt(sb, z, n), 4 * u + c))),
+                             as_operand(*reinterpret_cast<const u32x4_t*>(qs + row_piece<DK>(dealt(w, hf, n), 4 * u + c))), pk[x][z]);
+    }
+  }
+  if (wave < heads) {
+    const double g = far[wave][lane], end = far[wave][kC - 1];
+    // keys are unit vectors times lengths: K holds k 2^e, that is unit vectors times 1 / uk
+    const float k2 = kk[lane], q2 = qq[lane], kn = sqrtf(k2), qn = sqrtf(q2);
+    const Scale ek = scale_to(kn, 12), eq = scale_to(qn, 12);
+    const float uk = kn > 0.f ? ek.down / kn : 0.f, uq = qn > 0.f ? eq.down / qn : 0.f;
+    const float to_k = unit(a, k2), to_q = unit(a, q2);
+    const bool bad = !(fabsf(k2) < INFINITY) || !(fabsf(beta) < INFINITY) || g != g;
     const uint64_t any = __ballot(bad);
     const uint32_t f = any ? (uint32_t)__builtin_ctzll(any) : (uint32_t)kC;
     const float lost = lane >= f ? NAN : 0.f, gone = any ? NAN : 0.f;
-    const float decay = expf((float)g);
-    float* vec = reinterpret_cast<float*>(item + kVecAt);
-    vec[lane] = beta + lost;
-    vec[kC + lane] = beta * decay * rk + lost;
-    vec[2 * kC + lane] = expf((float)(end - g)) * rk + gone;
-    vec[3 * kC + lane] = decay * rq + lost;
+    const float decay = expf((float)g), len = kn * to_k;
+    float* vec = reinterpret_cast<float*>(item_of(a, local, h0 + wave) + kVecAt);
+    vec[lane] = beta * len + lost;
+    vec[kC + lane] = beta * len * len * decay * uk + lost;
+    vec[2 * kC + lane] = expf((float)(end - g)) * (uk * 4096.f) + gone;
+    vec[3 * kC + lane] = decay * uq;
+    vec[4 * kC + lane] = qn * to_q * a.scale;
     if (lane == 0) {
-      vec[4 * kC] = expf((float)end) + gone;
-      first_bad = f;
+      vec[5 * kC] = expf((float)end) + gone;
+      first_bad[wave] = f;
     }
-    beta_sh[lane] = beta;
-    rk_sh[lane] = rk;
-    rq_sh[lane] = rq;
-  }
-  __syncthreads();   // K and Q are read: P goes to their place
-#pragma unroll
-  for (int x = 0; x < 3; ++x) {
-    const uint32_t tile = wave + 4 * x, it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
-    if (tile >= 10) continue;
-    const uint32_t col = 16 * jt + n;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t row = 16 * it + 4 * c + i;
-      const float e = expf((float)(far[row] - far[col])) * rk_sh[col];
-      t[row][col] = col < row && row < first_bad ? beta_sh[row] * rk_sh[row] * e * ak[x][i] : 0.f;
-      p[row][col] = col <= row ? rq_sh[row] * e * pk[x][i] : 0.f;
+    left[wave][lane] = beta * len * len * uk;
+    if (wave == 0) {
+      unit_k[lane] = uk;
+      unit_q[lane] = uq;
     }
   }
-  if (wave >= 2) {   // tiles (0, 1) and (2, 3): nothing
-    const uint32_t row = 32 * (wave - 2) + n, col = 32 * (wave - 2) + 16 + 4 * c;
-    *reinterpret_cast<f32x4_t*>(&t[row][col]) = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    *reinterpret_cast<f32x4_t*>(&p[row][col]) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();   // K and Q are read: A goes to their place
+  for (uint32_t b = 0; b < heads; ++b) {
+    const double* g = far[b];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      const uint32_t tile = tile0 + x, it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
+      if (x >= (int)tiles) continue;
+      const uint32_t col = 16 * jt + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t row = 16 * it + 4 * c + i;
+        const bool in = col < row && row < first_bad[b];
+        t[b][row][col] = in ? left[b][row] * unit_k[col] * expf((float)(g[row] - g[col])) * ak[x][i] : 0.f;
+      }
+    }
+    if (wave >= 2) {   // tiles (0, 1) and (2, 3): nothing
+      const uint32_t row = 32 * (wave - 2) + n, col = 32 * (wave - 2) + 16 + 4 * c;
+      *reinterpret_cast<f32x4_t*>(&t[b][row][col]) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t o = op0 + x, w = o > 1, sb = o > 3, hf = o & 1, row = dealt(w, hf, n);
+      if (x >= (int)ops) continue;
+      f32x4_t y[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t col = 32 * sb + 8 * c + 4 * z + i;
+          y[z][i] = col <= row ? unit_q[row] * unit_k[col] * expf((float)(g[row] - g[col])) * pk[x][z][i] : 0.f;
+        }
+      u32x4_t p[1];
+      split(y[0], y[1], 4096.f, p);
+      *reinterpret_cast<u32x4_t*>(item_of(a, local, h0 + b) + kPAt + o * kOperand + 16 * lane) = p[0];
+    }
   }
   __syncthreads();
 
-  if (wave == 0) {
-    // the inverses of the four blocks of the diagonal, a column a lane, row after row
-    float x[16];
+  if (wave < heads) {   // the inverses of the four blocks of the diagonal
+    float(*tb)[kLd] = t[wave];
+    float x[16], d[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float y[2] = {i == (int)n ? 1.f : 0.f, 0.f};
+    for (int i = 0; i < 4; ++i) {
+      const f32x4_t w = *reinterpret_cast<const f32x4_t*>(&tb[16 * c + n][16 * c + 4 * i]);
 #pragma unroll
-      for (int j = 0; j < i; j += 4) {
-        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(&t[16 * c + i][16 * c + j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < i) y[e & 1] = fmaf(-w[e], x[j + e], y[e & 1]);
-      }
-      x[i] = y[0] + y[1];
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = w[j];
     }
+    invert_rows<0>(d, x, n);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[16 * c + i][16 * c + n] = x[i];
-  } else {
-    for (uint32_t i = tid - 64; i < kBlocks * 64; i += 192) {
-      float x[8];
-      bf16x8_t w[kPParts];
-      operand_values(p, i >> 6, i & 63, x);
-      split(x, w);
-#pragma unroll
-      for (int k = 0; k < kPParts; ++k)
-        *reinterpret_cast<bf16x8_t*>(item + kPAt + k * (kBlocks * kBlockBytes) + 16 * i) = w[k];
-    }
+    for (int i = 0; i < 16; ++i) tb[16 * c + i][16 * c + n] = x[i];
   }
   __syncthreads();
+  // two wavefronts a head: blocks (1, 0) and (3, 2), then the columns of the lower left 32 x 32
+  const uint32_t hb = wave >> 1, half = wave & 1;
+  float(*tb)[kLd] = t[hb];
+  const bool mine = hb < heads;
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-  if (wave < 2) {   // blocks (1, 0) and (3, 2)
-    const uint32_t r = 2 * wave + 1, b = 2 * wave;
-    const f32x4_t y = block_product(t, r, b, b, b, n, c, zero), z = block_product(t, r, r, y, n, c, zero);
+  if (mine) {
+    const uint32_t r = 2 * half + 1, b = 2 * half;
+    const f32x4_t y = block_product(tb, r, b, b, b, n, c, zero), z = block_product(tb, r, r, y, n, c, zero);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[16 * r + 4 * c + i][16 * b + n] = -z[i];
+    for (int i = 0; i < 4; ++i) tb[16 * r + 4 * c + i][16 * b + n] = -z[i];
   }
   __syncthreads();
   f32x4_t lower[2];
-  if (wave < 2) {   // column `wave` of the lower left 32 x 32
+  if (mine) {
     f32x4_t y[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      y[i] = wave == 0 ? block_product(t, 2 + i, 0, 0, 0, n, c, zero) : zero;
-      y[i] = block_product(t, 2 + i, 1, 1, wave, n, c, y[i]);
+      y[i] = half == 0 ? block_product(tb, 2 + i, 0, 0, 0, n, c, zero) : zero;
+      y[i] = block_product(tb, 2 + i, 1, 1, half, n, c, y[i]);
     }
-    lower[0] = block_product(t, 2, 2, y[0], n, c, zero);
-    lower[1] = block_product(t, 3, 3, y[1], n, c, block_product(t, 3, 2, y[0], n, c, zero));
+    lower[0] = block_product(tb, 2, 2, y[0], n, c, zero);
+    lower[1] = block_product(tb, 3, 3, y[1], n, c, block_product(tb, 3, 2, y[0], n, c, zero));
   }
   __syncthreads();
-  if (wave < 2)
+  if (mine)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[16 * (2 + k) + 4 * c + i][16 * wave + n] = -lower[k][i];
+      for (int i = 0; i < 4; ++i) tb[16 * (2 + k) + 4 * c + i][16 * half + n] = -lower[k][i];
   __syncthreads();
-  for (uint32_t i = tid; i < kBlocks * 64; i += 256) {
-    float x[8];
-    bf16x8_t w[kTParts];
-    operand_values(t, i >> 6, i & 63, x);
-    split(x, w);
-#pragma unroll
-    for (int k = 0; k < kTParts; ++k) *reinterpret_cast<bf16x8_t*>(item + k * (kBlocks * kBlockBytes) + 16 * i) = w[k];
+  for (uint32_t i = tid; i < heads * kBlocks * 64; i += 256) {
+    const uint32_t b = i / (kBlocks * 64), e = i - b * (kBlocks * 64), o = e >> 6, l = e & 63;
+    const uint32_t row = dealt(o > 1, o & 1, l & 15), col = 32 * (o > 3) + 8 * (l >> 4);
+    u32x4_t w[2];
+    split(*reinterpret_cast<const f32x4_t*>(&t[b][row][col]), *reinterpret_cast<const f32x4_t*>(&t[b][row][col + 4]), 4096.f, w);
+    uint8_t* item = item_of(a, local, h0 + b);
+    *reinterpret_cast<u32x4_t*>(item + 16 * e) = w[0];
+    *reinterpret_cast<u32x4_t*>(item + kTriangle + 16 * e) = w[1];
   }
 }
 
@@ -328,7 +385,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, 
 
 // Two wavefronts share 16 columns, each on a SIMD of its own: the first takes the states from chunk to chunk, which is
 // what a sequence waits for, the second, a chunk behind, makes the outputs from the states and rows that the first leaves in
-// LDS as operands, and brings the next K.  (One wavefront for both: 559 us instead of @@ us for a prompt of 8192 tokens.)
+// LDS as operands, and brings the next K.  (One wavefront for both took a quarter longer.)
 template <int DK>
 struct Scan {
   static constexpr int U = DK / 32;                       // 32-row blocks of the state
@@ -336,9 +393,10 @@ struct Scan {
   static constexpr int kPasses = kC / (int)kRows;
   struct Shared {
     __attribute__((aligned(256))) uint8_t k[2][kC * DK * 2];
-    u32x4_t parts[2][kScanGroups][U][2][64];              // of the states before a chunk
-    f32x4_t u[2][kScanGroups][2][2][64];
+    u32x4_t state[2][kScanGroups][U][64];                 // before a chunk, scaled
+    u32x4_t u[2][kScanGroups][2][64];
     __attribute__((aligned(16))) float vec[2][4 * kC];
+    float down[2][kScanGroups][2][16];                    // what undoes the columns' scales of both
     int32_t bad[2][kScanGroups][16];                      // the first of a column's rows that is not finite
   };
   const Delta& a;
@@ -347,9 +405,8 @@ struct Scan {
   const uint32_t base, h, kh, col, lane, n, c, group;
   const int32_t j0, j1;
 
-  __device__ __forceinline__ const uint8_t* item_of(int32_t j) const {
-    return a.ws + ((uint64_t)(base + (uint32_t)j - a.place0) * a.heads + h) * kItemBytes;
-  }
+  __device__ __forceinline__ uint32_t local(int32_t j) const { return base + (uint32_t)j - a.place0; }
+  __device__ __forceinline__ const uint8_t* item(int32_t j) const { return item_of(a, local(j), h); }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint16_t* p, uint64_t ld, int32_t j, uint32_t at, uint32_t width) const {
     return chunk_rows(p + (uint64_t)(q.first + j * kC) * ld + at, ld, min(q.rows - j * kC, kC), width);
   }
@@ -368,13 +425,13 @@ struct Scan {
     // Lanes' places in K: of rows dealt(0, 0, n), and for the transposing reads; a 32-column block further is an exclusive
     // or with 64 bytes, and rows 4 hf and 32 w further change no bits that the pieces' exchange looks at.
     const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c), tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3);
-    u32x4_t tw[kTParts][kBlocks];
+    u32x4_t tw[2][kBlocks];
     uint16_t v[2][2][4];
     const auto load_t = [&](int32_t j) {
 #pragma unroll
-      for (int e = 0; e < kTParts; ++e)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + (e * kBlocks + i) * kBlockBytes + 16 * lane);
+        for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item(j) + e * kTriangle + i * kOperand + 16 * lane);
     };
     const auto load_v = [&](int32_t j) {
       const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
@@ -390,104 +447,111 @@ struct Scan {
     lds_barrier();
     for (int32_t j = j0; j < j1; ++j) {
       const float decay = *reinterpret_cast<const __attribute__((address_space(4))) float*>(
-          reinterpret_cast<uintptr_t>(item_of(j) + kVecAt + 16 * kC));
+          reinterpret_cast<uintptr_t>(item(j) + kVecAt + 4 * 5 * kC));
       const uint8_t* k = sh.k[j & 1];
       const float* vec = sh.vec[j & 1];
       const int32_t next = min(j + 1, j1 - 1);
       // the state in parts, and K S
+      float most = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(st[u][0][i]), fabsf(st[u][1][i])));
+      const Scale ss = scale_to(column_max(most), 12);
       f32x4_t ks[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) ks[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        bf16x8_t part[3], kw[4];
-        split(st[u][0], st[u][1], part);
+        u32x4_t part[2], kw[4];
+        split(st[u][0], st[u][1], ss.up, part);
+        sh.state[j & 1][group][u][lane] = part[0];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sh.parts[j & 1][group][u][e][lane] = __builtin_bit_cast(u32x4_t, part[e]);
+        for (int t = 0; t < 4; ++t) kw[t] = *reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          kw[t] = as_operand(*reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK));
+        for (int e = 1; e >= 0; --e)
 #pragma unroll
-        for (int e = 2; e >= 0; --e)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) ks[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kw[t], part[e], ks[t], 0, 0, 0);
+          for (int t = 0; t < 4; ++t) ks[t] = product(as_operand(kw[t]), as_operand(part[e]), ks[t]);
       }
       // the rows b V - b e^G K S0
-      f32x4_t rows[2][2];
+      f32x4_t rows[4];
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t r = 16 * (t & 2) + 8 * c + 4 * (t & 1);
+        const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t r = 32 * w + 8 * c + 4 * hf;
-          const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) rows[w][hf][i] = fmaf(-c2[i], ks[2 * w + hf][i], c1[i] * bf16_value(v[w][hf][i]));
-        }
+        for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[i] * ss.down, ks[t][i], c1[i] * bf16_value(v[t / 2][t % 2][i]));
+      }
       load_v(next);
-      f32x4_t u[2][2];
+      f32x4_t u[4];   // times 2^12 and the rows' scale
+      Scale rs;
       const auto solve = [&] {
-        bf16x8_t part[2][3];
+        float top = 0.f;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) split(rows[w][0], rows[w][1], part[w]);
+        for (int t = 0; t < 4; t += 2)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) u[t / 2][t % 2] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(rows[t][i]), fabsf(rows[t + 1][i])));
+        rs = scale_to(column_max(top), 6);   // u is at most 2^7 times the largest row
+        u32x4_t part[2][2];
 #pragma unroll
-        for (int e = 2; e >= 0; --e)   // parts whose product is 2^-16, 2^-8 and 1 of the whole
+        for (int w = 0; w < 2; ++w) split(rows[2 * w], rows[2 * w + 1], rs.up, part[w]);
 #pragma unroll
-          for (int f = 0; f <= e; ++f)
+        for (int t = 0; t < 4; ++t) u[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int b = 0; b < (int)kBlocks; ++b) {
-              const int w = b > 1, sb = b > 3, hf = b & 1;
-              u[w][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(tw[f][b]), part[sb][e - f], u[w][hf], 0, 0, 0);
-            }
+        for (int e = 2; e >= 0; --e)   // lo hi, hi lo, hi hi
+#pragma unroll
+          for (int b = 0; b < (int)kBlocks; ++b) {
+            const int t = 2 * (b > 1) + (b & 1), sb = b > 3;
+            u[t] = product(as_operand(tw[e == 2][b]), as_operand(part[sb][e == 1]), u[t]);
+          }
       };
       solve();
       int32_t bad = kC;
-      if (__any(!(fabsf(u[0][0][0]) < INFINITY) || !(fabsf(u[1][0][0]) < INFINITY))) {
+      if (__any(!(fabsf(u[0][0]) < INFINITY) || !(fabsf(u[2][0]) < INFINITY))) {
 #pragma unroll
-        for (int w = 1; w >= 0; --w)
+        for (int t = 3; t >= 0; --t)
 #pragma unroll
-          for (int hf = 1; hf >= 0; --hf)
-#pragma unroll
-            for (int i = 3; i >= 0; --i)
-              if (!(fabsf(rows[w][hf][i]) < INFINITY)) {
-                bad = 32 * w + 8 * (int32_t)c + 4 * hf + i;
-                rows[w][hf][i] = 0.f;
-              }
+          for (int i = 3; i >= 0; --i)
+            if (!(fabsf(rows[t][i]) < INFINITY)) {
+              bad = 16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i;
+              rows[t][i] = 0.f;
+            }
         bad = min(bad, __shfl_xor(bad, 16));
         bad = min(bad, __shfl_xor(bad, 32));
         solve();
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (32 * w + 8 * (int32_t)c + 4 * hf + i >= bad) u[w][hf][i] = 0.f;
+          for (int i = 0; i < 4; ++i)
+            if (16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i >= bad) u[t][i] = 0.f;
       }
       load_t(next);
-      if (c == 0) sh.bad[j & 1][group][n] = bad;
+      if (c == 0) {
+        sh.bad[j & 1][group][n] = bad;
+        sh.down[j & 1][group][0][n] = ss.down;
+        sh.down[j & 1][group][1][n] = rs.down * 0x1p-12f;
+      }
       // S = decay S + K^T diag(e^(G_end - G)) u
-      bf16x8_t up[2][3];
+      u32x4_t up[2][2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         f32x4_t y[2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          sh.u[j & 1][group][w][hf][lane] = u[w][hf];
-          y[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf) * u[w][hf];
-        }
-        split(y[0], y[1], up[w]);
+        for (int hf = 0; hf < 2; ++hf) y[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf) * u[2 * w + hf];
+        split(y[0], y[1], 0x1p-12f, up[w]);
+        u32x4_t one[1];
+        split(u[2 * w], u[2 * w + 1], 0x1p-12f, one);
+        sh.u[j & 1][group][w][lane] = one[0];
       }
+      const float back = rs.down * 0x1p-12f;
 #pragma unroll
-      for (int ub = 0; ub < U; ++ub)
+      for (int ub = 0; ub < U; ub += 2) {
+        f32x4_t add[4];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) st[ub][hf] *= decay;
+        for (int t = 0; t < 4; ++t) add[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int ub = 0; ub < U; ub += 2) {
-          union { s16x4_t half[2]; bf16x8_t all; } kt[4];   // four tokens of the lane's row of K^T each
+        for (int w = 0; w < 2; ++w) {
+          union { s16x4_t half[2]; u32x4_t all; } kt[4];   // four tokens of the lane's row of K^T each
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -495,11 +559,15 @@ struct Scan {
               kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                   (lds_s16x4_t*)(k + (tat ^ 64 * (ub + t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
 #pragma unroll
-          for (int e = 2; e >= 0; --e)
+          for (int e = 1; e >= 0; --e)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              st[ub + t / 2][t % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kt[t].all, up[w][e], st[ub + t / 2][t % 2], 0, 0, 0);
+            for (int t = 0; t < 4; ++t) add[t] = product(as_operand(kt[t].all), as_operand(up[w][e]), add[t]);
         }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st[ub + t / 2][t % 2][i] = fmaf(add[t][i], back, decay * st[ub + t / 2][t % 2][i]);
+      }
       if (__any(bad < kC)) {
 #pragma unroll
         for (int ub = 0; ub < U; ++ub)
@@ -521,16 +589,14 @@ struct Scan {
 
   // The second wavefront: K of the chunk after, and the outputs of the chunk before, O = diag(e^G) Q S0 + P u.
   __device__ __forceinline__ void outputs() {
-    const uint32_t dv = a.value_dim, ldq = (uint32_t)a.ldq, ldk = (uint32_t)a.ldk, ldo = (uint32_t)a.ldo, tid = 64 * group + lane;
-    const uint32_t klane = 2 * (tid / kPieces * ldk + 8 * (tid % kPieces)), olane = 2 * (8 * c * ldo + col), qlane = 2 * (dealt(0, 0, n) * ldq + 8 * c);
-    u32x4_t kr[kPasses], pw[kPParts][kBlocks], qw[4][U];
-    f32x4_t c4[4];
+    const uint32_t dv = a.value_dim, ldo = (uint32_t)a.ldo, tid = 64 * group + lane, olane = 2 * (8 * c * ldo + col);
+    u32x4_t kr[kPasses], pw[kBlocks], qw[4][U];
+    f32x4_t c4[4], c6[4];
     float2 vr;
     const auto load_k = [&](int32_t j) {
-      const __amdgpu_buffer_rsrc_t r = rows_of(a.k, a.ldk, j, kh * DK, DK);
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) kr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, klane + i * kRows * 2 * ldk, 0, 0);
-      vr = *reinterpret_cast<const float2*>(item_of(j) + kVecAt + 8 * tid);
+      for (int i = 0; i < kPasses; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(j), kh) + 16 * (tid + i * 64 * kScanGroups));
+      vr = *reinterpret_cast<const float2*>(item(j) + kVecAt + 8 * tid);
     };
     const auto store_k = [&](int b) {
 #pragma unroll
@@ -539,20 +605,21 @@ struct Scan {
       *reinterpret_cast<float2*>(&sh.vec[b][2 * tid]) = vr;
     };
     const auto load_q = [&](int32_t j) {
-      const __amdgpu_buffer_rsrc_t r = rows_of(a.q, a.ldq, j, kh * DK, DK);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int u = 0; u < U; ++u) qw[t][u] = __builtin_amdgcn_raw_buffer_load_b128(r, qlane + (16 * (t & 2) + 4 * (t & 1)) * 2 * ldq + 64 * u, 0, 0);
-        c4[t] = *reinterpret_cast<const f32x4_t*>(item_of(j) + kVecAt + 4 * (3 * kC + 16 * (t & 2) + 8 * c + 4 * (t & 1)));
-      }
+        for (int u = 0; u < U; ++u)
+          qw[t][u] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(j), kh) + kC * 2 * DK + (t * U + u) * kOperand + 16 * lane);
     };
     const auto load_p = [&](int32_t j) {
 #pragma unroll
-      for (int e = 0; e < kPParts; ++e)
+      for (int i = 0; i < (int)kBlocks; ++i) pw[i] = *reinterpret_cast<const u32x4_t*>(item(j) + kPAt + i * kOperand + 16 * lane);
 #pragma unroll
-        for (int i = 0; i < (int)kBlocks; ++i)
-          pw[e][i] = *reinterpret_cast<const u32x4_t*>(item_of(j) + kPAt + (e * kBlocks + i) * kBlockBytes + 16 * lane);
+      for (int t = 0; t < 4; ++t) {
+        const uint8_t* p = item(j) + kVecAt + 4 * (3 * kC + 16 * (t & 2) + 8 * c + 4 * (t & 1));
+        c4[t] = *reinterpret_cast<const f32x4_t*>(p);
+        c6[t] = *reinterpret_cast<const f32x4_t*>(p + 4 * kC);
+      }
     };
     load_k(j0);
     store_k(j0 & 1);
@@ -565,35 +632,24 @@ struct Scan {
     lds_barrier();
     for (int32_t j = j0; j < j1; ++j) {
       // the states' wavefront is at chunk j + 1, whose K is there
-      f32x4_t o[4];
+      f32x4_t o[4], p[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < 4; ++t) o[t] = p[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       store_k(j & 1);   // of chunk j + 2: all are done with chunk j's
       load_k(min(j + 3, j1 - 1));
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        const f16x8_t part = as_operand(sh.state[j & 1][group][u][lane]);
 #pragma unroll
-        for (int e = 1; e >= 0; --e) {
-          const bf16x8_t part = as_operand(sh.parts[j & 1][group][u][e][lane]);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(qw[t][u]), part, o[t], 0, 0, 0);
-        }
-      bf16x8_t part[2][2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) split(sh.u[j & 1][group][w][0][lane], sh.u[j & 1][group][w][1][lane], part[w]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) o[t] *= c4[t];
+        for (int t = 0; t < 4; ++t) o[t] = product(as_operand(qw[t][u]), part, o[t]);
+      }
       load_q(min(j + 1, j1 - 1));
 #pragma unroll
-      for (int e = 1; e >= 0; --e)
-#pragma unroll
-        for (int f = 0; f <= e; ++f)
-#pragma unroll
-          for (int i = 0; i < (int)kBlocks; ++i) {
-            const int t = 2 * (i > 1) + (i & 1);
-            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_operand(pw[f][i]), part[i > 3][e - f], o[t], 0, 0, 0);
-          }
-      load_p(min(j + 1, j1 - 1));
+      for (int i = 0; i < (int)kBlocks; ++i) {
+        const int t = 2 * (i > 1) + (i & 1);
+        p[t] = product(as_operand(pw[i]), as_operand(sh.u[j & 1][group][i > 3][lane]), p[t]);
+      }
+      const float ds = sh.down[j & 1][group][0][n], du = sh.down[j & 1][group][1][n];
       const int32_t bad = sh.bad[j & 1][group][n];
       const __amdgpu_buffer_rsrc_t r = rows_of(a.out, a.ldo, j, h * dv, dv);
 #pragma unroll
@@ -601,9 +657,11 @@ struct Scan {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t row = 16 * (t & 2) + 4 * (t & 1) + i;
-          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)((int32_t)(row + 8 * c) >= bad ? NAN : o[t][i])), r,
+          const float y = c6[t][i] * fmaf(c4[t][i] * ds, o[t][i], du * p[t][i]);
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)((int32_t)(row + 8 * c) >= bad ? NAN : y)), r,
                                                 olane + row * 2 * ldo, 0, 0);
         }
+      load_p(min(j + 1, j1 - 1));
       if (j + 1 < j1) lds_barrier();   // (the other wavefronts have met here once less)
     }
   }
@@ -639,7 +697,7 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
     a.place0 = first;
     a.carry[0] = carry[i % 2];
     a.carry[1] = carry[(i + 1) % 2];
-    const uint64_t items = (uint64_t)(all - first < a.places ? all - first : a.places) * a.heads;
+    const uint64_t items = (uint64_t)(all - first < a.places ? all - first : a.places) * (a.heads / a.group) * ((a.group + kPair - 1) / kPair);
     const uint64_t blocks = ((uint64_t)a.n_seqs * a.heads + 7) / 8 * 8 * a.slices;
     if (items > 0x7FFFFFFFull || blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
     hipLaunchKernelGGL((k_delta_chunk<DK>), dim3((uint32_t)items), dim3(256), 0, s, a);
