@@ -49,20 +49,28 @@ __device__ __forceinline__ f16x8_t as_operand(u32x4_t w) { return __builtin_bit_
 
 __device__ __forceinline__ f32x4_t product(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// Eight values, times s, as N parts in half precision: s x = p[0] + p[1]
+// Eight values, times s, as N parts in half precision: s x = p[0] + p[1], each part one rounding.
 template <int N>
-__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, float s, u32x4_t (&p)[N]) {
+__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, f32x4_t sx, f32x4_t sy, u32x4_t (&p)[N]) {
   static_assert(N == 1 || N == 2, "two parts hold 22 bits");
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float r0 = (i < 2 ? x[2 * i] : y[2 * i - 4]) * s, r1 = (i < 2 ? x[2 * i + 1] : y[2 * i - 3]) * s;
-    const f16x2_t hi = {(_Float16)r0, (_Float16)r1};
-    p[0][i] = __builtin_bit_cast(uint32_t, hi);
+    const float r0 = i < 2 ? x[2 * i] : y[2 * i - 4], r1 = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+    const float s0 = i < 2 ? sx[2 * i] : sy[2 * i - 4], s1 = i < 2 ? sx[2 * i + 1] : sy[2 * i - 3];
+    uint32_t w = __builtin_bit_cast(uint32_t, (f16x2_t{(_Float16)(r0 * s0), (_Float16)(r1 * s1)}));
+    if constexpr (N > 1) asm("" : "+v"(w));   // one value: what lo completes is what was stored, however it was rounded
+    p[0][i] = w;
     if constexpr (N > 1) {
-      const f16x2_t lo = {(_Float16)fmaf((float)hi[0], -1.f, r0), (_Float16)fmaf((float)hi[1], -1.f, r1)};
+      const f16x2_t hi = __builtin_bit_cast(f16x2_t, w);
+      const f16x2_t lo = {(_Float16)fmaf(r0, s0, -(float)hi[0]), (_Float16)fmaf(r1, s1, -(float)hi[1])};
       p[1][i] = __builtin_bit_cast(uint32_t, lo);
     }
   }
+}
+template <int N>
+__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, float s, u32x4_t (&p)[N]) {
+  const f32x4_t t = {s, s, s, s};
+  split(x, y, t, t, p);
 }
 
 // 2^(to - e) for values below 2^(e + 1), and 2^(e - to); e is at least -107.
@@ -74,6 +82,16 @@ __device__ __forceinline__ Scale scale_to(float most, int to) {
   return Scale{__uint_as_float((254u + to - e) << 23), __uint_as_float((e - to) << 23)};
 }
 
+// The largest magnitude of x and eight values; a NaN is passed over.  (Written out: fmaxf() would make each value a
+// number first.)
+__device__ __forceinline__ float largest(float x, f32x4_t y, f32x4_t z) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(x) : "v"(y[i]), "v"(y[i + 1]));
+    asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(x) : "v"(z[i]), "v"(z[i + 1]));
+  }
+  return x;
+}
 // The largest of the four lanes that hold a column.
 __device__ __forceinline__ float column_max(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -270,7 +288,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     float* vec = reinterpret_cast<float*>(item_of(a, local, h0 + wave) + kVecAt);
     vec[lane] = beta * len + lost;
     vec[kC + lane] = beta * len * len * decay * uk + lost;
-    vec[2 * kC + lane] = expf((float)(end - g)) * (uk * 4096.f) + gone;
+    vec[2 * kC + lane] = expf((float)(end - g)) * uk + gone;
     vec[3 * kC + lane] = decay * uq;
     vec[4 * kC + lane] = qn * to_q * a.scale;
     if (lane == 0) {
@@ -393,6 +411,7 @@ struct Scan {
   static constexpr int kPasses = kC / (int)kRows;
   struct Shared {
     __attribute__((aligned(256))) uint8_t k[2][kC * DK * 2];
+    __attribute__((aligned(16))) uint8_t v[2][kC * kSlice * 2];
     u32x4_t state[2][kScanGroups][U][64];                 // before a chunk, scaled
     u32x4_t u[2][kScanGroups][2][64];
     __attribute__((aligned(16))) float vec[2][4 * kC];
@@ -414,7 +433,7 @@ struct Scan {
   // The first wavefront: u and the state after each chunk.  What a chunk needs is loaded a chunk ahead, each part when
   // the one before is used.  Runs of products go over their tiles first, so that none waits for the one before.
   __device__ __forceinline__ void states(const float* before, float* after) {
-    const uint32_t dv = a.value_dim, ldv = (uint32_t)a.ldv, vlane = 2 * (8 * c * ldv + col);
+    const uint32_t dv = a.value_dim;
     f32x4_t st[U][2];   // element i: row 32 u + 8 c + 4 h + i
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -426,23 +445,12 @@ struct Scan {
     // or with 64 bytes, and rows 4 hf and 32 w further change no bits that the pieces' exchange looks at.
     const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c), tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3);
     u32x4_t tw[2][kBlocks];
-    uint16_t v[2][2][4];
     const auto load_t = [&](int32_t j) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item(j) + e * kTriangle + i * kOperand + 16 * lane);
     };
-    const auto load_v = [&](int32_t j) {
-      const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[w][hf][i] = __builtin_amdgcn_raw_buffer_load_b16(r, vlane + (32 * w + 4 * hf + i) * 2 * ldv, 0, 0);
-    };
-    load_v(j0);
     load_t(j0);
     lds_barrier();
     for (int32_t j = j0; j < j1; ++j) {
@@ -451,12 +459,20 @@ struct Scan {
       const uint8_t* k = sh.k[j & 1];
       const float* vec = sh.vec[j & 1];
       const int32_t next = min(j + 1, j1 - 1);
+      // the lane's rows of V, four tokens of its column each, and the rows' factors
+      s16x4_t v[4];
+      f32x4_t c1[4], c2[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t r = 16 * (t & 2) + 8 * c + 4 * (t & 1);
+        v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(sh.v[j & 1] + 2 * kSlice * (r + (n >> 2)) + 32 * group + 8 * (n & 3)));
+        c1[t] = *reinterpret_cast<const f32x4_t*>(vec + r);
+        c2[t] = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
+      }
       // the state in parts, and K S
       float most = 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(st[u][0][i]), fabsf(st[u][1][i])));
+      for (int u = 0; u < U; ++u) most = largest(most, st[u][0], st[u][1]);
       const Scale ss = scale_to(column_max(most), 12);
       f32x4_t ks[4];
 #pragma unroll
@@ -477,20 +493,15 @@ struct Scan {
       f32x4_t rows[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t r = 16 * (t & 2) + 8 * c + 4 * (t & 1);
-        const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[i] * ss.down, ks[t][i], c1[i] * bf16_value(v[t / 2][t % 2][i]));
+        for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[t][i] * ss.down, ks[t][i], c1[t][i] * bf16_value((uint16_t)v[t][i]));
       }
-      load_v(next);
       f32x4_t u[4];   // times 2^12 and the rows' scale
       Scale rs;
       const auto solve = [&] {
         float top = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; t += 2)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(rows[t][i]), fabsf(rows[t + 1][i])));
+        for (int t = 0; t < 4; t += 2) top = largest(top, rows[t], rows[t + 1]);
         rs = scale_to(column_max(top), 6);   // u is at most 2^7 times the largest row
         u32x4_t part[2][2];
 #pragma unroll
@@ -535,10 +546,10 @@ struct Scan {
       u32x4_t up[2][2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        f32x4_t y[2];
+        f32x4_t c3[2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) y[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf) * u[2 * w + hf];
-        split(y[0], y[1], 0x1p-12f, up[w]);
+        for (int hf = 0; hf < 2; ++hf) c3[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf);
+        split(u[2 * w], u[2 * w + 1], c3[0], c3[1], up[w]);
         u32x4_t one[1];
         split(u[2 * w], u[2 * w + 1], 0x1p-12f, one);
         sh.u[j & 1][group][w][lane] = one[0];
@@ -587,22 +598,28 @@ struct Scan {
           for (int i = 0; i < 4; ++i) after[(uint64_t)(32 * u + 4 * hf + i) * dv] = st[u][hf][i];
   }
 
-  // The second wavefront: K of the chunk after, and the outputs of the chunk before, O = diag(e^G) Q S0 + P u.
+  // The second wavefront: K and V of the chunks after, and the outputs of the chunk before, O = diag(e^G) Q S0 + P u.
   __device__ __forceinline__ void outputs() {
-    const uint32_t dv = a.value_dim, ldo = (uint32_t)a.ldo, tid = 64 * group + lane, olane = 2 * (8 * c * ldo + col);
-    u32x4_t kr[kPasses], pw[kBlocks], qw[4][U];
+    const uint32_t dv = a.value_dim, ldo = (uint32_t)a.ldo, ldv = (uint32_t)a.ldv, tid = 64 * group + lane;
+    const uint32_t olane = 2 * (8 * c * ldo + col), vlane = 2 * (tid / 4 * ldv + (col & ~(kSlice - 1)) + 8 * (tid % 4));
+    u32x4_t kr[kPasses], vr[2], pw[kBlocks], qw[4][U];
     f32x4_t c4[4], c6[4];
-    float2 vr;
+    float2 fr;
     const auto load_k = [&](int32_t j) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(j), kh) + 16 * (tid + i * 64 * kScanGroups));
-      vr = *reinterpret_cast<const float2*>(item(j) + kVecAt + 8 * tid);
+      fr = *reinterpret_cast<const float2*>(item(j) + kVecAt + 8 * tid);
+      const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) vr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, vlane + 64 * i * ldv, 0, 0);
     };
     const auto store_k = [&](int b) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
         *reinterpret_cast<u32x4_t*>(sh.k[b] + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
-      *reinterpret_cast<float2*>(&sh.vec[b][2 * tid]) = vr;
+      *reinterpret_cast<float2*>(&sh.vec[b][2 * tid]) = fr;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4_t*>(sh.v[b] + 16 * (tid + 128 * i)) = vr[i];
     };
     const auto load_q = [&](int32_t j) {
 #pragma unroll
