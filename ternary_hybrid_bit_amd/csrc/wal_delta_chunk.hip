@@ -82,6 +82,25 @@ __device__ __forceinline__ Scale scale_to(float most, int to) {
   return Scale{__uint_as_float((254u + to - e) << 23), __uint_as_float((e - to) << 23)};
 }
 
+// For a row by its sum of squares: 2^12 over its length to within a factor of two.
+__device__ __forceinline__ Scale row_scale(float squares) {
+  const uint32_t e = (__float_as_uint(squares) >> 23 & 0xFFu) + 127u >> 1;   // of the length, rounded down
+  return scale_to(__uint_as_float(e << 23), 12);
+}
+
+// The sum over 8 or 16 lanes side by side, in each of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+  x += dpp<0xB1>(x);    // quad_perm [1, 0, 3, 2]
+  x += dpp<0x4E>(x);    // quad_perm [2, 3, 0, 1]
+  x += dpp<0x141>(x);   // row_half_mirror
+  if constexpr (LANES == 16) x += dpp<0x140>(x);   // row_mirror
+  return x;
+}
+
+// 2^(x - y) of sums kept as high and low halves, exact to fp32 however long they are.
+__device__ __forceinline__ float power(float2 x, float2 y) { return __builtin_amdgcn_exp2f((x.x - y.x) + (x.y - y.y)); }
+
 // The largest magnitude of x and eight values; a NaN is passed over.  (Written out: fmaxf() would make each value a
 // number first.)
 __device__ __forceinline__ float largest(float x, f32x4_t y, f32x4_t z) {
@@ -166,7 +185,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
   constexpr uint32_t kPieces = DK / 8, kRows = 256 / kPieces, U = DK / 32;
   constexpr uint32_t kRaw = 2 * kC * DK * 2, kMat = kPair * kC * kLd * 4;
   __shared__ __attribute__((aligned(256))) uint8_t raw[kRaw > kMat ? kRaw : kMat];
-  __shared__ double far[kPair][kC];
+  __shared__ float2 far[kPair][kC];   // sums of the decays' logarithms to base 2, high and low halves
   __shared__ float kk[kC], qq[kC], left[kPair][kC], unit_k[kC], unit_q[kC];
   __shared__ uint32_t first_bad[kPair];
   uint8_t *ks = raw, *qs = raw + kRaw / 2;
@@ -201,7 +220,8 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       const double y = __shfl_up(x, d);
       if (lane >= (uint32_t)d) x += y;
     }
-    far[wave][lane] = x;
+    x *= 1.4426950408889634074;
+    far[wave][lane] = make_float2((float)x, (float)(x - (double)(float)x));
   }
   uint8_t* key_item = key_item_of(a, local, kh);
 #pragma unroll
@@ -222,18 +242,15 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       x = fmaf(k4[j / 4][j % 4], k4[j / 4][j % 4], x);
       y = fmaf(q4[j / 4][j % 4], q4[j / 4][j % 4], y);
     }
-#pragma unroll
-    for (int d = 1; d < (int)kPieces; d *= 2) {
-      x += __shfl_xor(x, d);
-      y += __shfl_xor(y, d);
-    }
+    x = lanes_sum<kPieces>(x);
+    y = lanes_sum<kPieces>(y);
     if (piece == 0) {
       kk[r] = x;
       qq[r] = y;
     }
     u32x4_t kw[1], qw[1];
-    split(k4[0], k4[1], scale_to(sqrtf(x), 12).up, kw);
-    split(q4[0], q4[1], scale_to(sqrtf(y), 12).up, qw);
+    split(k4[0], k4[1], row_scale(x).up, kw);
+    split(q4[0], q4[1], row_scale(y).up, qw);
     *reinterpret_cast<u32x4_t*>(ks + row_piece<DK>(r, piece)) = kw[0];
     *reinterpret_cast<u32x4_t*>(qs + row_piece<DK>(r, piece)) = qw[0];
     if (pair == 0) {
@@ -274,25 +291,25 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     }
   }
   if (wave < heads) {
-    const double g = far[wave][lane], end = far[wave][kC - 1];
+    const float2 g = far[wave][lane], end = far[wave][kC - 1], none = make_float2(0.f, 0.f);
     // keys are unit vectors times lengths: K holds k 2^e, that is unit vectors times 1 / uk
     const float k2 = kk[lane], q2 = qq[lane], kn = sqrtf(k2), qn = sqrtf(q2);
-    const Scale ek = scale_to(kn, 12), eq = scale_to(qn, 12);
+    const Scale ek = row_scale(k2), eq = row_scale(q2);
     const float uk = kn > 0.f ? ek.down / kn : 0.f, uq = qn > 0.f ? eq.down / qn : 0.f;
     const float to_k = unit(a, k2), to_q = unit(a, q2);
-    const bool bad = !(fabsf(k2) < INFINITY) || !(fabsf(beta) < INFINITY) || g != g;
+    const bool bad = !(fabsf(k2) < INFINITY) || !(fabsf(beta) < INFINITY) || g.x != g.x;
     const uint64_t any = __ballot(bad);
     const uint32_t f = any ? (uint32_t)__builtin_ctzll(any) : (uint32_t)kC;
     const float lost = lane >= f ? NAN : 0.f, gone = any ? NAN : 0.f;
-    const float decay = expf((float)g), len = kn * to_k;
+    const float decay = power(g, none), len = kn * to_k;
     float* vec = reinterpret_cast<float*>(item_of(a, local, h0 + wave) + kVecAt);
     vec[lane] = beta * len + lost;
     vec[kC + lane] = beta * len * len * decay * uk + lost;
-    vec[2 * kC + lane] = expf((float)(end - g)) * uk + gone;
+    vec[2 * kC + lane] = power(end, g) * uk + gone;
     vec[3 * kC + lane] = decay * uq;
     vec[4 * kC + lane] = qn * to_q * a.scale;
     if (lane == 0) {
-      vec[5 * kC] = expf((float)end) + gone;
+      vec[5 * kC] = power(end, none) + gone;
       first_bad[wave] = f;
     }
     left[wave][lane] = beta * len * len * uk;
@@ -303,7 +320,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
   }
   __syncthreads();   // K and Q are read: A goes to their place
   for (uint32_t b = 0; b < heads; ++b) {
-    const double* g = far[b];
+    const float2* g = far[b];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
       const uint32_t tile = tile0 + x, it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
@@ -313,7 +330,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       for (int i = 0; i < 4; ++i) {
         const uint32_t row = 16 * it + 4 * c + i;
         const bool in = col < row && row < first_bad[b];
-        t[b][row][col] = in ? left[b][row] * unit_k[col] * expf((float)(g[row] - g[col])) * ak[x][i] : 0.f;
+        t[b][row][col] = in ? left[b][row] * unit_k[col] * power(g[row], g[col]) * ak[x][i] : 0.f;
       }
     }
     if (wave >= 2) {   // tiles (0, 1) and (2, 3): nothing
@@ -330,7 +347,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t col = 32 * sb + 8 * c + 4 * z + i;
-          y[z][i] = col <= row ? unit_q[row] * unit_k[col] * expf((float)(g[row] - g[col])) * pk[x][z][i] : 0.f;
+          y[z][i] = col <= row ? unit_q[row] * unit_k[col] * power(g[row], g[col]) * pk[x][z][i] : 0.f;
         }
       u32x4_t p[1];
       split(y[0], y[1], 4096.f, p);
