@@ -84,7 +84,7 @@ __device__ __forceinline__ Scale scale_to(float most, int to) {
 
 // For a row by its sum of squares: 2^12 over its length to within a factor of two.
 __device__ __forceinline__ Scale row_scale(float squares) {
-  const uint32_t e = (__float_as_uint(squares) >> 23 & 0xFFu) + 127u >> 1;   // of the length, rounded down
+  const uint32_t e = ((__float_as_uint(squares) >> 23 & 0xFFu) + 127u) >> 1;   // of the length, rounded down
   return scale_to(__uint_as_float(e << 23), 12);
 }
 
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
   constexpr uint32_t kPieces = DK / 8, kRows = 256 / kPieces, U = DK / 32;
   constexpr uint32_t kRaw = 2 * kC * DK * 2, kMat = kPair * kC * kLd * 4;
   __shared__ __attribute__((aligned(256))) uint8_t raw[kRaw > kMat ? kRaw : kMat];
-  __shared__ float2 far[kPair][kC];   // sums of the decays' logarithms to base 2, high and low halves
-  __shared__ float kk[kC], qq[kC], left[kPair][kC], unit_k[kC], unit_q[kC];
+  __shared__ __attribute__((aligned(16))) float2 far[kPair][kC];   // sums of the decays' logarithms to base 2, high and low halves
+  __shared__ __attribute__((aligned(16))) float kk[kC], qq[kC], left[kPair][kC], unit_k[kC], unit_q[kC];
   __shared__ uint32_t first_bad[kPair];
   uint8_t *ks = raw, *qs = raw + kRaw / 2;
   float(*t)[kC][kLd] = reinterpret_cast<float(*)[kC][kLd]>(raw);
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       *reinterpret_cast<u32x4_t*>(key_item + kC * 2 * DK + (tile * U + piece / 4) * kOperand + 16 * (16 * (piece % 4) + m)) = qw[0];
     }
   }
-  __syncthreads();
+  lds_barrier();
 
   // The ten 16 x 16 tiles of A's lower triangle by rows; P's six operands: transposed tiles of K Q^T with dealt rows, whose
   // results are what a lane of the operand holds.  Wavefronts 0 and 1 take two tiles and two operands, the others three and one.
@@ -318,19 +318,23 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       unit_q[lane] = uq;
     }
   }
-  __syncthreads();   // K and Q are read: A goes to their place
+  lds_barrier();   // K and Q are read: A goes to their place
   for (uint32_t b = 0; b < heads; ++b) {
     const float2* g = far[b];
+    const uint32_t bad = first_bad[b];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
       const uint32_t tile = tile0 + x, it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
       if (x >= (int)tiles) continue;
-      const uint32_t col = 16 * jt + n;
+      const uint32_t col = 16 * jt + n, row = 16 * it + 4 * c;
+      const f32x4_t l = *reinterpret_cast<const f32x4_t*>(&left[b][row]), g0 = *reinterpret_cast<const f32x4_t*>(&g[row]),
+                    g1 = *reinterpret_cast<const f32x4_t*>(&g[row + 2]);
+      const float2 gc = g[col];
+      const float uk = unit_k[col];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t row = 16 * it + 4 * c + i;
-        const bool in = col < row && row < first_bad[b];
-        t[b][row][col] = in ? left[b][row] * unit_k[col] * power(g[row], g[col]) * ak[x][i] : 0.f;
+        const float2 gr = i < 2 ? make_float2(g0[2 * i], g0[2 * i + 1]) : make_float2(g1[2 * i - 4], g1[2 * i - 3]);
+        t[b][row + i][col] = col < row + i && row + i < bad ? l[i] * uk * power(gr, gc) * ak[x][i] : 0.f;
       }
     }
     if (wave >= 2) {   // tiles (0, 1) and (2, 3): nothing
@@ -342,19 +346,25 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       const uint32_t o = op0 + x, w = o > 1, sb = o > 3, hf = o & 1, row = dealt(w, hf, n);
       if (x >= (int)ops) continue;
       f32x4_t y[2];
+      const float2 gr = g[row];
+      const float uq = unit_q[row];
 #pragma unroll
-      for (int z = 0; z < 2; ++z)
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t col = 32 * sb + 8 * c + 4 * z;
+        const f32x4_t uk = *reinterpret_cast<const f32x4_t*>(&unit_k[col]), g0 = *reinterpret_cast<const f32x4_t*>(&g[col]),
+                      g1 = *reinterpret_cast<const f32x4_t*>(&g[col + 2]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t col = 32 * sb + 8 * c + 4 * z + i;
-          y[z][i] = col <= row ? unit_q[row] * unit_k[col] * power(g[row], g[col]) * pk[x][z][i] : 0.f;
+          const float2 gc = i < 2 ? make_float2(g0[2 * i], g0[2 * i + 1]) : make_float2(g1[2 * i - 4], g1[2 * i - 3]);
+          y[z][i] = col + i <= row ? uq * uk[i] * power(gr, gc) * pk[x][z][i] : 0.f;
         }
+      }
       u32x4_t p[1];
       split(y[0], y[1], 4096.f, p);
       *reinterpret_cast<u32x4_t*>(item_of(a, local, h0 + b) + kPAt + o * kOperand + 16 * lane) = p[0];
     }
   }
-  __syncthreads();
+  lds_barrier();
 
   if (wave < heads) {   // the inverses of the four blocks of the diagonal
     float(*tb)[kLd] = t[wave];
@@ -369,7 +379,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) tb[16 * c + i][16 * c + n] = x[i];
   }
-  __syncthreads();
+  lds_barrier();
   // two wavefronts a head: blocks (1, 0) and (3, 2), then the columns of the lower left 32 x 32
   const uint32_t hb = wave >> 1, half = wave & 1;
   float(*tb)[kLd] = t[hb];
@@ -381,7 +391,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) tb[16 * r + 4 * c + i][16 * b + n] = -z[i];
   }
-  __syncthreads();
+  lds_barrier();
   f32x4_t lower[2];
   if (mine) {
     f32x4_t y[2];
@@ -393,13 +403,13 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     lower[0] = block_product(tb, 2, 2, y[0], n, c, zero);
     lower[1] = block_product(tb, 3, 3, y[1], n, c, block_product(tb, 3, 2, y[0], n, c, zero));
   }
-  __syncthreads();
+  lds_barrier();
   if (mine)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) tb[16 * (2 + k) + 4 * c + i][16 * half + n] = -lower[k][i];
-  __syncthreads();
+  lds_barrier();
   for (uint32_t i = tid; i < heads * kBlocks * 64; i += 256) {
     const uint32_t b = i / (kBlocks * 64), e = i - b * (kBlocks * 64), o = e >> 6, l = e & 63;
     const uint32_t row = dealt(o > 1, o & 1, l & 15), col = 32 * (o > 3) + 8 * (l >> 4);
