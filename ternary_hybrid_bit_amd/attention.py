@@ -17,8 +17,8 @@ from typing import List, Sequence
 import numpy as np
 
 from . import (WAL_KV_BF16, WAL_MAX_BATCH, WAL_ROPE_HALF, make_kv_desc, make_rope_desc, wal_attn_paged,
-               wal_attn_paged_workspace_size, wal_attn_prompt, wal_gemm_prefill, wal_gemm_small, wal_kv_size,
-               wal_kv_write, wal_prefill_workspace_size, wal_rope, wal_rope_freqs, wal_workspace_size)
+               wal_attn_paged_workspace_size, wal_attn_prompt, wal_gemm_prefill, wal_gemm_small, wal_head_norm,
+               wal_kv_size, wal_kv_write, wal_prefill_workspace_size, wal_rope, wal_rope_freqs, wal_workspace_size)
 
 
 def _counts(new: Sequence[int], *rows) -> List[int]:
@@ -32,16 +32,32 @@ def _counts(new: Sequence[int], *rows) -> List[int]:
     return new
 
 
+def _sequences(seqs: Sequence[int], n: int, new=None) -> List[int]:
+    """Distinct sequences of a layer with n, as many as there are counts of new tokens."""
+    seqs = [index(s) for s in seqs]
+    if new is not None and len(seqs) != len(new):
+        raise ValueError(f"{len(seqs)} sequences with {len(new)} counts of new tokens")
+    if len(set(seqs)) != len(seqs):
+        raise ValueError(f"a sequence more than once in {seqs}")
+    for s in seqs:
+        if not 0 <= s < n:
+            raise ValueError(f"sequence {s} of a layer with {n}")
+    return seqs
+
+
 class AttentionLayer:
     """q, k, v, o: (info, packed bytes on the GPU) of the layer's matrices; the
     heads' size is head_dim.  The cache holds n_pages pages of page_size
-    tokens for max_seqs sequences."""
+    tokens for max_seqs sequences.  q_norm, k_norm: weights [head_dim] of norms of the heads of q and
+    of k before the rotation (one type, fp32 or bf16), with eps; None: there is none."""
 
     def __init__(self, q, k, v, o, head_dim: int, n_pages: int, max_seqs: int, page_size: int = 64,
-                 fmt: int = WAL_KV_BF16, rope=None, layout: int = WAL_ROPE_HALF):
+                 fmt: int = WAL_KV_BF16, rope=None, layout: int = WAL_ROPE_HALF, q_norm=None, k_norm=None,
+                 eps: float = 1e-6):
         import torch
         self.torch, self.dev = torch, q[1].device
         self.mats, self.head_dim, self.layout = (q, k, v, o), head_dim, layout
+        self.q_norm, self.k_norm, self.eps = q_norm, k_norm, eps
         self.q_heads, self.kv_heads = q[0].d.out // head_dim, k[0].d.out // head_dim
         turns, self.magnitude = wal_rope_freqs(rope if rope is not None else make_rope_desc(head_dim, base=1e6))
         self.turns = torch.from_numpy(turns).to(self.dev)
@@ -68,18 +84,8 @@ class AttentionLayer:
 
     def _checked(self, seqs: Sequence[int], new: Sequence[int], *rows):
         """seqs and new as lists of int: distinct sequences of the layer with as many new tokens as each tensor has rows."""
-        seqs, new = [index(s) for s in seqs], _counts(new, *rows)
-        if len(seqs) != len(new):
-            raise ValueError(f"{len(seqs)} sequences with {len(new)} counts of new tokens")
-        if len(set(seqs)) != len(seqs):
-            raise ValueError(f"a sequence more than once in {seqs}")
-        for s in seqs:
-            self._known(s)
-        return seqs, new
-
-    def _known(self, s: int):
-        if not 0 <= s < len(self.lens):
-            raise ValueError(f"sequence {s} of a layer with {len(self.lens)}")
+        new = _counts(new, *rows)
+        return _sequences(seqs, len(self.lens), new), new
 
     def _place(self, seqs: Sequence[int], new: Sequence[int]):
         """Where the new tokens go: their cache slots and positions, the sequences' pages with those that they
@@ -105,7 +111,7 @@ class AttentionLayer:
             self.pages[s], self.lens[s] = p, n
 
     def release(self, s: int):
-        self._known(s)
+        s, = _sequences([s], len(self.lens))
         self.free += self.pages[s]
         self.pages[s], self.lens[s] = [], 0
 
@@ -128,7 +134,7 @@ class AttentionLayer:
         slots, pos, lens_dev, starts, tables = self._put(slots, pos, lens, np.cumsum([0] + new), tables)
         q, out = (torch.empty(Q.shape, dtype=torch.bfloat16, device=self.dev) for _ in range(2))
         wal_kv_write(self.desc, self.cache, slots, K, V, pos=pos, turns=self.turns, layout=self.layout,
-                     magnitude=self.magnitude, Q=Q, Q_out=q)
+                     magnitude=self.magnitude, Q=Q, Q_out=q, q_norm=self.q_norm, k_norm=self.k_norm, eps=self.eps)
         max_new, max_len = max(new), max(lens)
         ws = self._workspace("attention", wal_attn_paged_workspace_size(self.desc, self.q_heads, len(seqs),
                                                                         Q.shape[0], max_new, max_len))
@@ -158,8 +164,12 @@ class AttentionLayer:
         Q, K, V = (self._product(m, X) for m in self.mats[:3])
         pos = torch.from_numpy(np.concatenate([np.arange(n) for n in lens]).astype(np.int32)).to(self.dev)
         q, k = (torch.empty(t.shape, dtype=torch.bfloat16, device=self.dev) for t in (Q, K))
-        for t, r in ((Q, q), (K, k)):
-            wal_rope(t, r, pos, self.turns, self.head_dim, layout=self.layout, magnitude=self.magnitude)
+        for t, r, w in ((Q, q, self.q_norm), (K, k, self.k_norm)):
+            if w is None:
+                wal_rope(t, r, pos, self.turns, self.head_dim, layout=self.layout, magnitude=self.magnitude)
+            else:
+                wal_head_norm(t, r, w, self.head_dim, eps=self.eps, pos=pos, turns=self.turns, layout=self.layout,
+                              magnitude=self.magnitude)
         starts = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device=self.dev)
         out = torch.empty_like(q)
         wal_attn_prompt(q, k, V.to(torch.bfloat16), starts, out, self.head_dim, max(lens))
