@@ -132,12 +132,13 @@ __device__ __forceinline__ uint32_t seq_of_place(const Delta& a, uint32_t place,
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)lo);
 }
 
-// What a launch's place holds of a value head and of a key head.
+// What a launch's place holds of a value head and of a key head: a head's places side by side, since they are read one
+// after another.
 __device__ __forceinline__ uint8_t* item_of(const Delta& a, uint32_t local, uint32_t head) {
-  return a.ws + ((uint64_t)local * a.heads + head) * kItemBytes;
+  return a.ws + ((uint64_t)head * a.places + local) * kItemBytes;
 }
 __device__ __forceinline__ uint8_t* key_item_of(const Delta& a, uint32_t local, uint32_t kh) {
-  return a.key_ws + ((uint64_t)local * (a.heads / a.group) + kh) * a.key_item;
+  return a.key_ws + ((uint64_t)kh * a.places + local) * a.key_item;
 }
 
 // Place of a row's 16-byte piece in LDS: 16 neighbours that are read together, the rows of dealt(), and in the transposing
@@ -306,10 +307,10 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     vec[lane] = beta * len + lost;
     vec[kC + lane] = beta * len * len * decay * uk + lost;
     vec[2 * kC + lane] = power(end, g) * uk + gone;
-    vec[3 * kC + lane] = decay * uq;
-    vec[4 * kC + lane] = qn * to_q * a.scale;
+    vec[4 * kC + lane] = decay * uq;
+    vec[5 * kC + lane] = qn * to_q * a.scale;
     if (lane == 0) {
-      vec[5 * kC] = power(end, none) + gone;
+      vec[3 * kC] = power(end, none) + gone;
       first_bad[wave] = f;
     }
     left[wave][lane] = beta * len * len * uk;
@@ -428,21 +429,30 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, 
   return rsrc(p, (uint32_t)(2 * ((uint64_t)(count - 1) * ld + width)));
 }
 
-// Two wavefronts share 16 columns, each on a SIMD of its own: the first takes the states from chunk to chunk, which is
-// what a sequence waits for, the second, a chunk behind, makes the outputs from the states and rows that the first leaves in
-// LDS as operands, and brings the next K.  (One wavefront for both took a quarter longer.)
+// Four wavefronts share 16 columns.  Two take the state from chunk to chunk, half of its rows each, which is what a
+// sequence waits for; they add up K S between them and make u both.  The others, behind them, make the outputs, of 32 of a
+// chunk's tokens each, from the states and rows that the first leave in LDS as operands, and bring the next chunks' K, V, T
+// and factors there.
+//
+// One barrier a chunk, between a chunk's K S and its u:
+//   states   .. | u of j, S, K S of j + 1 | u of j + 1, ..
+//   outputs  .. | out of j - 1, Q S of j, stores K of j + 2 and V, T of j + 1 | ..
+// K is read on both sides of a barrier and kept three times, the rest twice.
 template <int DK>
 struct Scan {
-  static constexpr int U = DK / 32;                       // 32-row blocks of the state
-  static constexpr uint32_t kPieces = DK / 8, kRows = 64 * kScanGroups / kPieces;
-  static constexpr int kPasses = kC / (int)kRows;
+  static constexpr int U = DK / 32, UH = U / 2;           // 32-row blocks of the state, of a half
+  static constexpr uint32_t kPieces = DK / 8, kThreads = 128 * kScanGroups, kRows = kThreads / kPieces;   // that stage
+  static constexpr int kPasses = kC / (int)kRows, kTPasses = 2 * (int)kTriangle / 16 / kThreads;
+  static_assert(kThreads == 256 && kC * kSlice * 2 == 16 * kThreads && 4 * kC == kThreads, "V and the factors in one pass");
   struct Shared {
-    __attribute__((aligned(256))) uint8_t k[2][kC * DK * 2];
+    __attribute__((aligned(256))) uint8_t k[3][kC * DK * 2];
     __attribute__((aligned(16))) uint8_t v[2][kC * kSlice * 2];
+    u32x4_t t[2][2 * kBlocks][64];
     u32x4_t state[2][kScanGroups][U][64];                 // before a chunk, scaled
     u32x4_t u[2][kScanGroups][2][64];
+    f32x4_t ks[2][kScanGroups][2][4][64];                 // the halves' K S
     __attribute__((aligned(16))) float vec[2][4 * kC];
-    float down[2][kScanGroups][2][16];                    // what undoes the columns' scales of both
+    float down[2][kScanGroups][2][16], udown[2][kScanGroups][16];   // what undoes the columns' scales
     int32_t bad[2][kScanGroups][16];                      // the first of a column's rows that is not finite
   };
   const Delta& a;
@@ -457,71 +467,66 @@ struct Scan {
     return chunk_rows(p + (uint64_t)(q.first + j * kC) * ld + at, ld, min(q.rows - j * kC, kC), width);
   }
 
-  // The first wavefront: u and the state after each chunk.  What a chunk needs is loaded a chunk ahead, each part when
-  // the one before is used.  Runs of products go over their tiles first, so that none waits for the one before.
-  __device__ __forceinline__ void states(const float* before, float* after) {
-    const uint32_t dv = a.value_dim;
-    f32x4_t st[U][2];   // element i: row 32 u + 8 c + 4 h + i
+  // Rows DK / 2 half .. of the state; element i of st[u][hf]: row 32 u + 8 c + 4 hf + i of them.  Runs of products go
+  // over their tiles first, so that none waits for the one before.
+  __device__ __forceinline__ void states(uint32_t half, const float* before, float* after) {
+    const uint32_t dv = a.value_dim, at0 = DK / 2 * half;
+    f32x4_t st[UH][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < UH; ++u)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(32 * u + 4 * hf + i) * dv] : 0.f;
+        for (int i = 0; i < 4; ++i) st[u][hf][i] = before ? before[(uint64_t)(at0 + 32 * u + 4 * hf + i) * dv] : 0.f;
     // Lanes' places in K: of rows dealt(0, 0, n), and for the transposing reads; a 32-column block further is an exclusive
     // or with 64 bytes, and rows 4 hf and 32 w further change no bits that the pieces' exchange looks at.
-    const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c), tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3);
-    u32x4_t tw[2][kBlocks];
-    const auto load_t = [&](int32_t j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < (int)kBlocks; ++i) tw[e][i] = *reinterpret_cast<const u32x4_t*>(item(j) + e * kTriangle + i * kOperand + 16 * lane);
-    };
-    load_t(j0);
-    lds_barrier();
-    for (int32_t j = j0; j < j1; ++j) {
-      const float decay = *reinterpret_cast<const __attribute__((address_space(4))) float*>(
-          reinterpret_cast<uintptr_t>(item(j) + kVecAt + 4 * 5 * kC));
-      const uint8_t* k = sh.k[j & 1];
-      const float* vec = sh.vec[j & 1];
-      const int32_t next = min(j + 1, j1 - 1);
-      // the lane's rows of V, four tokens of its column each, and the rows' factors
-      s16x4_t v[4];
-      f32x4_t c1[4], c2[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t r = 16 * (t & 2) + 8 * c + 4 * (t & 1);
-        v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(sh.v[j & 1] + 2 * kSlice * (r + (n >> 2)) + 32 * group + 8 * (n & 3)));
-        c1[t] = *reinterpret_cast<const f32x4_t*>(vec + r);
-        c2[t] = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
-      }
-      // the state in parts, and K S
+    const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c) ^ 64 * UH * half, tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3) ^ 64 * UH * half;
+    f32x4_t ks[4];
+    // the state in parts, and its half of K S of chunk j
+    const auto take = [&](int32_t j, const uint8_t* k) {
       float most = 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) most = largest(most, st[u][0], st[u][1]);
+      for (int u = 0; u < UH; ++u) most = largest(most, st[u][0], st[u][1]);
       const Scale ss = scale_to(column_max(most), 12);
-      f32x4_t ks[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) ks[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < UH; ++u) {
         u32x4_t part[2], kw[4];
-        split(st[u][0], st[u][1], ss.up, part);
-        sh.state[j & 1][group][u][lane] = part[0];
 #pragma unroll
         for (int t = 0; t < 4; ++t) kw[t] = *reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK);
+        split(st[u][0], st[u][1], ss.up, part);
+        sh.state[j & 1][group][UH * half + u][lane] = part[0];
 #pragma unroll
         for (int e = 1; e >= 0; --e)
 #pragma unroll
           for (int t = 0; t < 4; ++t) ks[t] = product(as_operand(kw[t]), as_operand(part[e]), ks[t]);
       }
-      // the rows b V - b e^G K S0
+      if (c == 0) sh.down[j & 1][group][half][n] = ss.down;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ks[t] *= ss.down;
+        sh.ks[j & 1][group][half][t][lane] = ks[t];
+      }
+    };
+    lds_barrier();
+    uint32_t kb = (uint32_t)j0 % 3;
+    take(j0, sh.k[kb]);
+    lds_barrier();
+    for (int32_t j = j0; j < j1; ++j) {
+      const uint8_t* k = sh.k[kb];
+      const float* vec = sh.vec[j & 1];
+      const float decay = vec[3 * kC];
+      // the rows b V - b e^G K S0; the lane's rows of V are four tokens of its column each
       f32x4_t rows[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
+        const uint32_t r = 16 * (t & 2) + 8 * c + 4 * (t & 1);
+        const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(sh.v[j & 1] + 2 * kSlice * (r + (n >> 2)) + 32 * group + 8 * (n & 3)));
+        const f32x4_t c1 = *reinterpret_cast<const f32x4_t*>(vec + r), c2 = *reinterpret_cast<const f32x4_t*>(vec + kC + r);
+        const f32x4_t both = ks[t] + sh.ks[j & 1][group][1 - half][t][lane];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[t][i] * ss.down, ks[t][i], c1[t][i] * bf16_value((uint16_t)v[t][i]));
+        for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[i], both[i], c1[i] * bf16_value((uint16_t)v[i]));
       }
       f32x4_t u[4];   // times 2^12 and the rows' scale
       Scale rs;
@@ -540,7 +545,7 @@ struct Scan {
 #pragma unroll
           for (int b = 0; b < (int)kBlocks; ++b) {
             const int t = 2 * (b > 1) + (b & 1), sb = b > 3;
-            u[t] = product(as_operand(tw[e == 2][b]), as_operand(part[sb][e == 1]), u[t]);
+            u[t] = product(as_operand(sh.t[j & 1][(e == 2) * kBlocks + b][lane]), as_operand(part[sb][e == 1]), u[t]);
           }
       };
       solve();
@@ -563,11 +568,9 @@ struct Scan {
           for (int i = 0; i < 4; ++i)
             if (16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i >= bad) u[t][i] = 0.f;
       }
-      load_t(next);
-      if (c == 0) {
+      if (half == 0 && c == 0) {
         sh.bad[j & 1][group][n] = bad;
-        sh.down[j & 1][group][0][n] = ss.down;
-        sh.down[j & 1][group][1][n] = rs.down * 0x1p-12f;
+        sh.udown[j & 1][group][n] = rs.down * 0x1p-12f;
       }
       // S = decay S + K^T diag(e^(G_end - G)) u
       u32x4_t up[2][2];
@@ -577,142 +580,167 @@ struct Scan {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) c3[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf);
         split(u[2 * w], u[2 * w + 1], c3[0], c3[1], up[w]);
-        u32x4_t one[1];
-        split(u[2 * w], u[2 * w + 1], 0x1p-12f, one);
-        sh.u[j & 1][group][w][lane] = one[0];
-      }
-      const float back = rs.down * 0x1p-12f;
-#pragma unroll
-      for (int ub = 0; ub < U; ub += 2) {
-        f32x4_t add[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) add[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          union { s16x4_t half[2]; u32x4_t all; } kt[4];   // four tokens of the lane's row of K^T each
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-              kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (lds_s16x4_t*)(k + (tat ^ 64 * (ub + t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
-#pragma unroll
-          for (int e = 1; e >= 0; --e)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) add[t] = product(as_operand(kt[t].all), as_operand(up[w][e]), add[t]);
+        if (half == 0) {
+          u32x4_t one[1];
+          split(u[2 * w], u[2 * w + 1], 0x1p-12f, one);
+          sh.u[j & 1][group][w][lane] = one[0];
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) st[ub + t / 2][t % 2][i] = fmaf(add[t][i], back, decay * st[ub + t / 2][t % 2][i]);
       }
-      if (__any(bad < kC)) {
+      const float back = bad < kC ? NAN : rs.down * 0x1p-12f;
+      f32x4_t add[2 * UH];
 #pragma unroll
-        for (int ub = 0; ub < U; ++ub)
+      for (int t = 0; t < 2 * UH; ++t) add[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
+      for (int w = 0; w < 2; ++w) {
+        union { s16x4_t half[2]; u32x4_t all; } kt[2 * UH];   // four tokens of the lane's row of K^T each
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st[ub][hf][i] = bad < kC ? NAN : st[ub][hf][i];
+        for (int t = 0; t < 2 * UH; ++t)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4_t*)(k + (tat ^ 64 * (t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
+#pragma unroll
+        for (int e = 1; e >= 0; --e)
+#pragma unroll
+          for (int t = 0; t < 2 * UH; ++t) add[t] = product(as_operand(kt[t].all), as_operand(up[w][e]), add[t]);
       }
+#pragma unroll
+      for (int t = 0; t < 2 * UH; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[t / 2][t % 2][i] = fmaf(add[t][i], back, decay * st[t / 2][t % 2][i]);
+      kb = kb == 2 ? 0 : kb + 1;
+      take(j + 1, sh.k[kb]);   // behind the last chunk: of some chunk's K, and not read
       lds_barrier();
     }
     if (after)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < UH; ++u)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) after[(uint64_t)(32 * u + 4 * hf + i) * dv] = st[u][hf][i];
+          for (int i = 0; i < 4; ++i) after[(uint64_t)(at0 + 32 * u + 4 * hf + i) * dv] = st[u][hf][i];
   }
 
-  // The second wavefront: K and V of the chunks after, and the outputs of the chunk before, O = diag(e^G) Q S0 + P u.
-  __device__ __forceinline__ void outputs() {
-    const uint32_t dv = a.value_dim, ldo = (uint32_t)a.ldo, ldv = (uint32_t)a.ldv, tid = 64 * group + lane;
-    const uint32_t olane = 2 * (8 * c * ldo + col), vlane = 2 * (tid / 4 * ldv + (col & ~(kSlice - 1)) + 8 * (tid % 4));
-    u32x4_t kr[kPasses], vr[2], pw[kBlocks], qw[4][U];
-    f32x4_t c4[4], c6[4];
-    float2 fr;
+  // O = diag(e^G) Q S0 + P u, of tokens 32 w ..  What is stored to LDS was loaded a chunk before, operands when the ones
+  // before are used.
+  __device__ __forceinline__ void outputs(uint32_t w) {
+    const uint32_t dv = a.value_dim, ldo = (uint32_t)a.ldo, ldv = (uint32_t)a.ldv, tid = 64 * (kScanGroups * w + group) + lane;
+    const uint32_t olane = 2 * ((32 * w + 8 * c) * ldo + col), vlane = 2 * (tid / 4 * ldv + (col & ~(kSlice - 1)) + 8 * (tid % 4));
+    u32x4_t kr[kPasses], vr, tr[kTPasses], pw[2][2], qw[2][U];   // P: of 32 tokens before (zeros for the first), of its own
+    f32x4_t c4[2], c6[2], o[2][2];
+    float fr;
+    const int32_t last = j1 - 1;
     const auto load_k = [&](int32_t j) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(j), kh) + 16 * (tid + i * 64 * kScanGroups));
-      fr = *reinterpret_cast<const float2*>(item(j) + kVecAt + 8 * tid);
-      const __amdgpu_buffer_rsrc_t r = rows_of(a.v, a.ldv, j, h * dv, dv);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) vr[i] = __builtin_amdgcn_raw_buffer_load_b128(r, vlane + 64 * i * ldv, 0, 0);
+      for (int i = 0; i < kPasses; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(min(j, last)), kh) + 16 * (tid + i * kThreads));
     };
-    const auto store_k = [&](int b) {
+    const auto store_k = [&](int32_t j) {
+      uint8_t* k = sh.k[(uint32_t)j % 3];
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i)
-        *reinterpret_cast<u32x4_t*>(sh.k[b] + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
-      *reinterpret_cast<float2*>(&sh.vec[b][2 * tid]) = fr;
+      for (int i = 0; i < kPasses; ++i) *reinterpret_cast<u32x4_t*>(k + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
+    };
+    const auto load_rest = [&](int32_t j) {
+      const uint8_t* p = item(min(j, last));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4_t*>(sh.v[b] + 16 * (tid + 128 * i)) = vr[i];
+      for (int i = 0; i < kTPasses; ++i) tr[i] = *reinterpret_cast<const u32x4_t*>(p + 16 * (tid + i * kThreads));
+      fr = *reinterpret_cast<const float*>(p + kVecAt + 4 * tid);
+      vr = __builtin_amdgcn_raw_buffer_load_b128(rows_of(a.v, a.ldv, min(j, last), h * dv, dv), vlane, 0, 0);
+    };
+    const auto store_rest = [&](int32_t j) {
+#pragma unroll
+      for (int i = 0; i < kTPasses; ++i) (&sh.t[j & 1][0][0])[tid + i * kThreads] = tr[i];
+      sh.vec[j & 1][tid] = fr;
+      *reinterpret_cast<u32x4_t*>(sh.v[j & 1] + 16 * tid) = vr;
     };
     const auto load_q = [&](int32_t j) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          qw[t][u] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(j), kh) + kC * 2 * DK + (t * U + u) * kOperand + 16 * lane);
+          qw[t][u] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(min(j, last)), kh) + kC * 2 * DK + ((2 * w + t) * U + u) * kOperand + 16 * lane);
     };
     const auto load_p = [&](int32_t j) {
+      const uint8_t* p = item(min(j, last));
 #pragma unroll
-      for (int i = 0; i < (int)kBlocks; ++i) pw[i] = *reinterpret_cast<const u32x4_t*>(item(j) + kPAt + i * kOperand + 16 * lane);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint8_t* p = item(j) + kVecAt + 4 * (3 * kC + 16 * (t & 2) + 8 * c + 4 * (t & 1));
-        c4[t] = *reinterpret_cast<const f32x4_t*>(p);
-        c6[t] = *reinterpret_cast<const f32x4_t*>(p + 4 * kC);
+      for (int t = 0; t < 2; ++t) {
+        pw[0][t] = w ? *reinterpret_cast<const u32x4_t*>(p + kPAt + (2 + t) * kOperand + 16 * lane) : u32x4_t{0, 0, 0, 0};
+        pw[1][t] = *reinterpret_cast<const u32x4_t*>(p + kPAt + (4 * w + t) * kOperand + 16 * lane);
+        const uint8_t* f = p + kVecAt + 4 * (4 * kC + 32 * w + 8 * c + 4 * t);
+        c4[t] = *reinterpret_cast<const f32x4_t*>(f);
+        c6[t] = *reinterpret_cast<const f32x4_t*>(f + 4 * kC);
       }
     };
-    load_k(j0);
-    store_k(j0 & 1);
-    lds_barrier();
-    load_k(min(j0 + 1, j1 - 1));
-    load_p(j0);
-    load_q(j0);
-    store_k((j0 + 1) & 1);
-    load_k(min(j0 + 2, j1 - 1));
-    lds_barrier();
-    for (int32_t j = j0; j < j1; ++j) {
-      // the states' wavefront is at chunk j + 1, whose K is there
-      f32x4_t o[4], p[4];
+    const auto from_state = [&](int32_t j) {   // Q S of chunk j, by the state's halves
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[t] = p[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      store_k(j & 1);   // of chunk j + 2: all are done with chunk j's
-      load_k(min(j + 3, j1 - 1));
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const f16x8_t part = as_operand(sh.state[j & 1][group][u][lane]);
+        for (int t = 0; t < 2; ++t) o[e][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) o[t] = product(as_operand(qw[t][u]), part, o[t]);
-      }
-      load_q(min(j + 1, j1 - 1));
+      for (int u = 0; u < UH; ++u)
 #pragma unroll
-      for (int i = 0; i < (int)kBlocks; ++i) {
-        const int t = 2 * (i > 1) + (i & 1);
-        p[t] = product(as_operand(pw[i]), as_operand(sh.u[j & 1][group][i > 3][lane]), p[t]);
-      }
-      const float ds = sh.down[j & 1][group][0][n], du = sh.down[j & 1][group][1][n];
-      const int32_t bad = sh.bad[j & 1][group][n];
+        for (int e = 0; e < 2; ++e) {
+          const f16x8_t part = as_operand(sh.state[j & 1][group][UH * e + u][lane]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) o[e][t] = product(as_operand(qw[t][UH * e + u]), part, o[e][t]);
+        }
+      const float d0 = sh.down[j & 1][group][0][n], d1 = sh.down[j & 1][group][1][n];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[0][t][i] = fmaf(d0, o[0][t][i], d1 * o[1][t][i]);
+    };
+    const auto finish = [&](int32_t j) {
+      f32x4_t p[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const f16x8_t first = as_operand(sh.u[j & 1][group][0][lane]), own = as_operand(sh.u[j & 1][group][w][lane]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) p[t] = product(as_operand(pw[0][t]), first, p[t]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) p[t] = product(as_operand(pw[1][t]), own, p[t]);
+      const float du = sh.udown[j & 1][group][n];
+      const int32_t bad = sh.bad[j & 1][group][n] - 32 * (int32_t)w;
       const __amdgpu_buffer_rsrc_t r = rows_of(a.out, a.ldo, j, h * dv, dv);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t row = 16 * (t & 2) + 4 * (t & 1) + i;
-          const float y = c6[t][i] * fmaf(c4[t][i] * ds, o[t][i], du * p[t][i]);
-          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)((int32_t)(row + 8 * c) >= bad ? NAN : y)), r,
-                                                olane + row * 2 * ldo, 0, 0);
+          const float y = c6[t][i] * fmaf(c4[t][i], o[0][t][i], du * p[t][i]);
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)((int32_t)(4 * t + i + 8 * c) >= bad ? NAN : y)), r,
+                                                olane + (4 * t + i) * 2 * ldo, 0, 0);
         }
-      load_p(min(j + 1, j1 - 1));
-      if (j + 1 < j1) lds_barrier();   // (the other wavefronts have met here once less)
+    };
+    load_k(j0);
+    load_rest(j0);
+    store_k(j0);
+    load_k(j0 + 1);
+    store_rest(j0);
+    store_k(j0 + 1);
+    load_k(j0 + 2);
+    load_rest(j0 + 1);
+    load_q(j0);
+    load_p(j0);
+    lds_barrier();
+    lds_barrier();   // the states' first K S
+    const auto step = [&](int32_t j) {
+      store_k(j + 2);
+      load_k(j + 3);
+      store_rest(j + 1);
+      load_rest(j + 2);
+      from_state(j);
+      load_q(j + 1);
+      lds_barrier();
+    };
+    step(j0);   // (before the loop and at its end: what is in flight is the same both ways in, and no wait covers more than it has to)
+    for (int32_t j = j0; j < last; ++j) {
+      finish(j);
+      load_p(j + 1);
+      step(j + 1);
     }
+    finish(last);
   }
 };
 
 template <int DK>
-__global__ __launch_bounds__(128 * kScanGroups, 1) void k_delta_scan(Delta a) {
+__global__ __launch_bounds__(256 * kScanGroups, 1) void k_delta_scan(Delta a) {
   __shared__ typename Scan<DK>::Shared sh;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, c = lane >> 4;
   const uint32_t group = wave % kScanGroups;
@@ -730,8 +758,9 @@ __global__ __launch_bounds__(128 * kScanGroups, 1) void k_delta_scan(Delta a) {
   const uint64_t head_at = ((uint64_t)h * DK + 8 * c) * a.value_dim + col;
   float* kept = slot < 0 ? nullptr : a.state + (uint64_t)slot * a.heads * DK * a.value_dim + head_at;
   Scan<DK> scan{a, sh, q, base, h, h / a.group, col, lane, n, c, group, j0, j1};
-  if (wave < kScanGroups) scan.states(j0 ? a.carry[0] + head_at : kept, j1 < chunks ? a.carry[1] + head_at : kept);
-  else scan.outputs();
+  const uint32_t role = wave / kScanGroups;
+  if (role < 2) scan.states(role, j0 ? a.carry[0] + head_at : kept, j1 < chunks ? a.carry[1] + head_at : kept);
+  else scan.outputs(role - 2);
 }
 
 template <int DK>
@@ -745,7 +774,7 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
     const uint64_t blocks = ((uint64_t)a.n_seqs * a.heads + 7) / 8 * 8 * a.slices;
     if (items > 0x7FFFFFFFull || blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
     hipLaunchKernelGGL((k_delta_chunk<DK>), dim3((uint32_t)items), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(128 * kScanGroups), 0, s, a);
+    hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(256 * kScanGroups), 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
