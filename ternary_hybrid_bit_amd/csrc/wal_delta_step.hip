@@ -6,16 +6,18 @@
 //
 // Bound by the bytes of the states, each read and written once however many tokens
 // a sequence has in the call.  A workgroup takes 32 columns of one head of one
-// sequence: a wavefront's load covers whole 128-byte pieces of eight rows, a thread keeps
-// key_dim / 32 rows of four columns in registers, and sums over rows meet by lane
-// exchange in a wavefront and once in LDS, summed in one order by every wavefront.
+// sequence, or 64: a wavefront's load covers whole 128-byte lines, a thread keeps some rows of
+// four columns in registers, and sums over rows meet by lane exchange in a
+// wavefront and once in LDS, summed in one order by every wavefront.
+//
+// Measured (16 key and 48 value heads of 128): 64 sequences 85 us, 4.8 TB/s (a copy reaches 5.2); one sequence 5.8 us.
 #include <hip/hip_runtime.h>
 
 #include "wal_delta.h"
 
 namespace {
 
-constexpr uint32_t kThreads = 256, kWaves = kThreads / 64, kRowThreads = kThreads / 8;
+constexpr uint32_t kThreads = 256, kWaves = kThreads / 64;
 
 // A token's rows as a thread needs them.
 template <int J>
@@ -27,31 +29,40 @@ struct Token {
 
 template <int J>
 __device__ __forceinline__ void load_row(const uint16_t* p, float (&x)[J]) {
-  if constexpr (J == 4) {
-    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+  uint32_t w[J / 2];
+  if constexpr (J >= 8) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < J / 8; ++i) {
+      const u32x4_t r = reinterpret_cast<const u32x4_t*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = r[j];
     }
+  } else if constexpr (J == 4) {
+    const u32x2_t r = *reinterpret_cast<const u32x2_t*>(p);
+    w[0] = r[0];
+    w[1] = r[1];
   } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    x[0] = __uint_as_float(w << 16);
-    x[1] = __uint_as_float(w & 0xFFFF0000u);
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int i = 0; i < J / 2; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 
-template <int DK>
+template <int DK, int NV>
 __global__ __launch_bounds__(kThreads) void k_delta_step(Delta a) {
-  constexpr int J = DK / kRowThreads;   // rows of a thread
+  constexpr uint32_t kCols = NV / 4;               // threads side by side
+  constexpr int J = DK / (int)(kThreads / kCols);  // rows of a thread
   constexpr int kSums = 11;             // S^T k and S^T q of four columns, k . k, q . q, k . q
-  __shared__ float sums[2][kWaves][8][kSums + 1];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = threadIdx.x & 7, r = threadIdx.x >> 3;
-  const uint32_t slice = blockIdx.x % a.slices, rest = blockIdx.x / a.slices, h = rest % a.heads, s = rest / a.heads;
+  __shared__ float sums[2][kWaves][kCols][kSums + 1];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = threadIdx.x % kCols, r = threadIdx.x / kCols;
+  const uint32_t slices = a.value_dim / NV, slice = blockIdx.x % slices, rest = blockIdx.x / slices, h = rest % a.heads, s = rest / a.heads;
   const Seq seq = delta_seq(a, s);
   if (!seq.rows) return;
   const int64_t slot = kept_at(a, s);
-  const uint32_t kh = h / a.group, col = kSlice * slice + 4 * c;
+  const uint32_t kh = h / a.group, col = NV * slice + 4 * c;
   float* state = a.state + ((uint64_t)max(slot, (int64_t)0) * a.heads + h) * DK * a.value_dim + (uint64_t)(J * r) * a.value_dim + col;
   const auto token = [&](int32_t i) {
     Token<J> t;
@@ -86,8 +97,8 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(Delta a) {
 #pragma unroll
     for (int e = 0; e < kSums; ++e)
 #pragma unroll
-      for (int d = 8; d < 64; d *= 2) x[e] += __shfl_xor(x[e], d);
-    if (lane < 8)
+      for (int d = kCols; d < 64; d *= 2) x[e] += __shfl_xor(x[e], d);
+    if (lane < kCols)
 #pragma unroll
       for (int e = 0; e < kSums; ++e) sums[i & 1][wave][c][e] = x[e];
     __syncthreads();   // (two buffers: the next token's sums go to the other one)
@@ -122,16 +133,29 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(Delta a) {
     for (int j = 0; j < J; ++j) *reinterpret_cast<f32x4_t*>(state + (uint64_t)j * a.value_dim) = m[j];
 }
 
+template <int DK, int NV>
+void launch(const Delta& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_delta_step<DK, NV>), dim3(a.n_seqs * a.heads * (a.value_dim / NV)), dim3(kThreads), 0, s, a);
+}
+
+// Columns of a workgroup: 64 where that makes two workgroups for each compute unit, else 32 (key heads of 128, 64 sequences
+// of 48 heads 85 us and 92 with 32; 13 sequences of up to 5 tokens, 32 heads 20 and 27; one sequence of 48 heads 6.1 and
+// 5.8).  128 are no faster (86, 20 and 7.0 us).
+template <int DK>
+void launch(const Delta& a, hipStream_t s) {
+  if (a.value_dim % 64 == 0 && (uint64_t)a.n_seqs * a.heads * (a.value_dim / 64) >= 512) launch<DK, 64>(a, s);
+  else launch<DK, 32>(a, s);
+}
+
 }  // namespace
 
 namespace wal {
 
 int delta_step(const Delta& a, uint32_t key_dim, void* stream) {
-  const uint64_t blocks = (uint64_t)a.n_seqs * a.heads * a.slices;
-  if (blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
+  if ((uint64_t)a.n_seqs * a.heads * a.slices > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (key_dim == 64) hipLaunchKernelGGL((k_delta_step<64>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_delta_step<128>), dim3((uint32_t)blocks), dim3(kThreads), 0, s, a);
+  if (key_dim == 64) launch<64>(a, s);
+  else launch<128>(a, s);
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
 
