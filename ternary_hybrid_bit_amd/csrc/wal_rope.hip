@@ -8,7 +8,7 @@
 // All calls are one pass over memory, bound by its bandwidth for many
 // tokens and by one round trip for few.  The work is cut into units of 16
 // elements of one head: eight pairs (two pieces of eight elements in the half
-// layout, 16 neighbours in the interleaved one) or 16 unrotated elements, so
+// layout, 16 neighbours in the interleaved one) or two pieces of unrotated elements, so
 // every access is 16 bytes a lane and the D / 16 lanes of a head sit side by
 // side for the row maximum.  A workgroup takes whole tokens; it computes the
 // sines of its tokens once, into LDS, for all their heads, while the first
@@ -151,9 +151,11 @@ __device__ __forceinline__ Unit unit_of(const RopeKv& a, uint32_t t, uint32_t u)
   x.head = w / a.lanes;
   x.j = w - x.head * a.lanes;
   x.rotated = x.kind < 2 && x.j < a.rot_units;
-  const bool split = x.rotated && !a.interleaved;
-  x.lo = split ? 8 * x.j : 16 * x.j;
-  x.hi = split ? a.rot / 2 + 8 * x.j : 16 * x.j + 8;
+  // pieces of neighbouring lanes side by side: of both halves of the rotated elements, and of the others
+  const uint32_t first = x.rotated ? 0 : x.kind < 2 ? a.rot : 0, width = x.rotated ? a.rot : a.dim - first;
+  const bool pairs = x.rotated && a.interleaved;
+  x.lo = pairs ? 16 * x.j : first + 8 * (x.j - first / 16);
+  x.hi = pairs ? 16 * x.j + 8 : x.lo + width / 2;
   return x;
 }
 
