@@ -8,7 +8,11 @@ namespace {
 
 constexpr uint32_t kMaxRows = 1u << 24;   // rows and sequences of a call
 constexpr uint32_t kMaxPitch = 1u << 24;  // elements from a row to the next: 64 rows in 32 bits of bytes
-constexpr uint32_t kFewRows = 16;         // of a sequence: token by token
+// Tokens of a sequence up to which a call goes token by token.  On chunks the time is the same up to 64 tokens and grows
+// with sequences times heads, token by token it grows with the tokens and little with the others before memory is busy (calls
+// from Python, tokens against chunks; one sequence, 48 heads of 128: 8 tokens 17 and 19 us, 12 tokens 23 and 19; 13 sequences,
+// 32 heads: 24 tokens 49 and 55 us, 32 tokens 64 and 55; 64 sequences, 48 heads: 24 tokens 202 and 296 us).
+constexpr uint32_t kFewRows = 8, kFewRowsOfMany = 24, kMany = 256;
 constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: what the last cache holds
 
 // How a call is cut.
@@ -20,7 +24,7 @@ struct Plan {
 
 Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new) {
   Plan p{};
-  p.step = max_new <= kFewRows;
+  p.step = max_new <= ((uint64_t)n_seqs * d->value_heads >= kMany ? kFewRowsOfMany : kFewRows);
   if (p.step || !n || !n_seqs) return p;
   const uint64_t place = place_bytes(d->key_heads, d->value_heads, d->key_dim), most = kMaxItems / place;
   p.all = n / kChunk + n_seqs;

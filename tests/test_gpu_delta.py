@@ -119,6 +119,7 @@ class Case:
 @pytest.mark.parametrize("new,kw", [
     ([1], {}), ([1], dict(kh=16, group=3, dk=128, dv=128)), ([1] * 5, dict(dk=128, dv=256)), ([1] * 70, dict(kh=1, group=1, raw=False)),
     ([2, 0, 5, 1, 0], dict(dv=96)), ([0, 0], {}), ([5, 3, 4], dict(dk=128, dv=64, norm=False)), ([16, 9, 2], dict(kh=3, group=1, raw=False)),
+    ([24, 1] + [3] * 62, dict(kh=2, group=2, dv=64)), ([7, 8], dict(kh=1, group=5, dk=128, dv=192)),
     ([1, 1, 1], dict(slots=[-1, 9, 1], places=4)), ([3, 2], dict(keep=False)), ([4, 1], dict(before=3, behind=5)),
     ([2, 2], dict(scale=-0.7, dv=160)),
 ])
@@ -249,6 +250,60 @@ def test_max_new_cuts_and_starts_that_do_not_rise(wal, new):
         assert (whole[:10] == -7).all() and (whole[n + 10:] == -7).all() and (whole[:, c.h * c.dv:] == -7).all()
         others = [i for i in range(c.places) if i not in c.slots]
         assert torch.equal(state[others], c.state0[others])
+
+
+def recurrence(c):
+    """The definition in float64 with torch on the GPU, for calls that are long for numpy: (out, state)."""
+    heads = lambda t, d: t.double().unflatten(1, (-1, d))  # noqa: E731
+    q, k, v = heads(c.q, c.dk), heads(c.k, c.dk), heads(c.v, c.dv)
+    q, k = ((t * torch.rsqrt(t.square().sum(-1, keepdim=True) + 1e-6)).repeat_interleave(c.h // c.kh, 1) for t in (q, k))
+    alpha, beta = (torch.from_numpy(t).cuda() for t in B.gates(host(c.a), host(c.b), host(c.decay), host(c.shift)))
+    out, state = torch.zeros_like(v), c.state0.double()
+    for s, slot in enumerate(c.slots):
+        m = state[slot].clone()
+        for t in range(c.starts[s], c.starts[s + 1]):
+            m *= alpha[t][:, None, None]
+            u = beta[t][:, None] * (v[t] - torch.matmul(k[t][:, None], m)[:, 0])
+            m += k[t][:, :, None] * u[:, None]
+            out[t] = c.desc.scale * torch.matmul(q[t][:, None], m)[:, 0]
+        state[slot] = m
+    return out.flatten(1), state
+
+
+def test_calls_cut_into_several_launches(wal):
+    """More chunks than one launch's share of the workspace: states of sequences that go on are carried over, short ones lie
+    between and at the cuts."""
+    new = [1500, 3, 64, 2500, 1, 700, 0, 130]
+    c = Case(wal, new, kh=96, group=1, dk=128, dv=32, seed=81)
+    assert c.ws.numel() < (c.n // 64 + len(new)) * 96 * 50000   # less than all chunks at once need
+    out, state = c.call()
+    ref, ref_state = recurrence(c)
+    for s in range(len(new)):
+        rows = slice(int(c.starts[s]), int(c.starts[s + 1]))
+        assert (out[rows].double() - ref[rows]).norm() <= 3e-3 * ref[rows].norm(), s
+        got, want = state[c.slots[s]].double(), ref_state[c.slots[s]]
+        assert (got - want).norm() <= 1e-6 * want.norm(), s
+    again, state2 = c.call()
+    assert torch.equal(again, out) and torch.equal(state2, state)
+
+
+def test_calls_at_the_same_time(wal):
+    """Two streams, each with its own workspace and states."""
+    cases = [Case(wal, new, dk=128, dv=64, seed=90 + i) for i, new in enumerate(([300, 20], [257], [2, 1, 3]))]
+    want = [tuple(t.clone() for t in c.call()) for c in cases]
+    starts, slots = [i32(c.starts) for c in cases], [i32(c.slots) for c in cases]
+    states, outs = [c.state0.clone() for c in cases], [torch.full_like(c.out, -7.0) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, st, x, y, state, out in zip(cases, streams, starts, slots, states, outs):
+            with torch.cuda.stream(st):
+                state.copy_(c.state0)
+                wal.wal_delta(c.desc, c.q, c.k, c.v, c.a, c.b, x, out[:, :c.h * c.dv], state=state, slots=y, ws=c.ws, decay=c.decay,
+                              shift=c.shift, max_new=c.max_new)
+        torch.cuda.synchronize()
+        for (o, s), state, out, c in zip(want, states, outs, cases):
+            assert torch.equal(out[:, :c.h * c.dv], o) and torch.equal(state, s)
 
 
 @pytest.mark.parametrize("new", [[1, 1, 1], [2, 70, 130]])
