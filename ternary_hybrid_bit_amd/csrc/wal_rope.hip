@@ -388,6 +388,10 @@ int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
     if (a.slice > a.units) a.slice = a.units;
   } else {
     while (a.tokens < by_lds && a.tokens * a.units < 4 * kRopeThreads) ++a.tokens;
+    // fewer, down to two units a thread, where they fill the threads' last round better
+    const auto rounds = [&](uint32_t tokens) { return (tokens * a.units + kRopeThreads - 1) / kRopeThreads; };
+    for (uint32_t t = a.tokens; t && t * a.units >= 2 * kRopeThreads; --t)
+      if ((uint64_t)t * rounds(a.tokens) > (uint64_t)a.tokens * rounds(t)) a.tokens = t;
   }
   const dim3 grid((a.n + a.tokens - 1) / a.tokens, (a.units + a.slice - 1) / a.slice);
   if (mode == kAsIs) launch<kAsIs>(a, bf16_in, grid, s);
