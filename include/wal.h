@@ -761,7 +761,9 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  * head h / (value_heads / key_heads); for each token of a sequence in turn
  *     S <- alpha S + beta k (v - alpha S^T k)^T,     out[t][h] = scale S^T q.
  *   k, q     k[t], q[t] divided by sqrt(sum_j x_j^2 + norm_eps) when that is above 0
- *            (normal), as they are when it is 0
+ *            (normal), as they are when it is 0.  The sum is fp32: a row for which it is past
+ *            its range counts as not finite, and one for which it is neither 0 nor normal
+ *            loses bits
  *   alpha    exp(-decay[h] softplus(a[t][h] + shift[h])), beta = 1 / (1 + exp(-b[t][h]));
  *            decay and shift NULL: alpha = exp(a[t][h]), beta = b[t][h].  The
  *            logarithm of alpha is taken as 0 where it is above
@@ -773,9 +775,12 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  *   max_new  bounds the sequences' rows: rows past it are neither computed nor kept
  *   ws       wal_delta_workspace_size bytes, 256-byte aligned (NULL when that is 0),
  *            contents arbitrary.  Calls that may overlap in time need their own
- * States, norms, gates and sums are fp32.  From a token with an infinity or NaN among its
- * q, k, v or gates on, what depends on it is an infinity or NaN.  The result does not
- * depend on timing.
+ * States, norms, gates and sums are fp32; a call whose max_new is large enough works on
+ * chunks of 64 tokens, where products take values in 22 bits for the state and 11 for the outputs.
+ * beta |k|^2 (of k as used) is meant to be from 0 to 2, where no token enlarges a state: past that
+ * states grow from token to token, and where calls work on chunks they are less exact, from
+ * about 16 on infinities or NaN.  From a token on whose q, k, v, alpha or beta holds an infinity
+ * or NaN, what depends on it is an infinity or NaN.  The result does not depend on timing.
  * Errors: ARG, SHAPE, ALIGN, BUFFER, DEVICE. */
 typedef struct {
   uint32_t key_heads, value_heads;  /* value_heads a multiple of key_heads, at most 1024    */

@@ -40,6 +40,7 @@ struct Delta {
   uint8_t* key_ws;               // of key heads
   float* carry[2];
   uint32_t place0, places, key_item;
+  uint32_t seqs;                 // sequences that a launch of the scan looks at
 };
 
 // Launches (wal_status).
@@ -77,7 +78,10 @@ __device__ __forceinline__ Gates gates_of(const Delta& a, uint64_t row, uint32_t
 
 __device__ __forceinline__ float bf16_value(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
 
-// 1 / sqrt(sum of squares + eps): what a row of q or k is multiplied by.
-__device__ __forceinline__ float unit(const Delta& a, float squares) { return a.eps > 0.f ? 1.f / sqrtf(squares + a.eps) : 1.f; }
+// 1 / sqrt(sum of squares + eps): what a row of q or k is multiplied by.  Squares past the range of fp32 would make it 0 and
+// the row's part vanish without a sign of it: NaN, as on chunks.
+__device__ __forceinline__ float unit(const Delta& a, float squares) {
+  return !(squares < INFINITY) ? NAN : a.eps > 0.f ? 1.f / sqrtf(squares + a.eps) : 1.f;
+}
 
 }  // namespace

@@ -747,8 +747,11 @@ __global__ __launch_bounds__(256 * kScanGroups, 1) void k_delta_scan(Delta a) {
   // The workgroups of a head sit on one chiplet, so that its cache serves what they share: blocks go to the eight
   // chiplets in turn.
   const uint32_t x = blockIdx.x % 8, g = blockIdx.x / 8, pair = g / a.slices * 8 + x;
-  if (pair >= a.n_seqs * a.heads) return;
-  const uint32_t s = pair / a.heads, h = pair % a.heads, col = kSlice * (g % a.slices) + 16 * group + n;
+  if (pair >= a.seqs * a.heads) return;
+  // from the sequence of the launch's first place on
+  const uint32_t s = (a.place0 ? seq_of_place(a, a.place0, lane) : 0) + pair / a.heads, h = pair % a.heads;
+  if (s >= a.n_seqs) return;
+  const uint32_t col = kSlice * (g % a.slices) + 16 * group + n;
   const Seq q = delta_seq(a, s);
   const uint32_t base = (uint32_t)q.first / kC + s;
   const int32_t chunks = (q.rows + kC - 1) / kC;
@@ -771,7 +774,8 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
     a.carry[0] = carry[i % 2];
     a.carry[1] = carry[(i + 1) % 2];
     const uint64_t items = (uint64_t)(all - first < a.places ? all - first : a.places) * (a.heads / a.group) * ((a.group + kPair - 1) / kPair);
-    const uint64_t blocks = ((uint64_t)a.n_seqs * a.heads + 7) / 8 * 8 * a.slices;
+    a.seqs = a.n_seqs < a.places ? a.n_seqs : a.places;   // a sequence has a place at least
+    const uint64_t blocks = ((uint64_t)a.seqs * a.heads + 7) / 8 * 8 * a.slices;
     if (items > 0x7FFFFFFFull || blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
     hipLaunchKernelGGL((k_delta_chunk<DK>), dim3((uint32_t)items), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(256 * kScanGroups), 0, s, a);

@@ -7,7 +7,8 @@ Tolerances, fixed before the first run: the bounds that the oracle carries along
   roundings: below 2^-18 in all;
 * 2^-16 in calls on chunks of 64 tokens: sums of up to 64 such terms meet once more, 64 roundings of 2^-24 of terms with
   weights of at most 1;
-* bf16 output: 2^-8 of the value, and on chunks what the bf16 operands of the products that only outputs see are off by:
+* bf16 output: 2^-8 of the value, and on chunks what the rounded operands of the products that only outputs see are off by
+  (half precision is within what bf16 would be):
   2^-7 (|s| + the largest |v|) of a row's own sums, in place of which the relative 2-norm of all outputs is held to 3e-3,
   too (1.7e-3 is what rounding the exact outputs to bf16 gives).
 """
@@ -285,6 +286,41 @@ def test_calls_cut_into_several_launches(wal):
         assert (got - want).norm() <= 1e-6 * want.norm(), s
     again, state2 = c.call()
     assert torch.equal(again, out) and torch.equal(state2, state)
+
+
+def test_many_sequences_cut_into_several_launches(wal):
+    """A launch looks at the sequences that can have a place in it only."""
+    rng = np.random.default_rng(82)
+    new = [int(x) for x in rng.integers(0, 70, 160)] + [70]
+    c = Case(wal, new, kh=96, group=1, dk=128, dv=32, seed=83)
+    assert c.ws.numel() < (c.n // 64 + len(new)) * 96 * 50000 / 2   # three launches or more
+    out, state = c.call()
+    ref, ref_state = recurrence(c)
+    for s in range(len(new)):
+        rows = slice(int(c.starts[s]), int(c.starts[s + 1]))
+        assert (out[rows].double() - ref[rows]).norm() <= 3e-3 * ref[rows].norm(), s
+        got, want = state[c.slots[s]].double(), ref_state[c.slots[s]]
+        assert (got - want).norm() <= 1e-6 * want.norm(), s
+    others = [i for i in range(c.places) if i not in c.slots]
+    assert torch.equal(state[others], c.state0[others])
+
+
+@pytest.mark.parametrize("new", [[5, 6], [90, 70]])
+@pytest.mark.parametrize("what", ["q", "k"])
+def test_squares_past_the_range_are_not_finite(wal, new, what):
+    """A row of finite values whose squares add up past fp32 is lost with a sign of it, token by token and on chunks."""
+    c = Case(wal, new, kh=2, group=1, dk=64, dv=32, seed=43)
+    clean, clean_state = (t.clone() for t in c.call())
+    row = int(c.starts[1]) + new[1] // 2
+    getattr(c, what)[row, 64:128] = 3e18      # 64 times 9e36 is past 3.4e38
+    out, state = c.call()
+    end = row + 1 if what == "q" else int(c.starts[2])
+    assert (~torch.isfinite(out[row:end, 32:])).all()
+    lost = torch.zeros_like(out, dtype=torch.bool)
+    lost[row:end, 32:] = True
+    assert torch.equal(out[~lost], clean[~lost])
+    assert torch.isfinite(state[c.slots[1], 1]).any().item() == (what == "q")
+    assert torch.equal(state[c.slots[0]], clean_state[c.slots[0]])
 
 
 def test_calls_at_the_same_time(wal):
