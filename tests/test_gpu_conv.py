@@ -74,6 +74,8 @@ def test_many_rows_and_sequences(wal):
     rng = np.random.default_rng(9)
     check(wal, rng.integers(0, 9, 5000), 64, 4, tin="b", seed=3)          # two looks at the starts
     check(wal, [40000, 3, 2500], 264, 4, tin="f", seed=4)                 # long tiles
+    check(wal, [16000, 1, 2, 15, 0, 17, 3, 17100], 1024, 4, tin="b", seed=5)   # the longest
+    check(wal, [1, 2, 3, 1, 0, 2], 520, 4, tin="b", seed=6)               # a row each
 
 
 def test_rows_outside_the_sequences(wal):
