@@ -19,6 +19,7 @@ constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: wh
 struct Plan {
   bool step;                 // token by token, else on chunks
   uint32_t all, places;      // places of chunks, and those of one launch
+  uint32_t pitch;            // places from a head to the next: odd, since heads in step would else meet on few memory channels
   uint64_t carry, bytes;     // bytes of a carried state; of the workspace
 };
 
@@ -30,7 +31,8 @@ Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_
   p.all = n / kChunk + n_seqs;
   p.places = p.all <= most ? p.all : most ? (uint32_t)most : 1;
   p.carry = p.places < p.all ? 4ull * d->value_heads * d->key_dim * d->value_dim : 0;
-  p.bytes = p.places * place + 2 * p.carry;
+  p.pitch = p.places | 1;
+  p.bytes = p.pitch * place + 2 * p.carry;
   return p;
 }
 
@@ -117,10 +119,11 @@ extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ld
   const Plan p = plan_of(d, n_seqs, n, max_new);
   if (p.step) return delta_step(a, d->key_dim, stream);
   a.ws = static_cast<uint8_t*>(ws_dev);
-  a.key_ws = a.ws + (uint64_t)p.places * d->value_heads * kItemBytes;
+  a.key_ws = a.ws + (uint64_t)p.pitch * d->value_heads * kItemBytes;
   a.key_item = key_item_bytes(d->key_dim);
   a.places = p.places;
-  a.carry[0] = reinterpret_cast<float*>(a.ws + p.places * place_bytes(d->key_heads, d->value_heads, d->key_dim));
+  a.pitch = p.pitch;
+  a.carry[0] = reinterpret_cast<float*>(a.ws + p.pitch * place_bytes(d->key_heads, d->value_heads, d->key_dim));
   a.carry[1] = a.carry[0] + p.carry / 4;
   return delta_chunks(a, d->key_dim, p.all, stream);
 }

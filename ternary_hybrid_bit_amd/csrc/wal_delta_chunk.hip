@@ -49,7 +49,8 @@ __device__ __forceinline__ f16x8_t as_operand(u32x4_t w) { return __builtin_bit_
 
 __device__ __forceinline__ f32x4_t product(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// Eight values, times s, as N parts in half precision: s x = p[0] + p[1], each part one rounding.
+// Eight values, times s, as N parts in half precision: s x = p[0] + p[1], each part one rounding.  (A value's product and its
+// rounding in one instruction, v_fma_mix, are fewer instructions and slower: 141 us for 130 at 4096 tokens of 32 heads.)
 template <int N>
 __device__ __forceinline__ void split(f32x4_t x, f32x4_t y, f32x4_t sx, f32x4_t sy, u32x4_t (&p)[N]) {
   static_assert(N == 1 || N == 2, "two parts hold 22 bits");
@@ -135,10 +136,10 @@ __device__ __forceinline__ uint32_t seq_of_place(const Delta& a, uint32_t place,
 // What a launch's place holds of a value head and of a key head: a head's places side by side, since they are read one
 // after another.
 __device__ __forceinline__ uint8_t* item_of(const Delta& a, uint32_t local, uint32_t head) {
-  return a.ws + ((uint64_t)head * a.places + local) * kItemBytes;
+  return a.ws + ((uint64_t)head * a.pitch + local) * kItemBytes;
 }
 __device__ __forceinline__ uint8_t* key_item_of(const Delta& a, uint32_t local, uint32_t kh) {
-  return a.key_ws + ((uint64_t)kh * a.places + local) * a.key_item;
+  return a.key_ws + ((uint64_t)kh * a.pitch + local) * a.key_item;
 }
 
 // Place of a row's 16-byte piece in LDS: 16 neighbours that are read together, the rows of dealt(), and in the transposing
@@ -482,8 +483,14 @@ struct Scan {
     // or with 64 bytes, and rows 4 hf and 32 w further change no bits that the pieces' exchange looks at.
     const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c) ^ 64 * UH * half, tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3) ^ 64 * UH * half;
     f32x4_t ks[4];
+    const auto load_k = [&](const uint8_t* k, u32x4_t (&kw)[UH][4]) {
+#pragma unroll
+      for (int u = 0; u < UH; ++u)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) kw[u][t] = *reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK);
+    };
     // the state in parts, and its half of K S of chunk j
-    const auto take = [&](int32_t j, const uint8_t* k) {
+    const auto take = [&](int32_t j, const u32x4_t (&kw)[UH][4]) {
       float most = 0.f;
 #pragma unroll
       for (int u = 0; u < UH; ++u) most = largest(most, st[u][0], st[u][1]);
@@ -492,17 +499,15 @@ struct Scan {
       for (int t = 0; t < 4; ++t) ks[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < UH; ++u) {
-        u32x4_t part[2], kw[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) kw[t] = *reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK);
+        u32x4_t part[2];
         split(st[u][0], st[u][1], ss.up, part);
         sh.state[j & 1][group][UH * half + u][lane] = part[0];
 #pragma unroll
         for (int e = 1; e >= 0; --e)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) ks[t] = product(as_operand(kw[t]), as_operand(part[e]), ks[t]);
+          for (int t = 0; t < 4; ++t) ks[t] = product(as_operand(kw[u][t]), as_operand(part[e]), ks[t]);
       }
-      if (c == 0) sh.down[j & 1][group][half][n] = ss.down;
+      sh.down[j & 1][group][half][n] = ss.down;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         ks[t] *= ss.down;
@@ -511,7 +516,9 @@ struct Scan {
     };
     lds_barrier();
     uint32_t kb = (uint32_t)j0 % 3;
-    take(j0, sh.k[kb]);
+    u32x4_t kw[UH][4];
+    load_k(sh.k[kb], kw);
+    take(j0, kw);
     lds_barrier();
     for (int32_t j = j0; j < j1; ++j) {
       const uint8_t* k = sh.k[kb];
@@ -527,6 +534,20 @@ struct Scan {
         const f32x4_t both = ks[t] + sh.ks[j & 1][group][1 - half][t][lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[i], both[i], c1[i] * bf16_value((uint16_t)v[i]));
+      }
+      // read here, where nothing waits for them yet, for the products with K^T: four tokens of the lane's row of it each
+      union { s16x4_t half[2]; u32x4_t all; } kt[2][2 * UH];
+      f32x4_t c3[2][2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int t = 0; t < 2 * UH; ++t)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            kt[w][t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4_t*)(k + (tat ^ 64 * (t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) c3[w][hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf);
       }
       f32x4_t u[4];   // times 2^12 and the rows' scale
       Scale rs;
@@ -568,48 +589,33 @@ struct Scan {
           for (int i = 0; i < 4; ++i)
             if (16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i >= bad) u[t][i] = 0.f;
       }
-      if (half == 0 && c == 0) {
-        sh.bad[j & 1][group][n] = bad;
-        sh.udown[j & 1][group][n] = rs.down * 0x1p-12f;
-      }
       // S = decay S + K^T diag(e^(G_end - G)) u
-      u32x4_t up[2][2];
+      u32x4_t up[2][2], one[1];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        f32x4_t c3[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) c3[hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf);
-        split(u[2 * w], u[2 * w + 1], c3[0], c3[1], up[w]);
-        if (half == 0) {
-          u32x4_t one[1];
-          split(u[2 * w], u[2 * w + 1], 0x1p-12f, one);
-          sh.u[j & 1][group][w][lane] = one[0];
-        }
-      }
-      const float back = bad < kC ? NAN : rs.down * 0x1p-12f;
+      for (int w = 0; w < 2; ++w) split(u[2 * w], u[2 * w + 1], c3[w][0], c3[w][1], up[w]);
+      split(half ? u[2] : u[0], half ? u[3] : u[1], 0x1p-12f, one);
+      sh.u[j & 1][group][half][lane] = one[0];
+      // every lane that holds a value writes it: a branch here would keep what is around it apart
+      sh.bad[j & 1][group][n] = bad;
+      sh.udown[j & 1][group][n] = rs.down * 0x1p-12f;
+      float back = bad < kC ? NAN : rs.down * 0x1p-12f;
+      asm("" : "+v"(back));   // chosen once, not after each of the sums below
       f32x4_t add[2 * UH];
 #pragma unroll
       for (int t = 0; t < 2 * UH; ++t) add[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      kb = kb == 2 ? 0 : kb + 1;
+      load_k(sh.k[kb], kw);
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        union { s16x4_t half[2]; u32x4_t all; } kt[2 * UH];   // four tokens of the lane's row of K^T each
-#pragma unroll
-        for (int t = 0; t < 2 * UH; ++t)
-#pragma unroll
-          for (int z = 0; z < 2; ++z)
-            kt[t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t*)(k + (tat ^ 64 * (t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int e = 1; e >= 0; --e)
 #pragma unroll
-          for (int t = 0; t < 2 * UH; ++t) add[t] = product(as_operand(kt[t].all), as_operand(up[w][e]), add[t]);
-      }
+          for (int t = 0; t < 2 * UH; ++t) add[t] = product(as_operand(kt[w][t].all), as_operand(up[w][e]), add[t]);
 #pragma unroll
       for (int t = 0; t < 2 * UH; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) st[t / 2][t % 2][i] = fmaf(add[t][i], back, decay * st[t / 2][t % 2][i]);
-      kb = kb == 2 ? 0 : kb + 1;
-      take(j + 1, sh.k[kb]);   // behind the last chunk: of some chunk's K, and not read
+      take(j + 1, kw);   // behind the last chunk: of some chunk's K, and not read
       lds_barrier();
     }
     if (after)
@@ -744,14 +750,15 @@ __global__ __launch_bounds__(256 * kScanGroups, 1) void k_delta_scan(Delta a) {
   __shared__ typename Scan<DK>::Shared sh;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, c = lane >> 4;
   const uint32_t group = wave % kScanGroups;
-  // The workgroups of a head sit on one chiplet, so that its cache serves what they share: blocks go to the eight
-  // chiplets in turn.
-  const uint32_t x = blockIdx.x % 8, g = blockIdx.x / 8, pair = g / a.slices * 8 + x;
+  // The workgroups of a head sit on one chiplet, or those of all heads of a key head, so that its cache serves what they
+  // share: blocks go to the eight chiplets in turn.
+  const uint32_t per = a.together * a.slices, g = blockIdx.x / 8, slice = g % per % a.slices;
+  const uint32_t pair = (g / per * 8 + blockIdx.x % 8) * a.together + g % per / a.slices;
   if (pair >= a.seqs * a.heads) return;
   // from the sequence of the launch's first place on
   const uint32_t s = (a.place0 ? seq_of_place(a, a.place0, lane) : 0) + pair / a.heads, h = pair % a.heads;
   if (s >= a.n_seqs) return;
-  const uint32_t col = kSlice * (g % a.slices) + 16 * group + n;
+  const uint32_t col = kSlice * slice + 16 * group + n;
   const Seq q = delta_seq(a, s);
   const uint32_t base = (uint32_t)q.first / kC + s;
   const int32_t chunks = (q.rows + kC - 1) / kC;
@@ -775,7 +782,12 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
     a.carry[1] = carry[(i + 1) % 2];
     const uint64_t items = (uint64_t)(all - first < a.places ? all - first : a.places) * (a.heads / a.group) * ((a.group + kPair - 1) / kPair);
     a.seqs = a.n_seqs < a.places ? a.n_seqs : a.places;   // a sequence has a place at least
-    const uint64_t blocks = ((uint64_t)a.seqs * a.heads + 7) / 8 * 8 * a.slices;
+    // heads of a key head together where no chiplet's 32 compute units get more workgroups than otherwise, or all at once (5
+    // sequences of 300 tokens, 16 heads of 128 on 8 38.7 us, each head by itself 44.6; one of 4096 tokens, 32 heads 130 and
+    // 131; one of 8192 tokens, 48 heads 321 and 317)
+    const uint64_t units = (uint64_t)a.seqs * (a.heads / a.group), each = (units + 7) / 8 * a.group * a.slices;
+    a.together = units % 8 == 0 || each <= 32 ? a.group : 1;
+    const uint64_t blocks = a.together > 1 ? each * 8 : ((uint64_t)a.seqs * a.heads + 7) / 8 * 8 * a.slices;
     if (items > 0x7FFFFFFFull || blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
     hipLaunchKernelGGL((k_delta_chunk<DK>), dim3((uint32_t)items), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(256 * kScanGroups), 0, s, a);
