@@ -10,7 +10,7 @@
 // four columns in registers, and sums over rows meet by lane exchange in a
 // wavefront and once in LDS, summed in one order by every wavefront.
 //
-// Measured (16 key and 48 value heads of 128): 64 sequences 85 us, 4.8 TB/s (a copy reaches 5.2); one sequence 5.8 us.
+// Measured (16 key and 48 value heads of 128): 64 sequences 85 us, 4.8 TB/s (a copy reaches 5.0); one sequence 5.8 us.
 #include <hip/hip_runtime.h>
 
 #include "wal_delta.h"

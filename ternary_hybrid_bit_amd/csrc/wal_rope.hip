@@ -20,9 +20,13 @@
 // sums of sine and cosine in fp32 (next terms below 2e-9).  In fp32 the
 // product itself would be off by 0.06 rad at position 10^6.
 //
-// Measured: 16001 tokens of 40 heads of 128 rotated bf16 to bf16 66 us (5.0 TB/s; a copy
-// reaches 5.2), 8191 tokens written as int8 with their q rows 52 us, 100003 tokens
-// read back from int8 123 us (5.0 TB/s); one token of 32 heads 2.3 us.
+// A norm adds the sum of squares to the same pass: the lanes of a head sit side by side, a power of two of them (idle
+// ones with zeros), and add up by lane exchange; the weights lie in LDS.
+//
+// Measured: 16001 tokens of 40 heads of 128 rotated bf16 to bf16 70 us in a graph (4.7 TB/s; a copy
+// reaches 5.0), 8191 tokens written as int8 with their q rows 57 us (with the norms 60), 100003 tokens
+// read back from int8 123 us; one token of 32 heads 3.1 us.  Normed: 8192 tokens of 48 heads of 128 with an fp32 gate
+// 81 us (5.0 TB/s), 8001 tokens of 20 heads of 256 rotated, fp32 to bf16, 57 us; one token with a gate 3.7 us.
 #include <hip/hip_runtime.h>
 
 #include "wal_args.h"
@@ -369,8 +373,6 @@ void set_rotary(RopeKv& a, const wal_rotary* r) {
   a.magnitude = r->magnitude;
 }
 
-// Tokens of a workgroup and the slice of their units: whole tokens, about four units a thread
-// when there are many, a unit a thread over more workgroups when there are few.
 template <int MODE>
 void launch(const RopeKv& a, bool bf16_in, dim3 grid, hipStream_t s) {
   if (bf16_in)
@@ -379,6 +381,8 @@ void launch(const RopeKv& a, bool bf16_in, dim3 grid, hipStream_t s) {
     hipLaunchKernelGGL((k_rope_kv<false, MODE>), grid, dim3(kRopeThreads), 0, s, a);
 }
 
+// Tokens of a workgroup and the slice of their units: whole tokens, about four units a thread
+// when there are many, a unit a thread over more workgroups when there are few.
 int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
   const uint32_t by_lds = a.rot ? kRopeLdsPairs / (a.rot / 2) : 64;
   a.tokens = 1;
@@ -388,7 +392,8 @@ int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
     if (a.slice > a.units) a.slice = a.units;
   } else {
     while (a.tokens < by_lds && a.tokens * a.units < 4 * kRopeThreads) ++a.tokens;
-    // fewer, down to two units a thread, where they fill the threads' last round better
+    // fewer, down to two units a thread, where they fill the threads' last round better (int8 write of 8191 tokens, 32 and 8
+    // heads of 128 59.5 -> 57 us, normed 62 -> 60; 16001 tokens of 40 heads as before, 70)
     const auto rounds = [&](uint32_t tokens) { return (tokens * a.units + kRopeThreads - 1) / kRopeThreads; };
     for (uint32_t t = a.tokens; t && t * a.units >= 2 * kRopeThreads; --t)
       if ((uint64_t)t * rounds(a.tokens) > (uint64_t)a.tokens * rounds(t)) a.tokens = t;
