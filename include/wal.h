@@ -775,8 +775,8 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  *   max_new  bounds the sequences' rows: rows past it are neither computed nor kept
  *   ws       wal_delta_workspace_size bytes, 256-byte aligned (NULL when that is 0),
  *            contents arbitrary.  Calls that may overlap in time need their own
- * States, norms, gates and sums are fp32; a call whose max_new is large enough works on
- * chunks of 64 tokens, where products take values in 22 bits for the state and 11 for the outputs.
+ * States, norms, gates and sums are fp32; sequences that bring many rows are taken in chunks
+ * of 64 tokens, where products take values in 22 bits for the state and 11 for the outputs.
  * beta |k|^2 (of k as used) is meant to be from 0 to 2, where no token enlarges a state: past that
  * states grow from token to token, and where calls work on chunks they are less exact, from
  * about 16 on infinities or NaN.  From a token on whose q, k, v, alpha or beta holds an infinity

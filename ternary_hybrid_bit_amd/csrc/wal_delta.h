@@ -34,6 +34,7 @@ struct Delta {
   uint32_t n_seqs, n, max_new, n_slots;
   uint32_t heads, group, value_dim, slices;   // value heads, those that share a key head
   float eps, scale;              // eps 0: q and k as they are
+  int32_t few;                   // a call in both forms: sequences of at most so many rows go token by token, others on chunks
   // calls on chunks: sequence s has the places from starts[s] / 64 + s on, one for each chunk; a launch takes `places`
   // of them from place0, and a sequence that goes on leaves its state in carry[1] and finds it in carry[0]
   uint8_t* ws;                   // of value heads
@@ -43,7 +44,7 @@ struct Delta {
   uint32_t seqs, together;       // sequences that a launch of the scan looks at, heads that it puts on one chiplet
 };
 
-// Launches (wal_status).
+// Launches (wal_status).  Token by token: of sequences with at most a.few rows; on chunks: of those with more.
 int delta_step(const Delta& a, uint32_t key_dim, void* stream);
 // In as many launches as a.places take of the call's `all` places.
 int delta_chunks(Delta& a, uint32_t key_dim, uint32_t all, void* stream);

@@ -17,7 +17,8 @@ constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: wh
 
 // How a call is cut.
 struct Plan {
-  bool step;                 // token by token, else on chunks
+  bool step, chunks;         // token by token, on chunks, or each sequence in one of both
+  uint32_t few;              // rows of a sequence up to which it goes token by token
   uint32_t all, places;      // places of chunks, and those of one launch
   uint32_t pitch;            // places from a head to the next: odd, since heads in step would else meet on few memory channels
   uint64_t carry, bytes;     // bytes of a carried state; of the workspace
@@ -25,8 +26,14 @@ struct Plan {
 
 Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new) {
   Plan p{};
-  p.step = max_new <= ((uint64_t)n_seqs * d->value_heads >= kMany ? kFewRowsOfMany : kFewRows);
-  if (p.step || !n || !n_seqs) return p;
+  p.few = (uint64_t)n_seqs * d->value_heads >= kMany ? kFewRowsOfMany : kFewRows;
+  p.chunks = n && n_seqs && max_new > p.few;
+  // Both, if all but one sequence bring few rows on average: a prompt among sequences that bring a token each (48 heads of 128, 63
+  // of one token and one of 500 124 us, all on chunks 302; 15 and one of 1000 75 and 110; 5 of 300 tokens in a call whose
+  // max_new does not tell, 16 heads, 42.5 and 41).
+  p.step = !p.chunks || (n_seqs > 1 && n <= max_new + (n_seqs - 1ull) * p.few);
+  if (!p.chunks) return p;
+  if (!p.step) p.few = 0;
   const uint64_t place = place_bytes(d->key_heads, d->value_heads, d->key_dim), most = kMaxItems / place;
   p.all = n / kChunk + n_seqs;
   p.places = p.all <= most ? p.all : most ? (uint32_t)most : 1;
@@ -117,7 +124,9 @@ extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ld
   a.eps = d->norm_eps;
   a.scale = d->scale;
   const Plan p = plan_of(d, n_seqs, n, max_new);
-  if (p.step) return delta_step(a, d->key_dim, stream);
+  a.few = (int32_t)p.few;
+  if (p.step && (st = delta_step(a, d->key_dim, stream))) return st;
+  if (!p.chunks) return WAL_OK;
   a.ws = static_cast<uint8_t*>(ws_dev);
   a.key_ws = a.ws + (uint64_t)p.pitch * d->value_heads * kItemBytes;
   a.key_item = key_item_bytes(d->key_dim);

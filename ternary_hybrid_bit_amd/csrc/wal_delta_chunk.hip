@@ -206,7 +206,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
   const uint32_t s = seq_of_place(a, a.place0 + local, lane);
   const Seq q = delta_seq(a, s);
   const int32_t row0 = kC * (int32_t)(a.place0 + local - ((uint32_t)q.first / kC + s));   // of the sequence
-  if (row0 < 0 || row0 >= q.rows) return;
+  if (row0 < 0 || row0 >= q.rows || q.rows <= a.few) return;
   const int32_t count = min(q.rows - row0, kC);
   const uint64_t from = (uint64_t)(q.first + row0);
 
@@ -770,7 +770,7 @@ __global__ __launch_bounds__(256 * kScanGroups, 1) void k_delta_scan(Delta a) {
   const uint32_t base = (uint32_t)q.first / kC + s;
   const int32_t chunks = (q.rows + kC - 1) / kC;
   const int32_t j0 = max(0, (int32_t)a.place0 - (int32_t)base), j1 = min(chunks, (int32_t)(a.place0 + a.places) - (int32_t)base);
-  if (j0 >= j1) return;
+  if (j0 >= j1 || q.rows <= a.few) return;
   const int64_t slot = kept_at(a, s);
   const uint64_t head_at = ((uint64_t)h * DK + 8 * c) * a.value_dim + col;
   float* kept = slot < 0 ? nullptr : a.state + (uint64_t)slot * a.heads * DK * a.value_dim + head_at;

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(Delta a) {
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = threadIdx.x % kCols, r = threadIdx.x / kCols;
   const uint32_t slices = a.value_dim / NV, slice = blockIdx.x % slices, rest = blockIdx.x / slices, h = rest % a.heads, s = rest / a.heads;
   const Seq seq = delta_seq(a, s);
-  if (!seq.rows) return;
+  if (!seq.rows || seq.rows > a.few) return;
   const int64_t slot = kept_at(a, s);
   const uint32_t kh = h / a.group, col = NV * slice + 4 * c;
   float* state = a.state + ((uint64_t)max(slot, (int64_t)0) * a.heads + h) * DK * a.value_dim + (uint64_t)(J * r) * a.value_dim + col;

@@ -137,6 +137,32 @@ def test_prompts(wal, new, kw):
     Case(wal, new, seed=len(new) + 50, **kw).check()
 
 
+@pytest.mark.parametrize("new,kw", [
+    ([1, 1, 300, 1, 8, 0, 1], dict(dk=128, dv=64)), ([200] + [1] * 40, dict(dk=128)), ([8, 9, 1], {}), ([1, 130], dict(keep=False)),
+    ([1] * 70 + [24, 25, 100], dict(kh=2, group=2)), ([1, 2, 90, 1], dict(max_new=70, raw=False)), ([1, 70, 2], dict(before=6, behind=5)),
+    ([1, 1, 80], dict(slots=[9, 1, 0], places=3)), ([30, 0, 0, 0, 0, 20], {}),
+])
+def test_prompts_among_single_tokens(wal, new, kw):
+    """Each sequence of such a call goes in its own form."""
+    c = Case(wal, new, seed=len(new) + 90, **kw)
+    if "max_new" not in kw:
+        c.check()
+    else:   # what max_new cuts off is left
+        out, _ = c.call()
+        ref, *_ = c.oracle(0.0)
+        for s, (a, k) in enumerate(zip(c.starts, new)):
+            rows = slice(a, a + min(k, c.max_new))
+            got, want = host(out[rows]).reshape(-1, c.h, c.dv), ref[rows]
+            assert np.linalg.norm(got - want) <= 3e-3 * np.linalg.norm(want)
+            assert (out[a + c.max_new:a + k] == -7).all()
+
+
+@pytest.mark.parametrize("kh,group,dv", [(3, 4, 256), (3, 2, 32), (8, 2, 64), (1, 7, 256)])
+def test_heads_side_by_side(wal, kh, group, dv):
+    """Heads that share a key head on one chiplet, and by themselves: numbers of workgroups that leave chiplets uneven."""
+    Case(wal, [70, 100, 90], kh=kh, group=group, dv=dv, seed=kh + dv).check()
+
+
 @pytest.mark.parametrize("dk,dv", [(64, 32), (128, 128)])
 def test_chunks_and_tokens_continue_each_other(wal, dk, dv):
     """A sequence taken in pieces of any size, through the state, stays with the oracle's bounds of the whole."""
