@@ -23,10 +23,10 @@
 // A norm adds the sum of squares to the same pass: the lanes of a head sit side by side, a power of two of them (idle
 // ones with zeros), and add up by lane exchange; the weights lie in LDS.
 //
-// Measured: 16001 tokens of 40 heads of 128 rotated bf16 to bf16 70 us in a graph (4.7 TB/s; a copy
-// reaches 5.0), 8191 tokens written as int8 with their q rows 57 us (with the norms 60), 100003 tokens
+// Measured in graphs: 16001 tokens of 40 heads of 128 rotated bf16 to bf16 64 us (5.1 TB/s; a copy
+// reaches 5.0), 8191 tokens written as int8 with their q rows 54 us (with the norms 55), 100003 tokens
 // read back from int8 123 us; one token of 32 heads 3.1 us.  Normed: 8192 tokens of 48 heads of 128 with an fp32 gate
-// 81 us (5.0 TB/s), 8001 tokens of 20 heads of 256 rotated, fp32 to bf16, 57 us; one token with a gate 3.7 us.
+// 80 us, 8001 tokens of 20 heads of 256 rotated, fp32 to bf16, 50 us (4.9 TB/s); one token with a gate 3.7 us.
 #include <hip/hip_runtime.h>
 
 #include "wal_args.h"
@@ -381,8 +381,11 @@ void launch(const RopeKv& a, bool bf16_in, dim3 grid, hipStream_t s) {
     hipLaunchKernelGGL((k_rope_kv<false, MODE>), grid, dim3(kRopeThreads), 0, s, a);
 }
 
-// Tokens of a workgroup and the slice of their units: whole tokens, about four units a thread
-// when there are many, a unit a thread over more workgroups when there are few.
+// Tokens of a workgroup and the slice of their units: as many whole tokens as one unit a thread takes, at least one; a unit a
+// thread over more workgroups when there are few.  More units a thread are slower although they share sines and weights
+// (8001 tokens of 320 units, normed and rotated fp32, 1, 2, 4 and 8 tokens 50, 53, 58 and 54 us; 16001 of 320, rotated bf16,
+// 64, 66, 69 and 73; 8191 written as int8, 384 units, 54, 56, 59 and 61), and fewer are, too (30000 tokens of 32 units,
+// normed, 1, 4, 8 and 16 tokens 35, 16, 15.5 and 15 us).
 int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
   const uint32_t by_lds = a.rot ? kRopeLdsPairs / (a.rot / 2) : 64;
   a.tokens = 1;
@@ -391,12 +394,9 @@ int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
     a.slice = kRopeThreads / a.lanes * a.lanes;
     if (a.slice > a.units) a.slice = a.units;
   } else {
-    while (a.tokens < by_lds && a.tokens * a.units < 4 * kRopeThreads) ++a.tokens;
-    // fewer, down to two units a thread, where they fill the threads' last round better (int8 write of 8191 tokens, 32 and 8
-    // heads of 128 59.5 -> 57 us, normed 62 -> 60; 16001 tokens of 40 heads as before, 70)
-    const auto rounds = [&](uint32_t tokens) { return (tokens * a.units + kRopeThreads - 1) / kRopeThreads; };
-    for (uint32_t t = a.tokens; t && t * a.units >= 2 * kRopeThreads; --t)
-      if ((uint64_t)t * rounds(a.tokens) > (uint64_t)a.tokens * rounds(t)) a.tokens = t;
+    a.tokens = kRopeThreads / a.units;
+    if (a.tokens > by_lds) a.tokens = by_lds;
+    if (!a.tokens) a.tokens = 1;
   }
   const dim3 grid((a.n + a.tokens - 1) / a.tokens, (a.units + a.slice - 1) / a.slice);
   if (mode == kAsIs) launch<kAsIs>(a, bf16_in, grid, s);
