@@ -776,10 +776,11 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  *   ws       wal_delta_workspace_size bytes, 256-byte aligned (NULL when that is 0),
  *            contents arbitrary.  Calls that may overlap in time need their own
  * States, norms, gates and sums are fp32; sequences that bring many rows are taken in chunks
- * of 64 tokens, where products take values in 22 bits for the state and 11 for the outputs.
+ * of 64 tokens, where products take values in 24 bits for the state and 16 for the outputs, each
+ * value for itself: a large one takes nothing from those beside it.
  * beta |k|^2 (of k as used) is meant to be from 0 to 2, where no token enlarges a state: past that
- * states grow from token to token, and where calls work on chunks they are less exact, from
- * about 16 on infinities or NaN.  From a token on whose q, k, v, alpha or beta holds an infinity
+ * states grow from token to token, and where calls work on chunks they are less exact, and a
+ * column that grows past fp32's range is not finite from its chunk's first token on.  From a token on whose q, k, v, alpha or beta holds an infinity
  * or NaN, what depends on it is an infinity or NaN.  The result does not depend on timing.
  * Errors: ARG, SHAPE, ALIGN, BUFFER, DEVICE. */
 typedef struct {

@@ -10,9 +10,10 @@ namespace wal {
 constexpr uint32_t kSlice = 32;   // columns of a state that a workgroup takes
 constexpr int kChunk = 64;        // tokens that meet in products
 // What the scan over chunks reads, by the place of a chunk: of a key head K by rows and Q as operands, of a value head
-// T in two parts and P as operands and the factors of the rows (all but the factors in half precision).
+// T in three parts and P in two as operands and the factors of the rows (all but the factors in bf16).
 constexpr uint32_t kOperand = 1024, kTriangle = 6 * kOperand;   // 16 bytes a lane; a 64 x 64 lower triangle
-constexpr uint32_t kPAt = 2 * kTriangle, kVecAt = kPAt + kTriangle, kItemBytes = kVecAt + 6 * 256;
+constexpr uint32_t kTParts = 3, kPParts = 2;
+constexpr uint32_t kPAt = kTParts * kTriangle, kVecAt = kPAt + kPParts * kTriangle, kItemBytes = kVecAt + 6 * 256;
 constexpr uint32_t key_item_bytes(uint32_t key_dim) { return 2 * kChunk * 2 * key_dim; }
 constexpr uint64_t place_bytes(uint32_t key_heads, uint32_t heads, uint32_t key_dim) {
   return (uint64_t)key_heads * key_item_bytes(key_dim) + (uint64_t)heads * kItemBytes;

@@ -7,16 +7,18 @@
 //     S = e^G_end S0 + K^T diag(e^(G_end - G)) u
 // so that tokens meet in products on the matrix cores and only states go from chunk
 // to chunk.  k_delta_chunk makes T, P and the factors of the rows of every chunk and head, all of
-// them at once; k_delta_scan walks the chunks of a sequence and head, a wavefront
-// keeping 16 columns of the state in registers: everything that a column of the
-// values meets belongs to that column alone.
+// them at once; k_delta_scan walks the chunks of a sequence and head, two wavefronts
+// keeping 16 columns of the state in registers, half of the rows each: everything that a
+// column of the values meets belongs to that column alone.
 //
-// Numbers.  What an update of a state sees is as exact as fp32: values enter its products as two parts in half
-// precision, x = hi + lo, 22 bits; one part does for what only outputs in bf16 see.  Half precision has those bits but
-// little range, so every operand is scaled by a power of two that some factor in fp32 undoes: rows of K and Q (bf16, so
-// one part holds them) to lengths of 2^12, columns of the state and of b V - .. by their largest values, T and P, whose
-// values are at most 2 as long as b |k|^2 is, by 2^12.  (Three parts in bf16, which needs no scales, took twice the
-// products: the scan of 8192 tokens 441 us for 338.)  Keys and queries are taken as unit vectors and lengths, the lengths into the
+// Numbers.  Values enter the products as sums of parts in bf16, which has fp32's range: what an update of a state sees (the
+// state, T, the rows b V - .., u) as three, 24 bits, and what only outputs in bf16 see (P, u and the state there) as two, 16
+// bits; K and Q hold bf16 to begin with.  So a value keeps its bits whatever lies beside it: a row a billion times its
+// neighbours takes nothing from the rows before it, nor from those behind a token that forgets it.  Two parts in half precision
+// hold 22 bits and lose them as soon as rows of a column that share a scale differ by 2^9 (that scan took 271 us for 311 at
+// 8192 tokens of 48 heads); outputs of one part in half precision were off by up to 3.2e-3 where keys are alike and stored rows
+// cancel, for the 1.66e-3 of their rounding to bf16.  Rows of K and Q are brought to
+// lengths of 1 to 2 by powers of two.  Keys and queries are taken as unit vectors and lengths, the lengths into the
 // factors of the rows.  G is added up in 64 bits, because e^(G_i - G_j) has to be exact also after a token that
 // forgets everything.  Exponents are never above 0.
 //
@@ -26,11 +28,11 @@
 // finite takes the rows that are not out of the product and puts NaN where they belong.
 //
 // What bounds it.  k_delta_chunk: instructions and latencies (dropping all its stores of T took 3 us of 77).  k_delta_scan: the
-// chain of a chunk, K S, the sum of its halves, T, K^T u, about 4400 cycles of which the matrix cores take 800 and vector
-// instructions 1600; what else there is are their latencies and those of LDS.  With 192 workgroups of 16 + 16 columns the clock
-// falls besides (1.8 GHz at the end of 8192 tokens, 2.3 with 128).
-// Measured: 8192 tokens, 48 heads of 128 on 16 320 us, 77 of them k_delta_chunk; 32 heads 271; 4096 tokens, 32 heads 130;
-// 9 sequences up to 1111, 8 heads of 64 x 96 on 4, 43 with the call from Python.
+// chain of a chunk, K S, the sum of its halves, T, K^T u, about 4800 cycles of which the matrix cores take 1350;
+// what else there is are the parts' roundings and latencies, of LDS too.  With 192 workgroups of 16 + 16 columns the clock
+// falls besides.
+// Measured: 8192 tokens, 48 heads of 128 on 16 365 us, 86 of them k_delta_chunk; 32 heads 324; 4096 tokens, 32 heads 169;
+// 9 sequences up to 1111, 8 heads of 64 x 96 on 4, 49 with the call from Python.
 #include <hip/hip_runtime.h>
 
 #include "wal_delta.h"
@@ -41,10 +43,11 @@ constexpr int kC = kChunk;
 constexpr uint32_t kLd = kC + 4;       // of T in LDS: four 16 x 16 blocks of the diagonal on different banks
 constexpr uint32_t kBlocks = kTriangle / kOperand;   // (32-row block, half, 32-column block) of a lower triangle
 constexpr int kPair = 2;               // value heads of a workgroup of k_delta_chunk
+// The rows of u are taken times 2^-8: T's values are at most 2 as long as b |k|^2 is, so that 64 of them with a row at the end
+// of fp32's range stay inside it.
+constexpr float kRow = 0x1p-8f, kRowBack = 0x1p8f;
 constexpr float kForget = -1000.f;     // logarithms of decays below this one are it: e^-1000 is 0
 
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
@@ -52,48 +55,36 @@ typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 // halves make the eight rows 8 c .. of a B operand.
 __device__ __forceinline__ uint32_t dealt(uint32_t u, uint32_t h, uint32_t m) { return 32 * u + 8 * (m >> 2) + 4 * h + (m & 3); }
 
-__device__ __forceinline__ f16x8_t as_operand(u32x4_t w) { return __builtin_bit_cast(f16x8_t, w); }
+__device__ __forceinline__ f32x4_t product(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
 
-__device__ __forceinline__ f32x4_t product(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-
-// Eight values, times s, as N parts in half precision: s x = p[0] + p[1], each part one rounding.  (A value's product and its
-// rounding in one instruction, v_fma_mix, are fewer instructions and slower: 141 us for 130 at 4096 tokens of 32 heads.)
+// Eight values as the sum of N parts in bf16, each the nearest to what the ones before leave: 8 bits more apiece.
 template <int N>
-__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, f32x4_t sx, f32x4_t sy, u32x4_t (&p)[N]) {
-  static_assert(N == 1 || N == 2, "two parts hold 22 bits");
+__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, u32x4_t (&p)[N]) {
+  static_assert(N >= 1 && N <= 3, "three parts hold what fp32 does");
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float r0 = i < 2 ? x[2 * i] : y[2 * i - 4], r1 = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
-    const float s0 = i < 2 ? sx[2 * i] : sy[2 * i - 4], s1 = i < 2 ? sx[2 * i + 1] : sy[2 * i - 3];
-    uint32_t w = __builtin_bit_cast(uint32_t, (f16x2_t{(_Float16)(r0 * s0), (_Float16)(r1 * s1)}));
-    if constexpr (N > 1) asm("" : "+v"(w));   // one value: what lo completes is what was stored, however it was rounded
-    p[0][i] = w;
-    if constexpr (N > 1) {
-      const f16x2_t hi = __builtin_bit_cast(f16x2_t, w);
-      const f16x2_t lo = {(_Float16)fmaf(r0, s0, -(float)hi[0]), (_Float16)fmaf(r1, s1, -(float)hi[1])};
-      p[1][i] = __builtin_bit_cast(uint32_t, lo);
+    float r0 = i < 2 ? x[2 * i] : y[2 * i - 4], r1 = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const uint32_t w = __builtin_bit_cast(uint32_t, (bf16x2_t{(__bf16)r0, (__bf16)r1}));
+      p[e][i] = w;
+      if (e + 1 < N) {
+        r0 -= __uint_as_float(w << 16);
+        r1 -= __uint_as_float(w & 0xFFFF0000u);
+      }
     }
   }
 }
-template <int N>
-__device__ __forceinline__ void split(f32x4_t x, f32x4_t y, float s, u32x4_t (&p)[N]) {
-  const f32x4_t t = {s, s, s, s};
-  split(x, y, t, t, p);
-}
 
-// 2^(to - e) for values below 2^(e + 1), and 2^(e - to); e is at least -107.
+// 2^-e and 2^e of a row's length, rounded down to 2^e, by its sum of squares; e is at least -107.
 struct Scale {
   float up, down;
 };
-__device__ __forceinline__ Scale scale_to(float most, int to) {
-  const uint32_t e = max(__float_as_uint(most) >> 23 & 0xFFu, 20u);
-  return Scale{__uint_as_float((254u + to - e) << 23), __uint_as_float((e - to) << 23)};
-}
-
-// For a row by its sum of squares: 2^12 over its length to within a factor of two.
 __device__ __forceinline__ Scale row_scale(float squares) {
-  const uint32_t e = ((__float_as_uint(squares) >> 23 & 0xFFu) + 127u) >> 1;   // of the length, rounded down
-  return scale_to(__uint_as_float(e << 23), 12);
+  const uint32_t e = max(((__float_as_uint(squares) >> 23 & 0xFFu) + 127u) >> 1, 20u);
+  return Scale{__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};
 }
 
 // The sum over 8 or 16 lanes side by side, in each of them.
@@ -108,24 +99,6 @@ __device__ __forceinline__ float lanes_sum(float x) {
 
 // 2^(x - y) of sums kept as high and low halves, exact to fp32 however long they are.
 __device__ __forceinline__ float power(float2 x, float2 y) { return __builtin_amdgcn_exp2f((x.x - y.x) + (x.y - y.y)); }
-
-// The largest magnitude of x and eight values; a NaN is passed over.  (Written out: fmaxf() would make each value a
-// number first.)
-__device__ __forceinline__ float largest(float x, f32x4_t y, f32x4_t z) {
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(x) : "v"(y[i]), "v"(y[i + 1]));
-    asm("v_max3_f32 %0, |%1|, |%2|, %0" : "+v"(x) : "v"(z[i]), "v"(z[i + 1]));
-  }
-  return x;
-}
-// The largest of the four lanes that hold a column.
-__device__ __forceinline__ float column_max(float x) {
-  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
 
 // The sequence of a chunk's place: sequence s has those from starts[s] / 64 + s on.
 __device__ __forceinline__ uint32_t seq_of_place(const Delta& a, uint32_t place, uint32_t lane) {
@@ -258,8 +231,9 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       qq[r] = y;
     }
     u32x4_t kw[1], qw[1];
-    split(k4[0], k4[1], row_scale(x).up, kw);
-    split(q4[0], q4[1], row_scale(y).up, qw);
+    const float ks2 = row_scale(x).up, qs2 = row_scale(y).up;   // powers of two: bf16 holds the rows as before
+    split(k4[0] * ks2, k4[1] * ks2, kw);
+    split(q4[0] * qs2, q4[1] * qs2, qw);
     *reinterpret_cast<u32x4_t*>(ks + row_piece<DK>(r, piece)) = kw[0];
     *reinterpret_cast<u32x4_t*>(qs + row_piece<DK>(r, piece)) = qw[0];
     if (pair == 0) {
@@ -283,8 +257,8 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     if (x < (int)tiles)
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u)
-        ak[x] = product(as_operand(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(16 * it + n, 4 * u + c))),
-                        as_operand(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(16 * jt + n, 4 * u + c))), ak[x]);
+        ak[x] = product(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(16 * it + n, 4 * u + c)),
+                        *reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(16 * jt + n, 4 * u + c)), ak[x]);
   }
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
@@ -295,8 +269,8 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
       if (x < (int)ops)
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u)
-          pk[x][z] = product(as_operand(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(dealt(sb, z, n), 4 * u + c))),
-                             as_operand(*reinterpret_cast<const u32x4_t*>(qs + row_piece<DK>(dealt(w, hf, n), 4 * u + c))), pk[x][z]);
+          pk[x][z] = product(*reinterpret_cast<const u32x4_t*>(ks + row_piece<DK>(dealt(sb, z, n), 4 * u + c)),
+                             *reinterpret_cast<const u32x4_t*>(qs + row_piece<DK>(dealt(w, hf, n), 4 * u + c)), pk[x][z]);
     }
   }
   if (wave < heads) {
@@ -312,8 +286,8 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
     const float lost = lane >= f ? NAN : 0.f, gone = any ? NAN : 0.f;
     const float decay = power(g, none), len = kn * to_k;
     float* vec = reinterpret_cast<float*>(item_of(a, local, h0 + wave) + kVecAt);
-    vec[lane] = beta * len + lost;
-    vec[kC + lane] = beta * len * len * decay * uk + lost;
+    vec[lane] = kRow * beta * len + lost;
+    vec[kC + lane] = kRow * beta * len * len * decay * uk + lost;
     vec[2 * kC + lane] = power(end, g) * uk + gone;
     vec[4 * kC + lane] = decay * uq;
     vec[5 * kC + lane] = qn * to_q * a.scale;
@@ -368,9 +342,11 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
           y[z][i] = col + i <= row ? uq * uk[i] * power(gr, gc) * pk[x][z][i] : 0.f;
         }
       }
-      u32x4_t p[1];
-      split(y[0], y[1], 4096.f, p);
-      *reinterpret_cast<u32x4_t*>(item_of(a, local, h0 + b) + kPAt + o * kOperand + 16 * lane) = p[0];
+      u32x4_t p[kPParts];
+      split(y[0], y[1], p);
+#pragma unroll
+      for (int e = 0; e < (int)kPParts; ++e)
+        *reinterpret_cast<u32x4_t*>(item_of(a, local, h0 + b) + kPAt + e * kTriangle + o * kOperand + 16 * lane) = p[e];
     }
   }
   lds_barrier();
@@ -422,11 +398,11 @@ __global__ __launch_bounds__(256) void k_delta_chunk(Delta a) {
   for (uint32_t i = tid; i < heads * kBlocks * 64; i += 256) {
     const uint32_t b = i / (kBlocks * 64), e = i - b * (kBlocks * 64), o = e >> 6, l = e & 63;
     const uint32_t row = dealt(o > 1, o & 1, l & 15), col = 32 * (o > 3) + 8 * (l >> 4);
-    u32x4_t w[2];
-    split(*reinterpret_cast<const f32x4_t*>(&t[b][row][col]), *reinterpret_cast<const f32x4_t*>(&t[b][row][col + 4]), 4096.f, w);
+    u32x4_t w[kTParts];
+    split(*reinterpret_cast<const f32x4_t*>(&t[b][row][col]), *reinterpret_cast<const f32x4_t*>(&t[b][row][col + 4]), w);
     uint8_t* item = item_of(a, local, h0 + b);
-    *reinterpret_cast<u32x4_t*>(item + 16 * e) = w[0];
-    *reinterpret_cast<u32x4_t*>(item + kTriangle + 16 * e) = w[1];
+#pragma unroll
+    for (int k = 0; k < (int)kTParts; ++k) *reinterpret_cast<u32x4_t*>(item + k * kTriangle + 16 * e) = w[k];
   }
 }
 
@@ -445,22 +421,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, 
 // One barrier a chunk, between a chunk's K S and its u:
 //   states   .. | u of j, S, K S of j + 1 | u of j + 1, ..
 //   outputs  .. | out of j - 1, Q S of j, stores K of j + 2 and V, T of j + 1 | ..
-// K is read on both sides of a barrier and kept three times, the rest twice.
+// Everything is kept twice.
 template <int DK>
 struct Scan {
   static constexpr int U = DK / 32, UH = U / 2;           // 32-row blocks of the state, of a half
   static constexpr uint32_t kPieces = DK / 8, kThreads = 128 * kScanGroups, kRows = kThreads / kPieces;   // that stage
-  static constexpr int kPasses = kC / (int)kRows, kTPasses = 2 * (int)kTriangle / 16 / kThreads;
+  static constexpr int kPasses = kC / (int)kRows;
+  static constexpr uint32_t kTPieces = kTParts * kTriangle / 16;
+  static constexpr int kTPasses = (kTPieces + kThreads - 1) / kThreads;
   static_assert(kThreads == 256 && kC * kSlice * 2 == 16 * kThreads && 4 * kC == kThreads, "V and the factors in one pass");
   struct Shared {
-    __attribute__((aligned(256))) uint8_t k[3][kC * DK * 2];
+    __attribute__((aligned(256))) uint8_t k[2][kC * DK * 2];
     __attribute__((aligned(16))) uint8_t v[2][kC * kSlice * 2];
-    u32x4_t t[2][2 * kBlocks][64];
-    u32x4_t state[2][kScanGroups][U][64];                 // before a chunk, scaled
-    u32x4_t u[2][kScanGroups][2][64];
+    u32x4_t t[2][kTParts * kBlocks][64];
+    u32x4_t state[2][kScanGroups][U][2][64];              // before a chunk, its first two parts
+    u32x4_t u[2][kScanGroups][2][2][64];                  // of 32 tokens each, two parts
     f32x4_t ks[2][kScanGroups][2][4][64];                 // the halves' K S
     __attribute__((aligned(16))) float vec[2][4 * kC];
-    float down[2][kScanGroups][2][16], udown[2][kScanGroups][16];   // what undoes the columns' scales
     int32_t bad[2][kScanGroups][16];                      // the first of a column's rows that is not finite
   };
   const Delta& a;
@@ -490,45 +467,43 @@ struct Scan {
     // or with 64 bytes, and rows 4 hf and 32 w further change no bits that the pieces' exchange looks at.
     const uint32_t kat = dealt_piece<DK>(dealt(0, 0, n), c) ^ 64 * UH * half, tat = dealt_piece<DK>(8 * c + (n >> 2), n & 3) ^ 64 * UH * half;
     f32x4_t ks[4];
-    const auto load_k = [&](const uint8_t* k, u32x4_t (&kw)[UH][4]) {
+    union { s16x4_t half[2]; u32x4_t all; } kt[2][2 * UH];   // four tokens of the lane's row of K^T each
+    // the state in parts, and its half of K S of chunk j; what the chunk needs of K^T besides
+    const auto take = [&](int32_t j) {
+      const uint8_t* k = sh.k[j & 1];
+      u32x4_t kw[UH][4];
 #pragma unroll
       for (int u = 0; u < UH; ++u)
 #pragma unroll
         for (int t = 0; t < 4; ++t) kw[u][t] = *reinterpret_cast<const u32x4_t*>(k + (kat ^ 64 * u) + (16 * (t & 2) + 4 * (t & 1)) * 2 * DK);
-    };
-    // the state in parts, and its half of K S of chunk j
-    const auto take = [&](int32_t j, const u32x4_t (&kw)[UH][4]) {
-      float most = 0.f;
-#pragma unroll
-      for (int u = 0; u < UH; ++u) most = largest(most, st[u][0], st[u][1]);
-      const Scale ss = scale_to(column_max(most), 12);
 #pragma unroll
       for (int t = 0; t < 4; ++t) ks[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < UH; ++u) {
-        u32x4_t part[2];
-        split(st[u][0], st[u][1], ss.up, part);
-        sh.state[j & 1][group][UH * half + u][lane] = part[0];
+        u32x4_t part[3];
+        split(st[u][0], st[u][1], part);
 #pragma unroll
-        for (int e = 1; e >= 0; --e)
+        for (int e = 0; e < 2; ++e) sh.state[j & 1][group][UH * half + u][e][lane] = part[e];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) ks[t] = product(as_operand(kw[u][t]), as_operand(part[e]), ks[t]);
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) ks[t] = product(kw[u][t], part[e], ks[t]);
       }
-      sh.down[j & 1][group][half][n] = ss.down;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        ks[t] *= ss.down;
-        sh.ks[j & 1][group][half][t][lane] = ks[t];
-      }
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int t = 0; t < 2 * UH; ++t)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            kt[w][t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4_t*)(k + (tat ^ 64 * (t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) sh.ks[j & 1][group][half][t][lane] = ks[t];
     };
     lds_barrier();
-    uint32_t kb = (uint32_t)j0 % 3;
-    u32x4_t kw[UH][4];
-    load_k(sh.k[kb], kw);
-    take(j0, kw);
+    take(j0);
     lds_barrier();
     for (int32_t j = j0; j < j1; ++j) {
-      const uint8_t* k = sh.k[kb];
       const float* vec = sh.vec[j & 1];
       const float decay = vec[3 * kC];
       // the rows b V - b e^G K S0; the lane's rows of V are four tokens of its column each
@@ -542,39 +517,25 @@ struct Scan {
 #pragma unroll
         for (int i = 0; i < 4; ++i) rows[t][i] = fmaf(-c2[i], both[i], c1[i] * bf16_value((uint16_t)v[i]));
       }
-      // read here, where nothing waits for them yet, for the products with K^T: four tokens of the lane's row of it each
-      union { s16x4_t half[2]; u32x4_t all; } kt[2][2 * UH];
-      f32x4_t c3[2][2];
+      f32x4_t c3[4];   // read here, where nothing waits for them yet
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-#pragma unroll
-        for (int t = 0; t < 2 * UH; ++t)
-#pragma unroll
-          for (int z = 0; z < 2; ++z)
-            kt[w][t].half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4_t*)(k + (tat ^ 64 * (t / 2)) + (32 * w + 4 * z) * 2 * DK + 8 * (t % 2)));
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) c3[w][hf] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 32 * w + 8 * c + 4 * hf);
-      }
-      f32x4_t u[4];   // times 2^12 and the rows' scale
-      Scale rs;
+      for (int t = 0; t < 4; ++t) c3[t] = *reinterpret_cast<const f32x4_t*>(vec + 2 * kC + 16 * (t & 2) + 8 * c + 4 * (t & 1));
+      f32x4_t u[4];   // times 2^-8
       const auto solve = [&] {
-        float top = 0.f;
+        u32x4_t part[2][3];
 #pragma unroll
-        for (int t = 0; t < 4; t += 2) top = largest(top, rows[t], rows[t + 1]);
-        rs = scale_to(column_max(top), 6);   // u is at most 2^7 times the largest row
-        u32x4_t part[2][2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) split(rows[2 * w], rows[2 * w + 1], rs.up, part[w]);
+        for (int w = 0; w < 2; ++w) split(rows[2 * w], rows[2 * w + 1], part[w]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) u[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 2; e >= 0; --e)   // lo hi, hi lo, hi hi
+        for (int e = 0; e < 3; ++e)   // by size, so that they begin before the small parts are there; those below 2^-24 are left out
 #pragma unroll
-          for (int b = 0; b < (int)kBlocks; ++b) {
-            const int t = 2 * (b > 1) + (b & 1), sb = b > 3;
-            u[t] = product(as_operand(sh.t[j & 1][(e == 2) * kBlocks + b][lane]), as_operand(part[sb][e == 1]), u[t]);
-          }
+          for (int f = 0; f <= e; ++f)
+#pragma unroll
+            for (int b = 0; b < (int)kBlocks; ++b) {
+              const int t = 2 * (b > 1) + (b & 1), sb = b > 3;
+              u[t] = product(sh.t[j & 1][(e - f) * kBlocks + b][lane], part[sb][f], u[t]);
+            }
       };
       solve();
       int32_t bad = kC;
@@ -597,32 +558,30 @@ struct Scan {
             if (16 * (t & 2) + 8 * (int32_t)c + 4 * (t & 1) + i >= bad) u[t][i] = 0.f;
       }
       // S = decay S + K^T diag(e^(G_end - G)) u
-      u32x4_t up[2][2], one[1];
+      u32x4_t up[2][3], own[2];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) split(u[2 * w], u[2 * w + 1], c3[w][0], c3[w][1], up[w]);
-      split(half ? u[2] : u[0], half ? u[3] : u[1], 0x1p-12f, one);
-      sh.u[j & 1][group][half][lane] = one[0];
+      for (int w = 0; w < 2; ++w) split(c3[2 * w] * u[2 * w], c3[2 * w + 1] * u[2 * w + 1], up[w]);
+      split(half ? u[2] : u[0], half ? u[3] : u[1], own);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sh.u[j & 1][group][half][e][lane] = own[e];
       // every lane that holds a value writes it: a branch here would keep what is around it apart
       sh.bad[j & 1][group][n] = bad;
-      sh.udown[j & 1][group][n] = rs.down * 0x1p-12f;
-      float back = bad < kC ? NAN : rs.down * 0x1p-12f;
+      float back = bad < kC ? NAN : kRowBack;
       asm("" : "+v"(back));   // chosen once, not after each of the sums below
       f32x4_t add[2 * UH];
 #pragma unroll
       for (int t = 0; t < 2 * UH; ++t) add[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      kb = kb == 2 ? 0 : kb + 1;
-      load_k(sh.k[kb], kw);
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int e = 0; e < 3; ++e)
 #pragma unroll
-        for (int e = 1; e >= 0; --e)
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int t = 0; t < 2 * UH; ++t) add[t] = product(as_operand(kt[w][t].all), as_operand(up[w][e]), add[t]);
+          for (int t = 0; t < 2 * UH; ++t) add[t] = product(kt[w][t].all, up[w][e], add[t]);
 #pragma unroll
       for (int t = 0; t < 2 * UH; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) st[t / 2][t % 2][i] = fmaf(add[t][i], back, decay * st[t / 2][t % 2][i]);
-      take(j + 1, kw);   // behind the last chunk: of some chunk's K, and not read
+      take(j + 1);   // behind the last chunk: of some chunk's K, and not read
       lds_barrier();
     }
     if (after)
@@ -639,8 +598,8 @@ struct Scan {
   __device__ __forceinline__ void outputs(uint32_t w) {
     const uint32_t dv = a.value_dim, ldo = (uint32_t)a.ldo, ldv = (uint32_t)a.ldv, tid = 64 * (kScanGroups * w + group) + lane;
     const uint32_t olane = 2 * ((32 * w + 8 * c) * ldo + col), vlane = 2 * (tid / 4 * ldv + (col & ~(kSlice - 1)) + 8 * (tid % 4));
-    u32x4_t kr[kPasses], vr, tr[kTPasses], pw[2][2], qw[2][U];   // P: of 32 tokens before (zeros for the first), of its own
-    f32x4_t c4[2], c6[2], o[2][2];
+    u32x4_t kr[kPasses], vr, tr[kTPasses], pw[2][kPParts][2], qw[2][U];   // P: of 32 tokens before (zeros for the first), of its own
+    f32x4_t c4[2], c6[2], o[2];
     float fr;
     const int32_t last = j1 - 1;
     const auto load_k = [&](int32_t j) {
@@ -648,20 +607,21 @@ struct Scan {
       for (int i = 0; i < kPasses; ++i) kr[i] = *reinterpret_cast<const u32x4_t*>(key_item_of(a, local(min(j, last)), kh) + 16 * (tid + i * kThreads));
     };
     const auto store_k = [&](int32_t j) {
-      uint8_t* k = sh.k[(uint32_t)j % 3];
+      uint8_t* k = sh.k[j & 1];
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) *reinterpret_cast<u32x4_t*>(k + dealt_piece<DK>(tid / kPieces + i * kRows, tid % kPieces)) = kr[i];
     };
     const auto load_rest = [&](int32_t j) {
       const uint8_t* p = item(min(j, last));
 #pragma unroll
-      for (int i = 0; i < kTPasses; ++i) tr[i] = *reinterpret_cast<const u32x4_t*>(p + 16 * (tid + i * kThreads));
+      for (int i = 0; i < kTPasses; ++i) tr[i] = *reinterpret_cast<const u32x4_t*>(p + 16 * (tid + i * kThreads));   // and some of P behind it
       fr = *reinterpret_cast<const float*>(p + kVecAt + 4 * tid);
       vr = __builtin_amdgcn_raw_buffer_load_b128(rows_of(a.v, a.ldv, min(j, last), h * dv, dv), vlane, 0, 0);
     };
     const auto store_rest = [&](int32_t j) {
 #pragma unroll
-      for (int i = 0; i < kTPasses; ++i) (&sh.t[j & 1][0][0])[tid + i * kThreads] = tr[i];
+      for (int i = 0; i < kTPasses; ++i)
+        if ((i + 1) * kThreads <= kTPieces || 64 * kScanGroups * w + i * kThreads < kTPieces) (&sh.t[j & 1][0][0])[tid + i * kThreads] = tr[i];
       sh.vec[j & 1][tid] = fr;
       *reinterpret_cast<u32x4_t*>(sh.v[j & 1] + 16 * tid) = vr;
     };
@@ -676,47 +636,53 @@ struct Scan {
       const uint8_t* p = item(min(j, last));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        pw[0][t] = w ? *reinterpret_cast<const u32x4_t*>(p + kPAt + (2 + t) * kOperand + 16 * lane) : u32x4_t{0, 0, 0, 0};
-        pw[1][t] = *reinterpret_cast<const u32x4_t*>(p + kPAt + (4 * w + t) * kOperand + 16 * lane);
+#pragma unroll
+        for (int e = 0; e < (int)kPParts; ++e) {
+          const uint8_t* part = p + kPAt + e * kTriangle + 16 * lane;
+          pw[0][e][t] = w ? *reinterpret_cast<const u32x4_t*>(part + (2 + t) * kOperand) : u32x4_t{0, 0, 0, 0};
+          pw[1][e][t] = *reinterpret_cast<const u32x4_t*>(part + (4 * w + t) * kOperand);
+        }
         const uint8_t* f = p + kVecAt + 4 * (4 * kC + 32 * w + 8 * c + 4 * t);
         c4[t] = *reinterpret_cast<const f32x4_t*>(f);
         c6[t] = *reinterpret_cast<const f32x4_t*>(f + 4 * kC);
       }
     };
-    const auto from_state = [&](int32_t j) {   // Q S of chunk j, by the state's halves
+    const auto from_state = [&](int32_t j) {   // Q S of chunk j, by the state's parts
+      f32x4_t x[2][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) o[e][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 2; ++t) x[e][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < UH; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const f16x8_t part = as_operand(sh.state[j & 1][group][UH * e + u][lane]);
+          const u32x4_t part = sh.state[j & 1][group][u][e][lane];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) o[e][t] = product(as_operand(qw[t][UH * e + u]), part, o[e][t]);
+          for (int t = 0; t < 2; ++t) x[e][t] = product(qw[t][u], part, x[e][t]);
         }
-      const float d0 = sh.down[j & 1][group][0][n], d1 = sh.down[j & 1][group][1][n];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[0][t][i] = fmaf(d0, o[0][t][i], d1 * o[1][t][i]);
+      for (int t = 0; t < 2; ++t) o[t] = x[0][t] + x[1][t];
     };
     const auto finish = [&](int32_t j) {
       f32x4_t p[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const f16x8_t first = as_operand(sh.u[j & 1][group][0][lane]), own = as_operand(sh.u[j & 1][group][w][lane]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) p[t] = product(as_operand(pw[0][t]), first, p[t]);
+      for (int e = 1; e >= 0; --e)   // the product of the second parts, below 2^-16, is left out
 #pragma unroll
-      for (int t = 0; t < 2; ++t) p[t] = product(as_operand(pw[1][t]), own, p[t]);
-      const float du = sh.udown[j & 1][group][n];
+        for (int f = 0; f <= e; ++f)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const u32x4_t u = sh.u[j & 1][group][b ? w : 0][f][lane];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) p[t] = product(pw[b][e - f][t], u, p[t]);
+          }
       const int32_t bad = sh.bad[j & 1][group][n] - 32 * (int32_t)w;
       const __amdgpu_buffer_rsrc_t r = rows_of(a.out, a.ldo, j, h * dv, dv);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float y = c6[t][i] * fmaf(c4[t][i], o[0][t][i], du * p[t][i]);
+          const float y = c6[t][i] * fmaf(c4[t][i], o[t][i], kRowBack * p[t][i]);
           __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)((int32_t)(4 * t + i + 8 * c) >= bad ? NAN : y)), r,
                                                 olane + (4 * t + i) * 2 * ldo, 0, 0);
         }
