@@ -13,9 +13,37 @@ from typing import Sequence
 
 import numpy as np
 
-from . import (WAL_MAX_BATCH, make_delta_desc, wal_conv, wal_delta, wal_delta_workspace_size, wal_gemm_prefill,
-               wal_gemm_small, wal_head_norm, wal_prefill_workspace_size, wal_workspace_size)
+from . import (WAL_MAX_BATCH, _norm_weight, _types, _vec, make_delta_desc, wal_conv, wal_delta,
+               wal_delta_workspace_size, wal_gemm_prefill, wal_gemm_small, wal_head_norm, wal_prefill_workspace_size,
+               wal_workspace_size)
 from .attention import _counts, _sequences
+
+
+def _check_small(conv, conv_bias, decay, shift, norm, eps: float, channels: int, value_heads: int, value_dim: int, device):
+    """Everything that wal_conv, wal_delta and wal_head_norm would refuse of a layer's small tensors."""
+    T = _types()
+    for name, t in (("conv", conv), ("conv_bias", conv_bias), ("decay", decay), ("shift", shift), ("norm", norm)):
+        if t is None and name == "conv_bias":
+            continue
+        if not isinstance(t, T.tensor):
+            raise TypeError(f"{name} must be a torch tensor on the GPU, not {type(t).__name__}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the matrices on {device}")
+        if t.data_ptr() % (16 if name.startswith("conv") else t.element_size()):
+            raise ValueError(f"{name} is not aligned to {16 if name.startswith('conv') else t.element_size()} bytes")
+    if conv.dtype not in T.acts:
+        raise TypeError(f"conv has dtype {conv.dtype}; expected one of {[str(d) for d in T.acts]}")
+    if conv.dim() != 2 or conv.shape[0] != channels or not 2 <= conv.shape[1] <= 4 or not conv.is_contiguous():
+        raise ValueError(f"conv must be contiguous, [{channels}][2 to 4 taps] (shape {tuple(conv.shape)})")
+    if conv_bias is not None:
+        _norm_weight(T, conv_bias, "conv_bias", channels)
+        if conv_bias.dtype is not conv.dtype:
+            raise TypeError(f"conv_bias has dtype {conv_bias.dtype}, conv {conv.dtype}: they must be the same")
+    _vec(T, decay, "decay", T.f32, value_heads)
+    _vec(T, shift, "shift", T.f32, value_heads)
+    _norm_weight(T, norm, "norm", value_dim)
+    if not 2.0 ** -126 <= eps < float("inf"):
+        raise ValueError(f"eps {eps}: normal, finite and above 0")
 
 
 class DeltaLayer:
@@ -30,8 +58,12 @@ class DeltaLayer:
         import torch
         self.torch, self.dev = torch, qkv[1].device
         self.mats = (qkv, z, ab, o)
+        # all here, so that no call is refused between the launches that change states
+        _check_small(conv, conv_bias, decay, shift, norm, eps, 2 * key_heads * key_dim + value_heads * value_dim, value_heads,
+                     value_dim, self.dev)
         self.conv, self.conv_bias, self.decay, self.shift, self.norm, self.eps = conv, conv_bias, decay, shift, norm, eps
         self.desc = make_delta_desc(key_heads, value_heads, key_dim, value_dim, norm_eps=norm_eps)
+        wal_delta_workspace_size(self.desc, 1, 1, 1)   # refuses heads and sizes that wal_delta does not take
         kw, vw = key_heads * key_dim, value_heads * value_dim
         self.parts = (slice(0, kw), slice(kw, 2 * kw), slice(2 * kw, 2 * kw + vw))
         for name, m, rows in (("qkv", qkv, 2 * kw + vw), ("z", z, vw), ("ab", ab, 2 * value_heads)):
@@ -68,7 +100,8 @@ class DeltaLayer:
         self.state[s].zero_()
 
     def _run(self, X, new, slots):
-        """forward() and prompt(): of the states, only the last two launches before the o product change any."""
+        """forward() and prompt().  wal_conv and wal_delta change the kept rows and the states; what they and the calls behind
+        them could refuse is checked before, here or by the constructor."""
         torch = self.torch
         QKV, Z, AB = (self._product(m, X, self._product(m, X)) for m in self.mats[:3])
         h, n = self.desc.value_heads, X.shape[0]
