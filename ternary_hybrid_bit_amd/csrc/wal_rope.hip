@@ -37,6 +37,7 @@ namespace {
 constexpr uint32_t kRopeThreads = 256;
 constexpr uint32_t kRopeLdsPairs = 1024;   // sines of one workgroup's tokens, 8 KB
 constexpr uint32_t kMaxRopeDim = 512;      // at most 256 pairs a token
+constexpr uint32_t kMaxGroups = 0xFFFFFFFFu / kRopeThreads;   // of a launch, which has fewer than 2^32 threads along an axis
 
 struct RopeKv {
   const char* q;                  // the q rows, and from there to the k rows, from those to the v rows
@@ -50,7 +51,7 @@ struct RopeKv {
   uint64_t ldqo;
   uint64_t off_k, k_to_v, off_ks, ks_to_vs;   // bytes from the cache's start, from plane to plane
   float magnitude;
-  uint32_t n, tokens;             // tokens of the call, of a workgroup
+  uint32_t n, tokens, first;      // tokens of the call, of a workgroup, before the launch's
   uint32_t slice;                 // units of a token that a workgroup takes
   uint32_t units, q_units, k_units;   // units of a token, of its q and its k heads
   uint32_t per_head, rot_units;   // units of a head, rotated ones among them
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_kv(RopeKv a) {
   constexpr bool kGate = MODE >= kGatedF32;
   __shared__ float2 cs[kRopeLdsPairs];
   __shared__ __attribute__((aligned(16))) float wsh[MODE ? 2 : 1][MODE ? kMaxRopeDim : 1];
-  const uint32_t t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
+  const uint32_t t0 = a.first + blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
   const uint32_t u0 = blockIdx.y * a.slice, nu = min(a.slice, a.units - u0), total = nt * nu;
   uint32_t i = threadIdx.x;
   Unit x{};
@@ -313,12 +314,13 @@ struct KvRead {
   int64_t ld, ld_to_v;
   uint64_t off, off_to_v, off_s, off_s_to_v;
   uint32_t n, units, per_head_shift, n_slots, page_shift, kv_heads, dim, int8, out_bf16;
+  uint64_t first;                 // workgroups before the launch's
 };
 
 // A thread reads 16 elements of a row: 16 bytes of codes and the row's scale, or
 // 32 bytes of bf16.
 __global__ __launch_bounds__(kRopeThreads) void k_kv_read(KvRead a) {
-  const uint64_t i = (uint64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+  const uint64_t i = (a.first + blockIdx.x) * kRopeThreads + threadIdx.x;
   const uint32_t t = (uint32_t)(i / a.units), u = (uint32_t)(i - (uint64_t)t * a.units);
   const bool z = blockIdx.y;
   if (t >= a.n) return;
@@ -398,11 +400,15 @@ int launch(RopeKv& a, bool bf16_in, int mode, hipStream_t s) {
     if (a.tokens > by_lds) a.tokens = by_lds;
     if (!a.tokens) a.tokens = 1;
   }
-  const dim3 grid((a.n + a.tokens - 1) / a.tokens, (a.units + a.slice - 1) / a.slice);
-  if (mode == kAsIs) launch<kAsIs>(a, bf16_in, grid, s);
-  if (mode == kNormed) launch<kNormed>(a, bf16_in, grid, s);
-  if (mode == kGatedF32) launch<kGatedF32>(a, bf16_in, grid, s);
-  if (mode == kGatedBf16) launch<kGatedBf16>(a, bf16_in, grid, s);
+  const uint32_t groups = (a.n + a.tokens - 1) / a.tokens;
+  for (uint32_t g = 0; g < groups; g += kMaxGroups) {
+    a.first = g * a.tokens;
+    const dim3 grid(groups - g < kMaxGroups ? groups - g : kMaxGroups, (a.units + a.slice - 1) / a.slice);
+    if (mode == kAsIs) launch<kAsIs>(a, bf16_in, grid, s);
+    if (mode == kNormed) launch<kNormed>(a, bf16_in, grid, s);
+    if (mode == kGatedF32) launch<kGatedF32>(a, bf16_in, grid, s);
+    if (mode == kGatedBf16) launch<kGatedBf16>(a, bf16_in, grid, s);
+  }
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
 
@@ -623,8 +629,10 @@ extern "C" int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const in
   a.int8 = d->fmt == WAL_KV_INT8;
   a.out_bf16 = out_dtype == WAL_X_BF16;
   const uint64_t blocks = ((uint64_t)n * a.units + kRopeThreads - 1) / kRopeThreads;
-  if (blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
-  hipLaunchKernelGGL(k_kv_read, dim3((uint32_t)blocks, k_out_dev && v_out_dev ? 2 : 1),
-                     dim3(kRopeThreads), 0, static_cast<hipStream_t>(stream), a);
+  for (a.first = 0; a.first < blocks; a.first += kMaxGroups) {
+    const uint64_t left = blocks - a.first;
+    hipLaunchKernelGGL(k_kv_read, dim3(left < kMaxGroups ? (uint32_t)left : kMaxGroups, k_out_dev && v_out_dev ? 2 : 1),
+                       dim3(kRopeThreads), 0, static_cast<hipStream_t>(stream), a);
+  }
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
