@@ -35,6 +35,7 @@ struct Delta {
   uint32_t n_seqs, n, max_new, n_slots;
   uint32_t heads, group, value_dim, slices;   // value heads, those that share a key head
   float eps, scale;              // eps 0: q and k as they are
+  uint32_t seq0;                 // token by token: sequences before the launch's
   int32_t few;                   // a call in both forms: sequences of at most so many rows go token by token, others on chunks
   // calls on chunks: sequence s has the places from starts[s] / 64 + s on, one for each chunk; a launch takes `places`
   // of them from place0, and a sequence that goes on leaves its state in carry[1] and finds it in carry[0]

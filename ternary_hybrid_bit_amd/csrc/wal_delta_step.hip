@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(Delta a) {
   constexpr int kSums = 11;             // S^T k and S^T q of four columns, k . k, q . q, k . q
   __shared__ float sums[2][kWaves][kCols][kSums + 1];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = threadIdx.x % kCols, r = threadIdx.x / kCols;
-  const uint32_t slices = a.value_dim / NV, slice = blockIdx.x % slices, rest = blockIdx.x / slices, h = rest % a.heads, s = rest / a.heads;
+  const uint32_t slices = a.value_dim / NV, slice = blockIdx.x % slices, rest = blockIdx.x / slices, h = rest % a.heads, s = a.seq0 + rest / a.heads;
   const Seq seq = delta_seq(a, s);
   if (!seq.rows || seq.rows > a.few) return;
   const int64_t slot = kept_at(a, s);
@@ -133,9 +133,12 @@ __global__ __launch_bounds__(kThreads) void k_delta_step(Delta a) {
     for (int j = 0; j < J; ++j) *reinterpret_cast<f32x4_t*>(state + (uint64_t)j * a.value_dim) = m[j];
 }
 
+// A launch has fewer than 2^32 threads along an axis: of more sequences than that allows, several.
 template <int DK, int NV>
-void launch(const Delta& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_delta_step<DK, NV>), dim3(a.n_seqs * a.heads * (a.value_dim / NV)), dim3(kThreads), 0, s, a);
+void launch(Delta a, hipStream_t s) {
+  const uint32_t each = a.heads * (a.value_dim / NV), most = 0xFFFFFFFFu / kThreads / each;
+  for (a.seq0 = 0; a.seq0 < a.n_seqs; a.seq0 += most)
+    hipLaunchKernelGGL((k_delta_step<DK, NV>), dim3((a.n_seqs - a.seq0 < most ? a.n_seqs - a.seq0 : most) * each), dim3(kThreads), 0, s, a);
 }
 
 // Columns of a workgroup: 64 where that makes two workgroups for each compute unit, else 32 (key heads of 128, 64 sequences
@@ -152,7 +155,6 @@ void launch(const Delta& a, hipStream_t s) {
 namespace wal {
 
 int delta_step(const Delta& a, uint32_t key_dim, void* stream) {
-  if ((uint64_t)a.n_seqs * a.heads * a.slices > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (key_dim == 64) launch<64>(a, s);
   else launch<128>(a, s);

@@ -32,3 +32,23 @@ def test_cache_write_of_more_rows_than_a_launch_takes(wal):
     assert want.any() and torch.equal(cache, want)
     del x
     torch.cuda.empty_cache()
+
+
+def test_delta_rule_of_more_sequences_than_a_launch_takes(wal):
+    """1024 heads of 256 columns, 2^13 sequences of which three bring a token: 2^25 workgroups."""
+    seqs, n, h, dk, dv = 1 << 13, 3, 1024, 64, 256
+    desc = wal.make_delta_desc(h, h, dk, dv)
+    g = torch.Generator("cuda").manual_seed(2)
+    q, k = (torch.randn((n, h * dk), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    v = torch.randn((n, h * dv), device="cuda", generator=g).to(torch.bfloat16)
+    a, b = -torch.rand((n, h), device="cuda", generator=g), torch.rand((n, h), device="cuda", generator=g)
+    starts = torch.zeros(seqs + 1, dtype=torch.int32)
+    starts[1:] += 1
+    starts[seqs // 2:] += 1
+    starts[seqs:] += 1
+    few = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    want, out = (torch.full((n, h * dv), -7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wal.wal_delta(desc, q, k, v, a, b, few.cuda(), want, max_new=1)
+    wal.wal_delta(desc, q, k, v, a, b, starts.cuda(), out, max_new=1)
+    torch.cuda.synchronize()
+    assert (want != -7).all() and torch.equal(out, want)
