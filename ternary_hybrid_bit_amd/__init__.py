@@ -764,7 +764,7 @@ def _mat(T, t, name: str, dtypes, cols: int, rows: int = 0):
     if n < rows:
         raise ValueError(f"{name} has {n} rows; at least {rows} are needed")
     ld, step = t.stride()
-    if step != 1 and c > 1 and n:
+    if step != 1 and c > 1 and n:   # (one without rows may have any: numpy's have 0)
         raise ValueError(f"{name} must have unit stride along its last axis")
     if n <= 1:
         ld = (c + 7) & ~7   # the pitch of an only row means nothing: one of whole 16 bytes
