@@ -637,11 +637,18 @@ __global__ __launch_bounds__(128) void k_embed_mixed(const uint8_t* __restrict__
 
 }  // namespace
 
+// One workgroup row per token, in launches of fewer than 2^32 threads along the grid's x: f(first token, how many).
+constexpr uint32_t kEmbedThreads = 128, kEmbedRows = 0xFFFFFFFFu / kEmbedThreads;
+template <class F>
+static void embed_launches(uint32_t n, F f) {
+  for (uint32_t i = 0; i < n; i += kEmbedRows) f(i, n - i < kEmbedRows ? n - i : kEmbedRows);
+}
+
 static int embed_check(uint32_t in, uint32_t n, void* out_dev, int out_dtype, uint32_t ldo) {
   if (out_dtype != WAL_X_F32 && out_dtype != WAL_X_BF16) return WAL_ERR_ARG;
   if (in % 128) return WAL_ERR_SHAPE;
   if (ldo < in) return WAL_ERR_ARG;
-  if (n > 0x7FFFFFFFu) return WAL_ERR_SHAPE;   // one workgroup row per token: the grid's x limit
+  if (n > 0x7FFFFFFFu) return WAL_ERR_SHAPE;
   const size_t oe = out_dtype == WAL_X_BF16 ? 2 : 4;
   if ((reinterpret_cast<uintptr_t>(out_dev) & 15u) || (ldo * oe) % 16) return WAL_ERR_ALIGN;
   return WAL_OK;
@@ -660,12 +667,16 @@ extern "C" int wal_embed_rows(const void* W_dev, int bits, uint32_t V, uint32_t 
       overlaps(out_dev, obytes, ids_dev, (size_t)n * 4))
     return WAL_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(n, (in + 2047) / 2048), block(128);
   const uint8_t* W = static_cast<const uint8_t*>(W_dev);
-  if (bits == 3 && out_dtype == WAL_X_F32) hipLaunchKernelGGL((k_embed_rows<3, WAL_X_F32>), grid, block, 0, s, W, V, in, ids_dev, out_dev, ldo);
-  else if (bits == 3) hipLaunchKernelGGL((k_embed_rows<3, WAL_X_BF16>), grid, block, 0, s, W, V, in, ids_dev, out_dev, ldo);
-  else if (out_dtype == WAL_X_F32) hipLaunchKernelGGL((k_embed_rows<4, WAL_X_F32>), grid, block, 0, s, W, V, in, ids_dev, out_dev, ldo);
-  else hipLaunchKernelGGL((k_embed_rows<4, WAL_X_BF16>), grid, block, 0, s, W, V, in, ids_dev, out_dev, ldo);
+  embed_launches(n, [&](uint32_t first, uint32_t rows) {
+    const dim3 grid(rows, (in + 2047) / 2048), block(kEmbedThreads);
+    const int32_t* ids = ids_dev + first;
+    void* out = static_cast<char*>(out_dev) + (size_t)first * ldo * (out_dtype == WAL_X_BF16 ? 2 : 4);
+    if (bits == 3 && out_dtype == WAL_X_F32) hipLaunchKernelGGL((k_embed_rows<3, WAL_X_F32>), grid, block, 0, s, W, V, in, ids, out, ldo);
+    else if (bits == 3) hipLaunchKernelGGL((k_embed_rows<3, WAL_X_BF16>), grid, block, 0, s, W, V, in, ids, out, ldo);
+    else if (out_dtype == WAL_X_F32) hipLaunchKernelGGL((k_embed_rows<4, WAL_X_F32>), grid, block, 0, s, W, V, in, ids, out, ldo);
+    else hipLaunchKernelGGL((k_embed_rows<4, WAL_X_BF16>), grid, block, 0, s, W, V, in, ids, out, ldo);
+  });
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }
 
@@ -687,12 +698,16 @@ extern "C" int wal_embed_rows_mixed(const void* W3_dev, uint32_t V3, const void*
       overlaps(out_dev, obytes, map_dev, (size_t)V * 4) || overlaps(out_dev, obytes, ids_dev, (size_t)n * 4))
     return WAL_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(n, (in + 2047) / 2048), block(128);
   const uint8_t* W3 = static_cast<const uint8_t*>(W3_dev);
   const uint8_t* W4 = static_cast<const uint8_t*>(W4_dev);
-  if (out_dtype == WAL_X_F32)
-    hipLaunchKernelGGL(k_embed_mixed<WAL_X_F32>, grid, block, 0, s, W3, V3, W4, V4, in, map_dev, V, ids_dev, out_dev, ldo);
-  else
-    hipLaunchKernelGGL(k_embed_mixed<WAL_X_BF16>, grid, block, 0, s, W3, V3, W4, V4, in, map_dev, V, ids_dev, out_dev, ldo);
+  embed_launches(n, [&](uint32_t first, uint32_t rows) {
+    const dim3 grid(rows, (in + 2047) / 2048), block(kEmbedThreads);
+    const int32_t* ids = ids_dev + first;
+    void* out = static_cast<char*>(out_dev) + (size_t)first * ldo * (out_dtype == WAL_X_BF16 ? 2 : 4);
+    if (out_dtype == WAL_X_F32)
+      hipLaunchKernelGGL(k_embed_mixed<WAL_X_F32>, grid, block, 0, s, W3, V3, W4, V4, in, map_dev, V, ids, out, ldo);
+    else
+      hipLaunchKernelGGL(k_embed_mixed<WAL_X_BF16>, grid, block, 0, s, W3, V3, W4, V4, in, map_dev, V, ids, out, ldo);
+  });
   return hipGetLastError() == hipSuccess ? WAL_OK : WAL_ERR_DEVICE;
 }

@@ -131,14 +131,22 @@ extern "C" int wal_rotate_h128(const void* x_dev, int x_dtype, uint32_t rows, ui
   if (!same && xa < oa + ob && oa < xa + xb) return WAL_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const uint32_t chunks = (uint32_t)((groups + 31) / 32);
-  const dim3 grid((uint32_t)((total + 31) / 32)), grid_rows(rows * chunks);   // 32 groups per workgroup
+  const dim3 grid((uint32_t)((total + 31) / 32));   // 32 groups per workgroup
   const uint16_t* xh = static_cast<const uint16_t*>(x_dev);
   const float* xf = static_cast<const float*>(x_dev);
-  if (x_dtype == WAL_X_BF16 && out_dtype == WAL_X_BF16)
-    hipLaunchKernelGGL(k_rotate_h128_mfma<WAL_X_BF16>, grid_rows, dim3(256), 0, s, xh, ldx, out_dev, ldo, (uint32_t)groups, chunks);
-  else if (x_dtype == WAL_X_BF16)
-    hipLaunchKernelGGL(k_rotate_h128_mfma<WAL_X_F32>, grid_rows, dim3(256), 0, s, xh, ldx, out_dev, ldo, (uint32_t)groups, chunks);
-  else if (out_dtype == WAL_X_BF16)
+  if (x_dtype == WAL_X_BF16) {
+    // at least one workgroup a row, in launches of fewer than 2^32 threads (fewer than 2^23 chunks of a row)
+    const uint32_t most = 0xFFFFFFFFu / 256 / chunks;
+    for (uint32_t r = 0; r < rows; r += most) {
+      const dim3 grid_rows((rows - r < most ? rows - r : most) * chunks);
+      const uint16_t* x = xh + (size_t)r * ldx;
+      void* out = static_cast<char*>(out_dev) + (size_t)r * ldo * oe;
+      if (out_dtype == WAL_X_BF16)
+        hipLaunchKernelGGL(k_rotate_h128_mfma<WAL_X_BF16>, grid_rows, dim3(256), 0, s, x, ldx, out, ldo, (uint32_t)groups, chunks);
+      else
+        hipLaunchKernelGGL(k_rotate_h128_mfma<WAL_X_F32>, grid_rows, dim3(256), 0, s, x, ldx, out, ldo, (uint32_t)groups, chunks);
+    }
+  } else if (out_dtype == WAL_X_BF16)
     hipLaunchKernelGGL(k_rotate_h128_f32<WAL_X_BF16>, grid, dim3(256), 0, s, xf, ldx, out_dev, ldo, rows, (uint32_t)groups);
   else
     hipLaunchKernelGGL(k_rotate_h128_f32<WAL_X_F32>, grid, dim3(256), 0, s, xf, ldx, out_dev, ldo, rows, (uint32_t)groups);

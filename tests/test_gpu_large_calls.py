@@ -34,6 +34,41 @@ def test_cache_write_of_more_rows_than_a_launch_takes(wal):
     torch.cuda.empty_cache()
 
 
+def test_rotation_of_more_rows_than_a_launch_takes(wal):
+    """2^24 + 3 rows of one group (4.3 GB, in place)."""
+    n = (1 << 24) + 3
+    rows = torch.tensor([0, 5, 1 << 23, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, n - 1], device="cuda")
+    few = torch.randn((len(rows), 128), device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(torch.bfloat16)
+    want = torch.empty_like(few)
+    wal.wal_rotate_h128(few, want)
+    x = torch.empty((n, 128), dtype=torch.bfloat16, device="cuda")
+    x[rows] = few
+    wal.wal_rotate_h128(x, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x[rows], want) and not torch.equal(few, want)
+
+
+@pytest.mark.parametrize("mixed", [False, True])
+def test_embedding_of_more_tokens_than_a_launch_takes(wal, mixed):
+    """2^25 + 3 tokens of 128 columns (8.6 GB)."""
+    import numpy as np
+    rng, V = np.random.default_rng(4), 16
+    pack = lambda bits: torch.from_numpy((wal.wal_int3_pack if bits == 3 else wal.wal_int4_pack)(  # noqa: E731
+        rng.integers(-4, 4, (V, 128)).astype(np.int8), rng.uniform(0.1, 1, (V, 1)).astype(np.float16).astype(np.float32))).cuda()
+    W3, W4 = pack(3), pack(4)
+    n = (1 << 25) + 3
+    ids = torch.randint(0, V, (n,), dtype=torch.int32, device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    row_map = torch.tensor([v if v % 2 else -1 - v for v in range(V)], dtype=torch.int32, device="cuda")
+    embed = (lambda i, o: wal.wal_embed_rows_mixed(W3, V, W4, V, 128, row_map, i, o)) if mixed else (  # noqa: E731
+        lambda i, o: wal.wal_embed_rows(W3, 3, V, 128, i, o))
+    out = torch.full((n, 128), -9.0, dtype=torch.bfloat16, device="cuda")
+    embed(ids, out)
+    for part in (slice(0, 4), slice((1 << 25) - 4, n), slice(1 << 24, (1 << 24) + 4)):
+        want = torch.empty((ids[part].numel(), 128), dtype=torch.bfloat16, device="cuda")
+        embed(ids[part].clone(), want)
+        assert torch.equal(out[part], want) and (want != -9).any()
+
+
 def test_delta_rule_of_more_sequences_than_a_launch_takes(wal):
     """1024 heads of 256 columns, 2^13 sequences of which three bring a token: 2^25 workgroups."""
     seqs, n, h, dk, dv = 1 << 13, 3, 1024, 64, 256
