@@ -697,7 +697,8 @@ int wal_kv_read(const wal_kv_desc* d, const void* cache_dev, const int32_t* slot
  *               16-byte aligned rows; out must not overlap the inputs
  *   scale       finite, also times log2(e)
  *   n, n_seqs and max_new are at most 2^24, max_len at most 2^30, n * q_heads
- *               below 2^31
+ *               below 2^31; a call of more workgroups than a launch takes (2^23 and more: sequences
+ *               times kv_heads times pieces of the contexts) is refused (SHAPE)
  *   ws          wal_attn_paged_workspace_size bytes, 256-byte aligned (NULL when
  *               that is 0).  Its first WAL_ATTN_WS_ZERO_BYTES bytes are zero
  *               before the first call; every call leaves them so, whatever its
@@ -719,7 +720,7 @@ int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const int32_t* t
  * sequence s is rows starts[s] .. starts[s + 1] of q, k and v (all bf16, 16-byte
  * aligned rows of ldq, ldk, ldv elements, heads side by side, ldk and ldv at
  * most 2^26; views of one fused buffer are fine), each row sees its own sequence's rows up to itself
- * (causal) or all of them.  max_len bounds the sequences' lengths.
+ * (causal) or all of them.  max_len bounds the sequences' lengths.  Workgroups: as above.
  * Errors: ARG, SHAPE, ALIGN, DEVICE. */
 int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk, const void* v_dev,
                     uint32_t ldv, const int32_t* starts_dev, uint32_t n_seqs, uint32_t n, uint32_t max_len,

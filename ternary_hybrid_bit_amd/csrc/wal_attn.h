@@ -48,6 +48,11 @@ constexpr bool stream_wide(uint32_t n_seqs, uint32_t kv_heads, uint32_t max_len)
   return max_len <= 1024 && (uint64_t)n_seqs * kv_heads <= 256;
 }
 
+// Whether a launch takes so many workgroups: it has fewer than 2^32 threads along an axis, and does only a part of more.
+constexpr bool launch_takes(uint64_t blocks, uint32_t threads) { return blocks <= 0xFFFFFFFFu / threads; }
+// Query rows, counted by heads, that a workgroup of attn_join takes where there are many.
+constexpr uint32_t join_rows(uint32_t dim) { return 1024 / dim; }
+
 // Launches (wal_status).  attn_stream: rows of each key/value head <= 16 tiles, tiles 1 or 2;
 // attn_join adds what it wrote when a.n_splits > 1 and a.counters is NULL.
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream);

@@ -176,7 +176,8 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   a.page_shift = (uint32_t)__builtin_ctz(d->page_size);
   a.kv_heads = d->kv_heads;
   const Plan p = plan_of(d, q_heads, n_seqs, n, max_new, max_len);
-  const bool int8 = d->fmt == WAL_KV_INT8;
+  const bool int8 = d->fmt == WAL_KV_INT8, joined = p.n_splits > 1 && !p.join_here;
+  if (joined && !launch_takes((uint64_t)n * q_heads / join_rows(d->head_dim) + 1, 256)) return WAL_ERR_SHAPE;
   a.split = p.split;
   a.n_splits = p.n_splits;
   uint8_t* ws_bytes_dev = static_cast<uint8_t*>(ws_dev);
@@ -186,7 +187,7 @@ extern "C" int wal_attn_paged(const wal_kv_desc* d, const void* cache_dev, const
   a.ones_done = p.stream;
   st = p.stream ? attn_stream(a, int8, d->head_dim, max_new * a.group <= 16 ? 1 : 2, stream)
                 : attn_tile(a, int8 ? kPagedInt8 : kPagedBf16, d->head_dim, stream);
-  return st || p.n_splits == 1 || p.join_here ? st : attn_join(a, d->head_dim, stream);
+  return st || !joined ? st : attn_join(a, d->head_dim, stream);
 }
 
 extern "C" int wal_attn_prompt(const void* q_dev, uint32_t ldq, const void* k_dev, uint32_t ldk, const void* v_dev,

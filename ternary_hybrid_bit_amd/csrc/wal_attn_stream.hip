@@ -475,7 +475,7 @@ __global__ __launch_bounds__(256) void k_attn_join(Attn a) {
 // Few rows up to twice the compute units' number.
 template <int D>
 void join(const Attn& a, hipStream_t s) {
-  constexpr int kMany = 1024 / D;
+  constexpr int kMany = (int)join_rows(D);
   const uint64_t n = (uint64_t)a.n * a.q_heads;
   if (n <= 512) hipLaunchKernelGGL((k_attn_join<D, 1>), dim3((uint32_t)n), dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_attn_join<D, kMany>), dim3((uint32_t)((n + kMany - 1) / kMany)), dim3(256), 0, s, a);
@@ -499,7 +499,7 @@ namespace wal {
 
 int attn_stream(const Attn& a, bool int8, uint32_t dim, uint32_t tiles, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if ((uint64_t)a.n_splits * a.kv_heads * a.n_seqs > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
+  if (!launch_takes((uint64_t)a.n_splits * a.kv_heads * a.n_seqs, 256)) return WAL_ERR_SHAPE;   // (512 threads: at most 256 of them)
   if (int8) {
     if (dim == 64) launch<kPagedInt8, 64>(a, tiles, s);
     if (dim == 128) launch<kPagedInt8, 128>(a, tiles, s);

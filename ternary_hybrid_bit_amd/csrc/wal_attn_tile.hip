@@ -689,7 +689,7 @@ template <int KIND, int D>
 int launch(const Attn& a, hipStream_t s) {
   const uint32_t rows = attn_tile_rows(a.n_seqs, a.n, a.max_new, a.group, a.kv_heads, D);
   const uint64_t blocks = attn_tiles(a.n_seqs, a.n, a.max_new, a.group, a.kv_heads, D) * a.kv_heads * a.n_splits;
-  if (blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
+  if (!launch_takes(blocks, rows == 256 ? 512 : 256)) return WAL_ERR_SHAPE;
   if constexpr (D <= 128) {
     if (rows == 256) {
       hipLaunchKernelGGL((k_attn_pair<KIND, D>), dim3((uint32_t)blocks), dim3(512), 0, s, a);
