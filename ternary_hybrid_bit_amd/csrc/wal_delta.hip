@@ -8,11 +8,20 @@ namespace {
 
 constexpr uint32_t kMaxRows = 1u << 24;   // rows and sequences of a call
 constexpr uint32_t kMaxPitch = 1u << 24;  // elements from a row to the next: 64 rows in 32 bits of bytes
-// Tokens of a sequence up to which a call goes token by token.  On chunks the time is the same up to 64 tokens and grows
-// with sequences times heads, token by token it grows with the tokens and little with the others before memory is busy (calls
-// from Python, tokens against chunks; one sequence, 48 heads of 128: 8 tokens 17 and 19 us, 12 tokens 23 and 19; 13 sequences,
-// 32 heads: 24 tokens 49 and 55 us, 32 tokens 64 and 55; 64 sequences, 48 heads: 24 tokens 202 and 296 us).
-constexpr uint32_t kFewRows = 8, kFewRowsOfMany = 24, kMany = 256;
+// Tokens of a sequence up to which a call goes token by token, by its slices of states.  On chunks the time is the same up to
+// 64 tokens and grows with the slices, token by token it grows with the tokens and little with the others before memory
+// is busy.  Where the two meet (sequences of equal lengths in a graph, heads of 128 x 128 unless said; token by token and on
+// chunks, us): 192 slices, 8 tokens 18.6 and 20.2, 10 tokens 21.6 and 20.2; 256 slices of heads of 64 x 32, 10 tokens 21.1 and 21.8; 384,
+// 10 tokens 24.5 and 27.3, 12 tokens 27.9 and 27.4; 512 of 64 x 64, 12 tokens 26.4 and 27.8, 16 tokens 33.4 and 27.8; 768, 10 tokens 32.9
+// and 36.4, 12 tokens 37.6 and 36.5; 1024, 16 tokens 41.8 and 41.7; 1280 of 64 x 64, 16 tokens 42.8 and 48.2, 24 tokens 60.4 and 48.3;
+// 12288, 16 tokens 289 and 361, 24 tokens 412 and 367.
+constexpr uint32_t few_rows(uint64_t slices) { return slices < 384 ? 8 : slices < 1024 ? 12 : 16; }
+// The same for the sequences of a call that brings a prompt with them, each in its own form then, one after the other; 0: all
+// on chunks (a prompt of 300 among others, us in both forms and on chunks: 512 slices, 7 of 4 tokens 41.9 and 36.0; 768, 3 of 4 tokens
+// 49.8 and 47.9, of one 43.5 and 48.7; 1024, 15 of 4 tokens 46.8 and 49.3, of 12 62.4 and 49.3; 1536, 7 of 8 tokens 62.9 and
+// 65.5; 2048, 31 of 4 tokens 55.4 and 76.3, of 12 78.8 and 76.6; 12288, 63 of 16 tokens and a prompt of 500 353 and 385, of one
+// 151 and 369; 3072, 15 of one token and a prompt of 1000 86 and 132).
+constexpr uint32_t few_beside_prompt(uint64_t slices) { return slices < 1024 ? 0 : slices < 4096 ? 8 : 16; }
 constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: what the last cache holds
 
 // How a call is cut.
@@ -26,13 +35,14 @@ struct Plan {
 
 Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new) {
   Plan p{};
-  p.few = (uint64_t)n_seqs * d->value_heads >= kMany ? kFewRowsOfMany : kFewRows;
+  const uint64_t slices = (uint64_t)n_seqs * d->value_heads * (d->value_dim / kSlice);
+  p.few = few_rows(slices);
   p.chunks = n && n_seqs && max_new > p.few;
-  // Both, if all but one sequence bring few rows on average: a prompt among sequences that bring a token each (48 heads of 128, 63
-  // of one token and one of 500 124 us, all on chunks 302; 15 and one of 1000 75 and 110; 5 of 300 tokens in a call whose
-  // max_new does not tell, 16 heads, 42.5 and 41).
-  p.step = !p.chunks || (n_seqs > 1 && n <= max_new + (n_seqs - 1ull) * p.few);
-  if (!p.chunks) return p;
+  p.step = !p.chunks;
+  if (p.step) return p;
+  // Both, if all but one sequence can bring that few rows on average (the host knows the sum and the largest).
+  p.few = few_beside_prompt(slices);
+  p.step = n_seqs > 1 && p.few && n <= max_new + (n_seqs - 1ull) * p.few;
   if (!p.step) p.few = 0;
   const uint64_t place = place_bytes(d->key_heads, d->value_heads, d->key_dim), most = kMaxItems / place;
   p.all = n / kChunk + n_seqs;

@@ -23,7 +23,7 @@ def wal():
 @pytest.mark.parametrize("new,max_new,kw", [
     ([3, 5], 2, {}), ([5, 0, 9], 4, dict(dk=128, dv=64)), ([130, 70], 60, {}), ([130, 70], 64, dict(dk=128)), ([200, 65, 3], 65, dict(raw=False)),
     ([300, 10], 129, dict(dk=128, dv=96)), ([1, 2, 90, 1], 70, {}), ([1, 30, 100, 1, 1], 20, dict(dk=128, dv=64)), ([500] + [1] * 40, 100, {}),
-    ([24] * 40, 9, dict(kh=4, group=2)),
+    ([24] * 40, 9, dict(kh=4, group=2)), ([40] + [9, 1, 0] * 16, 30, dict(kh=8, group=2, dv=64)), ([300] + [1, 3] * 70, 200, dict(kh=8, group=2, dv=64)),
 ])
 def test_rows_past_max_new_are_kept_nowhere(wal, new, max_new, kw):
     c = Case(wal, new, seed=max_new, max_new=max_new, **kw)
@@ -46,6 +46,20 @@ def test_rows_past_max_new_are_kept_nowhere(wal, new, max_new, kw):
             assert np.linalg.norm(gap) <= 1e-6 * np.linalg.norm(want[c.slots[s]]), s
     others = [i for i in range(c.places) if i not in c.slots or not new[list(c.slots).index(i)]]
     assert torch.equal(state[others], c.state0[others])
+
+
+@pytest.mark.parametrize("new,kw", [
+    ([1, 1, 300, 1, 8, 0, 1] + [1] * 20, dict(dk=128, dv=64, kh=8, group=3)), ([200] + [1] * 40, dict(dk=128, kh=16, group=2)),
+    ([8, 9, 1] * 9 + [70], dict(kh=8, group=4, dv=96)), ([1, 130] + [2, 0] * 20, dict(keep=False, kh=16, group=1, dv=64)),
+    ([1] * 130 + [24, 16, 17, 100], dict(kh=8, group=4)), ([1] * 33 + [70, 2], dict(before=6, behind=5, kh=4, group=4, dv=64)),
+    ([1, 1, 80] + [3] * 30, dict(slots=[40, 1, 0] + list(range(2, 32)), places=33, kh=8, group=2, dv=64)),
+    ([30] + [0] * 40 + [20], dict(kh=8, group=4)),
+])
+def test_prompts_among_single_tokens_of_many_heads(wal, new, kw):
+    """From 1024 slices of states on each sequence of such a call goes in its own form."""
+    c = Case(wal, new, seed=len(new) + 190, **kw)
+    assert len(new) * c.h * (c.dv // 32) >= 1024 and c.n - c.before <= max(new) + (len(new) - 1) * 16
+    c.check()
 
 
 def test_both_forms_and_several_launches(wal):
