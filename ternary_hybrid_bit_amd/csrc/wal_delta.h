@@ -42,7 +42,7 @@ struct Delta {
   uint8_t* ws;                   // of value heads
   uint8_t* key_ws;               // of key heads
   float* carry[2];
-  uint32_t place0, places, pitch, key_item;   // places from a head to the next
+  uint32_t place0, places, key_item;
   uint32_t seqs, together;       // sequences that a launch of the scan looks at, heads that it puts on one chiplet
 };
 

@@ -29,7 +29,6 @@ struct Plan {
   bool step, chunks;         // token by token, on chunks, or each sequence in one of both
   uint32_t few;              // rows of a sequence up to which it goes token by token
   uint32_t all, places;      // places of chunks, and those of one launch
-  uint32_t pitch;            // places from a head to the next: odd, since heads in step would else meet on few memory channels
   uint64_t carry, bytes;     // bytes of a carried state; of the workspace
 };
 
@@ -44,12 +43,11 @@ Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_
   p.few = few_beside_prompt(slices);
   p.step = n_seqs > 1 && p.few && n <= max_new + (n_seqs - 1ull) * p.few;
   if (!p.step) p.few = 0;
-  const uint64_t place = place_bytes(d->key_heads, d->value_heads, d->key_dim), most = kMaxItems / place;
+  const uint64_t place = place_bytes(d->key_heads, d->value_heads, d->key_dim), most = kMaxItems / place;   // (four at least)
   p.all = n / kChunk + n_seqs;
-  p.places = p.all <= most ? p.all : most ? (uint32_t)most : 1;
+  p.places = p.all <= most ? p.all : (uint32_t)most;
   p.carry = p.places < p.all ? 4ull * d->value_heads * d->key_dim * d->value_dim : 0;
-  p.pitch = p.places | 1;
-  p.bytes = p.pitch * place + 2 * p.carry;
+  p.bytes = p.places * place + 2 * p.carry;
   return p;
 }
 
@@ -138,11 +136,10 @@ extern "C" int wal_delta(const wal_delta_desc* d, const void* q_dev, uint32_t ld
   if (p.step && (st = delta_step(a, d->key_dim, stream))) return st;
   if (!p.chunks) return WAL_OK;
   a.ws = static_cast<uint8_t*>(ws_dev);
-  a.key_ws = a.ws + (uint64_t)p.pitch * d->value_heads * kItemBytes;
+  a.key_ws = a.ws + (uint64_t)p.places * d->value_heads * kItemBytes;
   a.key_item = key_item_bytes(d->key_dim);
   a.places = p.places;
-  a.pitch = p.pitch;
-  a.carry[0] = reinterpret_cast<float*>(a.ws + p.pitch * place_bytes(d->key_heads, d->value_heads, d->key_dim));
+  a.carry[0] = reinterpret_cast<float*>(a.ws + p.places * place_bytes(d->key_heads, d->value_heads, d->key_dim));
   a.carry[1] = a.carry[0] + p.carry / 4;
   return delta_chunks(a, d->key_dim, p.all, stream);
 }

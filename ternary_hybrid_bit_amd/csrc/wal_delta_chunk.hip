@@ -116,10 +116,10 @@ __device__ __forceinline__ uint32_t seq_of_place(const Delta& a, uint32_t place,
 // What a launch's place holds of a value head and of a key head: a head's places side by side, since they are read one
 // after another.
 __device__ __forceinline__ uint8_t* item_of(const Delta& a, uint32_t local, uint32_t head) {
-  return a.ws + ((uint64_t)head * a.pitch + local) * kItemBytes;
+  return a.ws + ((uint64_t)head * a.places + local) * kItemBytes;
 }
 __device__ __forceinline__ uint8_t* key_item_of(const Delta& a, uint32_t local, uint32_t kh) {
-  return a.key_ws + ((uint64_t)kh * a.pitch + local) * a.key_item;
+  return a.key_ws + ((uint64_t)kh * a.places + local) * a.key_item;
 }
 
 // Place of a row's 16-byte piece in LDS: 16 neighbours that are read together, the rows of dealt(), and in the transposing
@@ -755,13 +755,14 @@ int launch(Delta& a, uint32_t all, hipStream_t s) {
     a.carry[1] = carry[(i + 1) % 2];
     const uint64_t items = (uint64_t)(all - first < a.places ? all - first : a.places) * (a.heads / a.group) * ((a.group + kPair - 1) / kPair);
     a.seqs = a.n_seqs < a.places ? a.n_seqs : a.places;   // a sequence has a place at least
-    // heads of a key head together where no chiplet's 32 compute units get more workgroups than otherwise, or all at once (5
-    // sequences of 300 tokens, 16 heads of 128 on 8 38.7 us, each head by itself 44.6; one of 4096 tokens, 32 heads 130 and
-    // 131; one of 8192 tokens, 48 heads 321 and 317)
+    // heads of a key head together where no chiplet's 32 compute units get more workgroups than otherwise, or all at once (us
+    // in a graph, together and each head by itself: 5 sequences of 300 tokens, 16 heads of 128 on 8 45.5 and 49.9; 9 up to 1111, 8
+    // heads on 4 52.7 and 54.9; one of 8192, 48 heads on 16 363 and 365; nine key heads, each chiplet by turns: one of 2048, 54 heads
+    // 161 and 104, one of 1024, 108 heads of 64 x 128 113 and 86)
     const uint64_t units = (uint64_t)a.seqs * (a.heads / a.group), each = (units + 7) / 8 * a.group * a.slices;
     a.together = units % 8 == 0 || each <= 32 ? a.group : 1;
     const uint64_t blocks = a.together > 1 ? each * 8 : ((uint64_t)a.seqs * a.heads + 7) / 8 * 8 * a.slices;
-    if (items > 0x7FFFFFFFull || blocks > 0x7FFFFFFFull) return WAL_ERR_SHAPE;
+    // (at most 256 MB of places, 32 KB a head: both are far below what a launch takes)
     hipLaunchKernelGGL((k_delta_chunk<DK>), dim3((uint32_t)items), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_delta_scan<DK>), dim3((uint32_t)blocks), dim3(256 * kScanGroups), 0, s, a);
   }
