@@ -36,6 +36,7 @@
 #include <hip/hip_runtime.h>
 
 #include "wal_delta.h"
+#include "wal_find.h"
 
 namespace {
 
@@ -102,15 +103,7 @@ __device__ __forceinline__ float power(float2 x, float2 y) { return __builtin_am
 
 // The sequence of a chunk's place: sequence s has those from starts[s] / 64 + s on.
 __device__ __forceinline__ uint32_t seq_of_place(const Delta& a, uint32_t place, uint32_t lane) {
-  uint32_t lo = 0, span = a.n_seqs;
-  while (span > 1) {
-    const uint32_t step = (span + 63) / 64, i = lane * step;
-    const bool before = i < span && (uint32_t)between(a.starts[lo + i], 0, (int32_t)a.n) / kC + lo + i <= place;
-    const uint32_t k = (uint32_t)max(__builtin_popcountll(__ballot(before)), 1) - 1;
-    lo += k * step;
-    span = min(step, span - k * step);
-  }
-  return (uint32_t)__builtin_amdgcn_readfirstlane((int)lo);
+  return last_begun(a.n_seqs, lane, [&](uint32_t s) { return (uint32_t)between(a.starts[s], 0, (int32_t)a.n) / kC + s <= place; });
 }
 
 // What a launch's place holds of a value head and of a key head: a head's places side by side, since they are read one
