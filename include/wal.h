@@ -778,7 +778,8 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  *            contents arbitrary.  Calls that may overlap in time need their own
  * States, norms, gates and sums are fp32; sequences that bring many rows are taken in chunks
  * of 64 tokens, where products take values in 24 bits for the state and 16 for the outputs, each
- * value for itself: a large one takes nothing from those beside it.
+ * value for itself: a large one takes nothing from those beside it (below about 1e-30 values have
+ * fewer bits there, since parts below fp32's normal range count as 0).
  * beta |k|^2 (of k as used) is meant to be from 0 to 2, where no token enlarges a state: past that
  * states grow from token to token, and where calls work on chunks they are less exact, and a
  * column that grows past fp32's range is not finite from its chunk's first token on.  From a token on whose q, k, v, alpha or beta holds an infinity

@@ -87,3 +87,21 @@ def test_delta_rule_of_more_sequences_than_a_launch_takes(wal):
     wal.wal_delta(desc, q, k, v, a, b, starts.cuda(), out, max_new=1)
     torch.cuda.synchronize()
     assert (want != -7).all() and torch.equal(out, want)
+
+
+def test_delta_rule_of_rows_far_apart(wal):
+    """The largest pitch, 2^24 elements, on chunks (2.3 GB each for v and the outputs)."""
+    n, h, dk, dv, far = 70, 2, 64, 64, 1 << 24
+    desc = wal.make_delta_desc(h, h, dk, dv)
+    g = torch.Generator("cuda").manual_seed(6)
+    q, k, v = (torch.randn((n, h * d), device="cuda", generator=g).to(torch.bfloat16) for d in (dk, dk, dv))
+    a, b = -torch.rand((n, h), device="cuda", generator=g), torch.rand((n, h), device="cuda", generator=g)
+    starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    ws = torch.empty(wal.wal_delta_workspace_size(desc, 1, n, n), dtype=torch.uint8, device="cuda")
+    want = torch.empty((n, h * dv), dtype=torch.bfloat16, device="cuda")
+    wal.wal_delta(desc, q, k, v, a, b, starts, want, ws=ws)
+    wide, out = (torch.empty((n, far), dtype=torch.bfloat16, device="cuda")[:, 8:8 + h * dv] for _ in range(2))
+    wide.copy_(v)
+    wal.wal_delta(desc, q, k, wide, a, b, starts, out, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.isfinite(want).all()
