@@ -775,7 +775,8 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  *   state_dev [n_slots][value_heads][key_dim][value_dim] fp32, 16-byte aligned
  *   max_new  bounds the sequences' rows: rows past it are neither computed nor kept
  *   ws       wal_delta_workspace_size bytes, 256-byte aligned (NULL when that is 0),
- *            contents arbitrary.  Calls that may overlap in time need their own
+ *            contents arbitrary.  Calls that may overlap in time need their own.  The size is that
+ *            of a call: one of fewer sequences can need more
  * States, norms, gates and sums are fp32; sequences that bring many rows are taken in chunks
  * of 64 tokens, where products take values in 24 bits for the state and 16 for the outputs, each
  * value for itself: a large one takes nothing from those beside it (below about 1e-30 values have

@@ -226,10 +226,11 @@ extern "C" int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t cha
   // Rows of a tile.  As many sequences as rows, or half as many where there is little work: one each, since a tile walks its
   // sequences one after another, and there is little above a row to read again (fp32, tiles of one row and those below:
   // 64 of one token, 10240 channels 8.2 and 15.2 us, 1000 of them 77 and 79; 63 of one token and one of 64, 10240 channels 10.5 and
-  // 16.6; 999 of one and one of 1000, 1024 channels 14 and 18.5, 8192 channels 95 and 79; 255 of one and one of 256, 8192 channels
-  // 23 and 22; 2000 of two, 1024 channels 25 and 17.5; one of 1000 and 999 without rows, 8192 channels 36 and 15, which the host cannot tell from 1000 of one, 64 and 70).  Else long tiles read little above them twice and short ones fill the GPU (fp32, 8192 channels, tiles of 4, 8 and
-  // 16: 1000 rows 13.9, 14.6 and 16.6 us, 4000 rows 51, 46 and 51, 16000 rows 189, 156 and 160; bf16: 1000 rows 14, 14 and
-  // 15, 4000 rows 51, 42 and 41, 8000 rows 98, 75 and 68, with tiles of 32 73).
+  // 16.6; 999 of one and one of 1000, 1024 channels 14 and 18.5, 8192 channels 95 and 79; 255 of one and one of 256, 8192
+  // channels 23 and 22; 2000 of two, 1024 channels 25 and 17.5; one of 1000 and 999 without rows, 8192 channels 36 and 15, which
+  // the host cannot tell from 1000 of one, 64 and 70).  Else long tiles read little above them twice and short ones fill the
+  // GPU (fp32, 8192 channels, tiles of 4, 8 and 16: 1000 rows 13.9, 14.6 and 16.6 us, 4000 rows 51, 46 and 51, 16000 rows 189,
+  // 156 and 160; bf16: 1000 rows 14, 14 and 15, 4000 rows 51, 42 and 41, 8000 rows 98, 75 and 68, with tiles of 32 73).
   const bool bf16 = x_dtype == WAL_X_BF16;
   const uint64_t work = (uint64_t)n * groups;
   a.tile = n <= n_seqs || (n <= 2ull * n_seqs && work < (1ull << 19)) ? 1 : work < (8ull << 18) ? 4 : bf16 && work >= (32ull << 18) ? 16 : 8;

@@ -15,8 +15,8 @@
 // state, T, the rows b V - .., u) as three, 24 bits, and what only outputs in bf16 see (P, u and the state there) as two, 16
 // bits; K and Q hold bf16 to begin with.  So a value keeps its bits whatever lies beside it: a row a billion times its
 // neighbours takes nothing from the rows before it, nor from those behind a token that forgets it.  Two parts in half precision
-// hold 22 bits and lose them as soon as rows of a column that share a scale differ by 2^9 (that scan took 271 us for 311 at
-// 8192 tokens of 48 heads); outputs of one part in half precision were off by up to 3.2e-3 where keys are alike and stored rows
+// hold 22 bits and lose them as soon as rows of a column that share a scale differ by 2^9 (that way 8192 tokens of 48 heads took
+// 320 us for 364, of 32 heads 271 for 322); outputs of one part in half precision were off by up to 3.2e-3 where keys are alike and stored rows
 // cancel, for the 1.66e-3 of their rounding to bf16.  Rows of K and Q are brought to
 // lengths of 1 to 2 by powers of two.  Keys and queries are taken as unit vectors and lengths, the lengths into the
 // factors of the rows.  G is added up in 64 bits, because e^(G_i - G_j) has to be exact also after a token that
@@ -27,12 +27,12 @@
 // factors are NaN; k_delta_scan looks at one row of u of each 32, and where it is not
 // finite takes the rows that are not out of the product and puts NaN where they belong.
 //
-// What bounds it.  k_delta_chunk: instructions and latencies (dropping all its stores of T took 3 us of 77).  k_delta_scan: the
-// chain of a chunk, K S, the sum of its halves, T, K^T u, about 4800 cycles of which the matrix cores take 1350;
-// what else there is are the parts' roundings and latencies, of LDS too.  With 192 workgroups of 16 + 16 columns the clock
-// falls besides.
-// Measured: 8192 tokens, 48 heads of 128 on 16 365 us, 86 of them k_delta_chunk; 32 heads 324; 4096 tokens, 32 heads 169;
-// 9 sequences up to 1111, 8 heads of 64 x 96 on 4, 49 with the call from Python.
+// What bounds it.  k_delta_chunk: instructions and latencies (its stores hide behind them).  k_delta_scan: the
+// chain of a chunk, K S, the sum of its halves, T, K^T u: 5200 cycles of which a SIMD's matrix cores are busy 1800 (1340 with
+// the states, the rest with outputs); what else there is are the parts' roundings and latencies, of LDS too.  With
+// 192 workgroups of 16 + 16 columns the clock falls besides (2.1 GHz).
+// Measured (graph): 8192 tokens, 48 heads of 128 on 16 364 us, about 82 of them k_delta_chunk; 32 heads 322; 4096 tokens, 32 heads
+// 168; 9 sequences up to 1111, 8 heads of 64 x 96 on 4, 53 (49 call by call, where a call's inputs are warmer).
 #include <hip/hip_runtime.h>
 
 #include "wal_delta.h"

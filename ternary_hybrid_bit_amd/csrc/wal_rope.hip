@@ -25,7 +25,7 @@
 //
 // Measured in graphs: 16001 tokens of 40 heads of 128 rotated bf16 to bf16 64 us (5.1 TB/s; a copy
 // reaches 5.0), 8191 tokens written as int8 with their q rows 54 us (with the norms 55), 100003 tokens
-// read back from int8 123 us; one token of 32 heads 3.1 us.  Normed: 8192 tokens of 48 heads of 128 with an fp32 gate
+// read back from int8 123 us; one token of 32 heads 3.1 to 3.4 us from launch to launch, 2.4 of them the kernel.  Normed: 8192 tokens of 48 heads of 128 with an fp32 gate
 // 80 us, 8001 tokens of 20 heads of 256 rotated, fp32 to bf16, 50 us (4.9 TB/s); one token with a gate 3.7 us.
 #include <hip/hip_runtime.h>
 
