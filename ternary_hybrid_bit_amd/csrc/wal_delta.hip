@@ -20,7 +20,7 @@ constexpr uint32_t few_rows(uint64_t slices) { return slices < 384 ? 8 : slices 
 // on chunks (a prompt of 300 among others, us in both forms and on chunks: 512 slices, 7 of 4 tokens 41.9 and 36.0; 768, 3 of 4 tokens
 // 49.8 and 47.9, of one 43.5 and 48.7; 1024, 15 of 4 tokens 46.8 and 49.3, of 12 62.4 and 49.3; 1536, 7 of 8 tokens 62.9 and
 // 65.5; 2048, 31 of 4 tokens 55.4 and 76.3, of 12 78.8 and 76.6; 12288, 63 of 16 tokens and a prompt of 500 353 and 385, of one
-// 151 and 369; 3072, 15 of one token and a prompt of 1000 86 and 132).
+// 151 and 369).
 constexpr uint32_t few_beside_prompt(uint64_t slices) { return slices < 1024 ? 0 : slices < 4096 ? 8 : 16; }
 constexpr uint64_t kMaxItems = 256ull << 20;   // bytes of a launch's chunks: what the last cache holds
 
