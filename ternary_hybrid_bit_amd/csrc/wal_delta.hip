@@ -8,14 +8,19 @@ namespace {
 
 constexpr uint32_t kMaxRows = 1u << 24;   // rows and sequences of a call
 constexpr uint32_t kMaxPitch = 1u << 24;  // elements from a row to the next: 64 rows in 32 bits of bytes
-// Tokens of a sequence up to which a call goes token by token, by its slices of states.  On chunks the time is the same up to
+// Tokens of a sequence up to which a call goes token by token, by its slices of states and tokens in all.  On chunks the time is the same up to
 // 64 tokens and grows with the slices, token by token it grows with the tokens and little with the others before memory
 // is busy.  Where the two meet (sequences of equal lengths in a graph, heads of 128 x 128 unless said; token by token and on
 // chunks, us): 192 slices, 8 tokens 18.6 and 20.2, 10 tokens 21.6 and 20.2; 256 slices of heads of 64 x 32, 10 tokens 21.1 and 21.8; 384,
 // 10 tokens 24.5 and 27.3, 12 tokens 27.9 and 27.4; 512 of 64 x 64, 12 tokens 26.4 and 27.8, 16 tokens 33.4 and 27.8; 768, 10 tokens 32.9
 // and 36.4, 12 tokens 37.6 and 36.5; 1024, 16 tokens 41.8 and 41.7; 1280 of 64 x 64, 16 tokens 42.8 and 48.2, 24 tokens 60.4 and 48.3;
-// 12288, 16 tokens 289 and 361, 24 tokens 412 and 367.
-constexpr uint32_t few_rows(uint64_t slices) { return slices < 384 ? 8 : slices < 1024 ? 12 : 16; }
+// 12288, 16 tokens 289 and 361, 24 tokens 412 and 367.  Uneven lengths, on average 0.4 of the largest: from 4096 slices on the sum
+// of the tokens is what counts (6144, up to 24 tokens 131 and 178, 32 tokens 165 and 179, 48 tokens 235 and 181; 12288, 32 tokens 274 and
+// 359, 48 tokens 388 and 365), below it is not quite (1280 of 64 x 64, 20 tokens 47.6 and 48.1; 1664, 24 tokens 53.5 and 59.8,
+// 32 tokens 67.5 and 59.7).
+constexpr uint32_t few_rows(uint64_t slices, uint32_t n_seqs, uint32_t n) {
+  return slices < 384 ? 8 : slices < 1024 ? 12 : slices >= 4096 && n <= 16ull * n_seqs ? 32 : 16;
+}
 // The same for the sequences of a call that brings a prompt with them, each in its own form then, one after the other; 0: all
 // on chunks (a prompt of 300 among others, us in both forms and on chunks: 512 slices, 7 of 4 tokens 41.9 and 36.0; 768, 3 of 4 tokens
 // 49.8 and 47.9, of one 43.5 and 48.7; 1024, 15 of 4 tokens 46.8 and 49.3, of 12 62.4 and 49.3; 1536, 7 of 8 tokens 62.9 and
@@ -35,7 +40,7 @@ struct Plan {
 Plan plan_of(const wal_delta_desc* d, uint32_t n_seqs, uint32_t n, uint32_t max_new) {
   Plan p{};
   const uint64_t slices = (uint64_t)n_seqs * d->value_heads * (d->value_dim / kSlice);
-  p.few = few_rows(slices);
+  p.few = few_rows(slices, n_seqs, n);
   p.chunks = n && n_seqs && max_new > p.few;
   p.step = !p.chunks;
   if (p.step) return p;

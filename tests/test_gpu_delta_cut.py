@@ -53,7 +53,7 @@ def test_rows_past_max_new_are_kept_nowhere(wal, new, max_new, kw):
     ([8, 9, 1] * 9 + [70], dict(kh=8, group=4, dv=96)), ([1, 130] + [2, 0] * 20, dict(keep=False, kh=16, group=1, dv=64)),
     ([1] * 130 + [24, 16, 17, 100], dict(kh=8, group=4)), ([1] * 33 + [70, 2], dict(before=6, behind=5, kh=4, group=4, dv=64)),
     ([1, 1, 80] + [3] * 30, dict(slots=[40, 1, 0] + list(range(2, 32)), places=33, kh=8, group=2, dv=64)),
-    ([30] + [0] * 40 + [20], dict(kh=8, group=4)),
+    ([30] + [0] * 40 + [20], dict(kh=8, group=4)), ([32, 1, 5, 17] + [2, 25, 16] * 5, dict(kh=16, group=4, dv=128)),   # (the last all token by token)
 ])
 def test_prompts_among_single_tokens_of_many_heads(wal, new, kw):
     """From 1024 slices of states on each sequence of such a call goes in its own form."""
