@@ -783,8 +783,9 @@ int wal_conv(const void* x_dev, int x_dtype, uint32_t n, uint32_t channels, uint
  * fewer bits there, since parts below fp32's normal range count as 0).
  * beta |k|^2 (of k as used) is meant to be from 0 to 2, where no token enlarges a state: past that
  * states grow from token to token, and where calls work on chunks they are less exact, and a
- * column that grows past fp32's range is not finite from its chunk's first token on.  From a token on whose q, k, v, alpha or beta holds an infinity
- * or NaN, what depends on it is an infinity or NaN.  The result does not depend on timing.
+ * column that grows past fp32's range is not finite from its chunk's first token on.  From a token
+ * on whose q, k, v, alpha or beta holds an infinity or NaN, what depends on it is an infinity or
+ * NaN.  The result does not depend on timing.
  * Errors: ARG, SHAPE, ALIGN, BUFFER, DEVICE. */
 typedef struct {
   uint32_t key_heads, value_heads;  /* value_heads a multiple of key_heads, at most 1024    */
